@@ -276,6 +276,107 @@ bkv_status bkv_score_select_noalloc(const bkv_config* cfg, const void* bq, const
                                     int32_t cache_len, int64_t step, int32_t* kept,
                                     uint32_t* status, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * The model's side of the caches: the calls that fill and read the K/V tensors
+ * bkv_evict compacts. A serving step stores the new tokens' keys and values
+ * (bkv_store_kv), attends over the cache (bkv_attend_prompt for prompts and
+ * prompt chunks, bkv_attend_tree for decode steps and trees of drafted
+ * tokens), and after a draft is verified keeps the accepted path
+ * (bkv_commit_tree); bkv_prefill / bkv_append_queries / bkv_evict then see the
+ * same caches and pre-RoPE queries.
+ *
+ * Shared by the four calls
+ *   - No handle, no workspace, no device allocation, nothing kept between
+ *     calls: calls on different streams may overlap, and calls may be captured
+ *     into CUDA graphs (lengths, masks and positions are read on the device at
+ *     replay).
+ *   - cfg as bkv_create (heads, kv_heads, d, batch, layers, max_cache and
+ *     rope_theta are used; the eviction fields must be valid);
+ *     BKV_ERR_UNSUPPORTED if heads / kv_heads > 128.
+ *   - K, V: device bf16 [batch][kv_heads][max_cache][d] of ONE layer (an array
+ *     of `layers` pointers for bkv_commit_tree).
+ *   - Packed tokens: sequence b of the batch owns tokens cu_seqlens[b] to
+ *     cu_seqlens[b + 1] (device int32 [batch + 1], non-decreasing, within
+ *     [0, total]; a sequence may have none). Tokens in front of the first or
+ *     behind the last sequence are left as they are.
+ *   - Strides: a packed tensor's tokens lie `stride` elements apart (a multiple
+ *     of 8, at least its heads * d); heads and elements are contiguous. So the
+ *     parts of a fused projection's output need no copy.
+ *   - status: optional device uint32 (4-byte aligned, caller-owned). The call
+ *     sets it to 0, then the kernels latch the first error seen on the device:
+ *     BKV_ERR_INVALID_ARG (a length, offset, slot or path out of range: it is
+ *     clamped or its rows are skipped, and nothing outside the tensors is
+ *     touched), BKV_ERR_NONFINITE (attention: a row's output or log-sum-exp is
+ *     not finite), BKV_ERR_TIMEOUT (a bounded wait ran out; the outputs must
+ *     not be used). NULL: such errors go unreported.
+ *   - Tensors live on the current device, cuda_stream belongs to it, and
+ *     outputs do not overlap inputs unless a call says so.
+ *   - Host checks return BKV_ERR_INVALID_ARG / BKV_ERR_UNSUPPORTED /
+ *     BKV_ERR_CUDA and enqueue nothing. */
+
+/* Rotates queries and keys to their positions and writes keys and values to
+ * their slots. Token i of sequence b takes slot first_slot[b] + i; its
+ * position is first_pos[b] + i, or first_pos[b] + depth[t] when depth is given
+ * (a draft tree's nodes: the depth of packed token t in the tree). Rotate-half
+ * pairs as everywhere here; any int32 position, also negative.
+ *   q_pre: device bf16, packed [total][heads][d]; k_pre, v: [total][kv_heads][d].
+ *   first_slot, first_pos: device int32 [batch]; depth: device int32 [total] or NULL.
+ *   q_rot: device bf16 [total][heads][d], contiguous; may be q_pre itself when
+ *          q_stride = heads * d.
+ * A token whose slot is outside [0, max_cache) gets its q_rot but no cache
+ * rows (BKV_ERR_INVALID_ARG in status). */
+bkv_status bkv_store_kv(const bkv_config* cfg, const void* q_pre, int64_t q_stride, const void* k_pre,
+                        int64_t k_stride, const void* v, int64_t v_stride, int32_t total,
+                        const int32_t* cu_seqlens, const int32_t* first_slot, const int32_t* first_pos,
+                        const int32_t* depth, void* q_rot, void* K, void* V, uint32_t* status,
+                        void* cuda_stream);
+
+/* Causal attention of packed prompts (or chunks of them) over the caches:
+ * token i of sequence b sees slots [0, first_slot[b] + i]; scale 1/sqrt(d),
+ * query head h reads KV head h / (heads / kv_heads).
+ *   q:   device bf16, packed [total][heads][d], rotated (bkv_store_kv's q_rot).
+ *   out: device bf16 [total][heads][d], contiguous.
+ *   lse: optional device fp32 [total][heads]: ln of the row's sum of
+ *        exponentials.
+ * Slots behind a sequence's last token may hold anything, NaN included. A
+ * non-finite value in a visible slot makes rows of its own sequence and KV
+ * head non-finite, also such as cannot see that slot. */
+bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K,
+                             const void* V, const int32_t* cu_seqlens, const int32_t* first_slot,
+                             int32_t total, void* out, float* lse, uint32_t* status, void* cuda_stream);
+
+/* Attention of a tree of n drafted tokens per sequence over its cache: the
+ * nodes' keys and values sit in slots cache_lens[b] + i. Node i sees the
+ * committed slots [0, cache_lens[b]) and the nodes j whose bit j is set in
+ * mask[b][i] (its ancestors and itself). n = 1 is a plain decode step.
+ *   q:          device bf16, [batch][n][heads][d] with q_stride between nodes.
+ *   cache_lens: device int32 [batch], the slots before the tree.
+ *   n:          1 .. 64 (BKV_ERR_UNSUPPORTED beyond).
+ *   mask:       device int64 [batch][n], bits at and above the sequence's node
+ *               count are ignored; NULL: a chain, node i sees nodes 0 .. i.
+ *   nodes:      optional device int32 [batch], nodes in use, 0 .. n; rows of
+ *               the others are left as they are. NULL: n everywhere.
+ *   out:        device bf16 [batch][n][heads][d]; lse: optional fp32
+ *               [batch][n][heads].
+ * A node that sees no slot at all gets zeros and a log-sum-exp of -inf. Slots
+ * behind the last node may hold anything; a non-finite value in a node's or a
+ * committed slot spreads as in bkv_attend_prompt. */
+bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K, const void* V,
+                           const int32_t* cache_lens, int32_t n, const int64_t* mask, const int32_t* nodes,
+                           void* out, float* lse, uint32_t* status, void* cuda_stream);
+
+/* Keeps an accepted path of a tree: slot cache_lens[b] + i takes the key and
+ * value that slot cache_lens[b] + path[b][i] held before the call, for
+ * i < count[b], in every layer; other slots stay. The caller adds count[b] to
+ * its lengths (and appends the accepted tokens' queries, bkv_append_queries).
+ *   K, V:  host arrays of `layers` device pointers, as bkv_evict.
+ *   path:  device int32 [batch][n]: node indices 0 .. n - 1 in any order, a node
+ *          may appear twice; entries at and behind count[b] are not read.
+ *   count: device int32 [batch], 0 .. n; n: 1 .. 64. */
+bkv_status bkv_commit_tree(const bkv_config* cfg, void* const* K, void* const* V, const int32_t* cache_lens,
+                           const int32_t* path, const int32_t* count, int32_t n, uint32_t* status,
+                           void* cuda_stream);
+
 /* Self-test of the bounded device-side waits every kernel uses (the timeout
  * latch and the abort of the other waiting warps): enqueues on the handle's
  * stream a kernel whose four warps wait up to wait_cycles SM clock cycles

@@ -43,6 +43,7 @@ EXPORTED = ["bkv_workspace_bytes", "bkv_create", "bkv_set_stream", "bkv_append_q
             "bkv_evict", "bkv_prefill", "bkv_coverage", "bkv_selftest_wait", "bkv_sync",
             "bkv_get_fps_trace", "bkv_get_scores", "bkv_get_head_state",
             "bkv_profile", "bkv_profile_read", "bkv_score_select_noalloc", "bkv_get_stats",
+            "bkv_store_kv", "bkv_attend_prompt", "bkv_attend_tree", "bkv_commit_tree",
             "bkv_destroy", "bkv_status_str"]
 KERNELS = ["append", "rope", "score_select", "fps", "coverage", "prefill"]
 
@@ -84,6 +85,13 @@ _lib.bkv_profile.argtypes = [_vp, _i32]
 _lib.bkv_profile_read.argtypes = [_vp, ctypes.POINTER(BkvKernelTimes)]
 _lib.bkv_score_select_noalloc.argtypes = [ctypes.POINTER(BkvConfig), _vp, _vp, _i32, _i32,
                                           ctypes.POINTER(_vp), _i32, _i64, _vp, _vp, _vp]
+_lib.bkv_store_kv.argtypes = [ctypes.POINTER(BkvConfig), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.bkv_attend_prompt.argtypes = [ctypes.POINTER(BkvConfig), _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.bkv_attend_tree.argtypes = [ctypes.POINTER(BkvConfig), _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                 _vp]
+_lib.bkv_commit_tree.argtypes = [ctypes.POINTER(BkvConfig), ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _vp,
+                                 _i32, _vp, _vp]
 _lib.bkv_destroy.argtypes = [_vp]
 _lib.bkv_destroy.restype = None
 _lib.bkv_status_str.argtypes = [_i32]
@@ -291,6 +299,141 @@ def bkv_score_select_noalloc(cfg: BkvConfig, bq, rq, beacons: int, recents: int,
                                          _vp(status.data_ptr() if status is not None else 0),
                                          _vp(_stream_ptr(stream))),
            "bkv_score_select_noalloc")
+
+
+def _check_on_device(t, name: str, dtype, shape, device):
+    """_check_tensor, and that t lives on the current device (kernels launch there)."""
+    _check_tensor(t, name, dtype, shape)
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _check_packed(t, name: str, shape, device):
+    """Raises ValueError unless t is a bf16 CUDA tensor of this shape whose heads and
+    elements are contiguous; returns its address and the elements between two tokens."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    ok = t.dtype == torch.bfloat16 and t.is_cuda and tuple(t.shape) == tuple(shape)
+    stride = shape[-2] * shape[-1]
+    if ok:
+        s = t.stride()
+        # a dimension of one element may have any stride
+        ok = s[-1] == 1 and (s[-2] == shape[-1] or shape[-2] == 1)
+        if shape[-3] != 1:
+            stride = s[-3]
+        elif len(shape) == 4 and shape[0] != 1:
+            stride = s[0]
+        if len(shape) == 4 and shape[0] != 1 and shape[1] != 1:
+            ok = ok and s[0] == shape[1] * stride
+    if not ok:
+        raise ValueError(f"{name}: expected a CUDA torch.bfloat16 tensor of shape {tuple(shape)} with contiguous "
+                         f"heads and evenly spaced tokens, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+    return t.data_ptr(), stride
+
+
+def _optional(t, name: str, dtype, shape, device) -> int:
+    return 0 if t is None else _check_on_device(t, name, dtype, shape, device)
+
+
+def _packed_total(t, name: str) -> int:
+    if getattr(t, "ndim", 0) != 3:
+        raise ValueError(f"{name}: expected a tensor [tokens][heads][d]")
+    return t.shape[0]
+
+
+def bkv_store_kv(cfg: BkvConfig, q_pre, k_pre, v, cu_seqlens, first_slot, first_pos, q_rot, K, V, *,
+                 depth=None, status=None, stream=None) -> None:
+    """RoPE and the write to the cache slots (see include/bkv.h). q_pre [total][heads][d],
+    k_pre, v [total][kv_heads][d]: bf16, tokens any multiple of 8 elements apart; q_rot bf16
+    [total][heads][d]; cu_seqlens int32 [batch + 1]; first_slot, first_pos int32 [batch];
+    depth: optional int32 [total]; K, V: one layer's bf16 caches
+    [batch][kv_heads][max_cache][d]; status: optional int32 of one element."""
+    import torch
+    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
+    total = _packed_total(q_pre, "q_pre")
+    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
+    q, qs = _check_packed(q_pre, "q_pre", (total, c.heads, c.d), dev)
+    k, ks = _check_packed(k_pre, "k_pre", (total, c.kv_heads, c.d), dev)
+    vv, vs = _check_packed(v, "v", (total, c.kv_heads, c.d), dev)
+    _check(_lib.bkv_store_kv(
+        ctypes.byref(c), q, qs, k, ks, vv, vs, total,
+        _check_on_device(cu_seqlens, "cu_seqlens", i32, (c.batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, (c.batch,), dev),
+        _check_on_device(first_pos, "first_pos", i32, (c.batch,), dev),
+        _optional(depth, "depth", i32, (total,), dev),
+        _check_on_device(q_rot, "q_rot", torch.bfloat16, (total, c.heads, c.d), dev),
+        _check_on_device(K, "K", torch.bfloat16, cache, dev), _check_on_device(V, "V", torch.bfloat16, cache, dev),
+        _optional(status, "status", i32, (1,), dev), _stream_ptr(stream)), "bkv_store_kv")
+
+
+def bkv_attend_prompt(cfg: BkvConfig, q, K, V, cu_seqlens, first_slot, out, *, lse=None, status=None,
+                      stream=None) -> None:
+    """Causal attention of packed prompts over one layer's caches (see include/bkv.h).
+    q [total][heads][d]: rotated queries, bf16, tokens any multiple of 8 elements apart;
+    out bf16 [total][heads][d]; lse: optional float32 [total][heads]; the others as
+    bkv_store_kv."""
+    import torch
+    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
+    total = _packed_total(q, "q")
+    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
+    qp, qs = _check_packed(q, "q", (total, c.heads, c.d), dev)
+    _check(_lib.bkv_attend_prompt(
+        ctypes.byref(c), qp, qs, _check_on_device(K, "K", torch.bfloat16, cache, dev),
+        _check_on_device(V, "V", torch.bfloat16, cache, dev),
+        _check_on_device(cu_seqlens, "cu_seqlens", i32, (c.batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, (c.batch,), dev), total,
+        _check_on_device(out, "out", torch.bfloat16, (total, c.heads, c.d), dev),
+        _optional(lse, "lse", torch.float32, (total, c.heads), dev), _optional(status, "status", i32, (1,), dev),
+        _stream_ptr(stream)), "bkv_attend_prompt")
+
+
+def bkv_attend_tree(cfg: BkvConfig, q, K, V, cache_lens, out, *, mask=None, nodes=None, lse=None, status=None,
+                    stream=None) -> None:
+    """Attention of a tree of drafted tokens (n = 1: a decode step) over one layer's
+    caches (see include/bkv.h). q: rotated queries, bf16 [batch][n][heads][d]; cache_lens
+    int32 [batch]; mask: optional int64 [batch][n]; nodes: optional int32 [batch]; out bf16
+    [batch][n][heads][d]; lse: optional float32 [batch][n][heads]."""
+    import torch
+    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
+    if getattr(q, "ndim", 0) != 4:
+        raise ValueError("q: expected a tensor [batch][n][heads][d]")
+    n = q.shape[1]
+    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
+    qp, qs = _check_packed(q, "q", (c.batch, n, c.heads, c.d), dev)
+    _check(_lib.bkv_attend_tree(
+        ctypes.byref(c), qp, qs, _check_on_device(K, "K", torch.bfloat16, cache, dev),
+        _check_on_device(V, "V", torch.bfloat16, cache, dev),
+        _check_on_device(cache_lens, "cache_lens", i32, (c.batch,), dev), n,
+        _optional(mask, "mask", torch.int64, (c.batch, n), dev), _optional(nodes, "nodes", i32, (c.batch,), dev),
+        _check_on_device(out, "out", torch.bfloat16, (c.batch, n, c.heads, c.d), dev),
+        _optional(lse, "lse", torch.float32, (c.batch, n, c.heads), dev),
+        _optional(status, "status", i32, (1,), dev), _stream_ptr(stream)), "bkv_attend_tree")
+
+
+def bkv_commit_tree(cfg: BkvConfig, K, V, cache_lens, path, count, *, status=None, stream=None) -> None:
+    """Keeps an accepted path in every layer (see include/bkv.h). K, V: `layers` bf16
+    caches [batch][kv_heads][max_cache][d]; cache_lens, count int32 [batch]; path int32
+    [batch][n]."""
+    import torch
+    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
+    if getattr(path, "ndim", 0) != 2:
+        raise ValueError("path: expected a tensor [batch][n]")
+    n = path.shape[1]
+    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
+    for name, ts in (("K", K), ("V", V)):
+        if len(ts) != c.layers:
+            raise ValueError(f"{name}: expected {c.layers} per-layer tensors, got {len(ts)}")
+    kp = (_vp * c.layers)(*[_check_on_device(t, f"K[{l}]", torch.bfloat16, cache, dev) for l, t in enumerate(K)])
+    vp = (_vp * c.layers)(*[_check_on_device(t, f"V[{l}]", torch.bfloat16, cache, dev) for l, t in enumerate(V)])
+    _check(_lib.bkv_commit_tree(
+        ctypes.byref(c), kp, vp, _check_on_device(cache_lens, "cache_lens", i32, (c.batch,), dev),
+        _check_on_device(path, "path", i32, (c.batch, n), dev),
+        _check_on_device(count, "count", i32, (c.batch,), dev), n, _optional(status, "status", i32, (1,), dev),
+        _stream_ptr(stream)), "bkv_commit_tree")
 
 
 def bkv_get_stats(h: Handle) -> BkvStats:

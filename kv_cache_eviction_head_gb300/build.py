@@ -43,7 +43,7 @@ def _nvcc() -> str:
 
 def _stamp(sources: list[str], nvcc: str) -> str:
     h = hashlib.sha256()
-    for p in sorted(sources + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "bkv.h")]):
+    for p in sorted(sources + glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + [os.path.join(INCLUDE, "bkv.h")]):
         h.update(p.encode())
         with open(p, "rb") as f:
             h.update(f.read())

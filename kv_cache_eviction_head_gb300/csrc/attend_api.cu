@@ -1,0 +1,216 @@
+// Host side of the model-side calls over the caches (bkv_store_kv,
+// bkv_attend_prompt, bkv_attend_tree, bkv_commit_tree): argument checks and
+// launches. No handle, no workspace, no device allocation.
+#include <cmath>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "attend/attend.cuh"
+
+namespace {
+
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// The checks of bkv_create's config, and what these kernels need of it.
+bkv_status check(const bkv_config* c) {
+  size_t bytes = 0;
+  const bkv_status st = bkv_workspace_bytes(c, &bytes);
+  if (st != BKV_OK) return st;
+  if (c->heads / c->kv_heads > bkv::kMaxGroup) return BKV_ERR_UNSUPPORTED;
+  return BKV_OK;
+}
+
+// A packed [tokens][heads][d] tensor whose tokens lie `stride` elements apart
+// (no tokens: the pointer is not looked at).
+bool strided_ok(const void* p, int64_t stride, int heads, int d, int tokens) {
+  return (tokens == 0 || p) && aligned(p, 16) && stride >= (int64_t)heads * d && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+bkv_status zero_status(uint32_t* status, cudaStream_t s) {
+  if (status && cudaMemsetAsync(status, 0, sizeof(uint32_t), s) != cudaSuccess) return BKV_ERR_CUDA;
+  return BKV_OK;
+}
+
+constexpr int kSlots1 = 2 * 152;  // CTAs of one tile that GB300 holds at once (two per SM)
+constexpr int kSlots2 = 152;      // CTAs of two tiles
+
+// Ring stages: two CTAs of one tile share an SM's 228 KB; fewer than two would
+// fit three there, and three ask for more TMEM columns (256 each) than it has.
+int stages_for(int nq, int group, int tpt) {
+  const int q = nq * 2 * ((group * tpt + 7) / 8) * 1024;
+  const int room = (nq == 1 ? 113 : 227) * 1024 - 1280 - q;
+  const int n = room / (32 * 1024);
+  return n < 6 ? n : 6;
+}
+
+}  // namespace
+
+extern "C" {
+
+bkv_status bkv_store_kv(const bkv_config* cfg, const void* q_pre, int64_t q_stride, const void* k_pre,
+                        int64_t k_stride, const void* v, int64_t v_stride, int32_t total, const int32_t* cu_seqlens,
+                        const int32_t* first_slot, const int32_t* first_pos, const int32_t* depth, void* q_rot,
+                        void* K, void* V, uint32_t* status, void* cuda_stream) {
+  NvtxRange nvtx("bkv_store_kv");
+  const bkv_status st = check(cfg);
+  if (st != BKV_OK) return st;
+  const bkv_config& c = *cfg;
+  if (total < 0 || !cu_seqlens || !first_slot || !first_pos || (total > 0 && !q_rot) || !K || !V || !aligned(cu_seqlens, 4) ||
+      !aligned(first_slot, 4) || !aligned(first_pos, 4) || !aligned(depth, 4) || !aligned(q_rot, 16) ||
+      !aligned(K, 16) || !aligned(V, 16) || !aligned(status, 4))
+    return BKV_ERR_INVALID_ARG;
+  if (!strided_ok(q_pre, q_stride, c.heads, c.d, total) || !strided_ok(k_pre, k_stride, c.kv_heads, c.d, total) ||
+      !strided_ok(v, v_stride, c.kv_heads, c.d, total))
+    return BKV_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
+  if (total == 0) return BKV_OK;
+  bkv::StoreParams p{};
+  p.q = static_cast<const uint4*>(q_pre);
+  p.k = static_cast<const uint4*>(k_pre);
+  p.v = static_cast<const uint4*>(v);
+  p.q_stride = q_stride / 8;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.cu = cu_seqlens;
+  p.first = first_slot;
+  p.pos = first_pos;
+  p.depth = depth;
+  p.q_rot = static_cast<uint4*>(q_rot);
+  p.K = static_cast<uint4*>(K);
+  p.V = static_cast<uint4*>(V);
+  p.status = status;
+  p.batch = c.batch;
+  p.heads = c.heads;
+  p.kv_heads = c.kv_heads;
+  p.max_cache = c.max_cache;
+  p.total = total;
+  for (int i = 0; i < bkv::kRopePairs; ++i) {
+    double turns = std::pow(c.rope_theta, -2.0 * i / (double)c.d) * 0.15915494309189535;  // 1 / (2 pi)
+    turns -= std::floor(turns);
+    p.turns[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0ull;
+  }
+  return bkv::launch_store(p, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+
+bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K, const void* V,
+                             const int32_t* cu_seqlens, const int32_t* first_slot, int32_t total, void* out,
+                             float* lse, uint32_t* status, void* cuda_stream) {
+  NvtxRange nvtx("bkv_attend_prompt");
+  const bkv_status st = check(cfg);
+  if (st != BKV_OK) return st;
+  const bkv_config& c = *cfg;
+  if (total < 0 || !K || !V || !cu_seqlens || !first_slot || (total > 0 && !out) || !aligned(K, 16) || !aligned(V, 16) ||
+      !aligned(cu_seqlens, 4) || !aligned(first_slot, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(status, 4) || !strided_ok(q, q_stride, c.heads, c.d, total))
+    return BKV_ERR_INVALID_ARG;
+  bkv::AttendParams p{};
+  p.cu = cu_seqlens;
+  p.first = first_slot;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.batch = c.batch;
+  p.heads = c.heads;
+  p.kv_heads = c.kv_heads;
+  p.group = c.heads / c.kv_heads;
+  p.max_cache = c.max_cache;
+  p.total = total;
+  p.tpt = 128 / p.group < total ? 128 / p.group : (total > 0 ? total : 1);
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.d));
+  // row blocks of nq tiles: at most total / (nq tpt) full ones and one ragged one per sequence
+  auto items_of = [&](int nq) { return ((int64_t)total / (nq * p.tpt) + c.batch) * c.kv_heads; };
+  const int nq = items_of(2) > kSlots2 / 2 && p.tpt < total ? 2 : 1;
+  const int64_t items = items_of(nq);
+  if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
+  p.stages = stages_for(nq, p.group, p.tpt);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (total > 0 && !bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
+  if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
+  if (total == 0) return BKV_OK;
+  return bkv::launch_attend(p, nq, 1, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+
+bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K, const void* V,
+                           const int32_t* cache_lens, int32_t n, const int64_t* mask, const int32_t* nodes, void* out,
+                           float* lse, uint32_t* status, void* cuda_stream) {
+  NvtxRange nvtx("bkv_attend_tree");
+  const bkv_status st = check(cfg);
+  if (st != BKV_OK) return st;
+  const bkv_config& c = *cfg;
+  if (n < 1 || !K || !V || !cache_lens || !out || !aligned(K, 16) || !aligned(V, 16) || !aligned(cache_lens, 4) ||
+      !aligned(mask, 8) || !aligned(nodes, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4) ||
+      !strided_ok(q, q_stride, c.heads, c.d, 1))
+    return BKV_ERR_INVALID_ARG;
+  if (n > bkv::kMaxNodes || (int64_t)c.batch * n > 0x7FFFFFFF) return BKV_ERR_UNSUPPORTED;
+  bkv::AttendParams p{};
+  p.first = cache_lens;
+  p.nodes = nodes;
+  p.mask = mask;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.batch = c.batch;
+  p.heads = c.heads;
+  p.kv_heads = c.kv_heads;
+  p.group = c.heads / c.kv_heads;
+  p.max_cache = c.max_cache;
+  p.total = c.batch * n;
+  p.n = n;
+  p.tpt = 128 / p.group < n ? 128 / p.group : n;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.d));
+  const int nq = p.tpt < n ? 2 : 1;
+  p.qblocks = (n + nq * p.tpt - 1) / (nq * p.tpt);
+  const int64_t items = (int64_t)c.batch * c.kv_heads * p.qblocks;
+  if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
+  // keys split over a cluster while CTAs are fewer than the GPU holds
+  const int slots = nq == 1 ? kSlots1 : kSlots2, tiles = (c.max_cache + 127) / 128;
+  int splits = 1;
+  while (splits < 16 && items * splits * 2 <= slots && splits * 2 <= tiles) splits *= 2;
+  p.stages = stages_for(nq, p.group, p.tpt);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (!bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
+  if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
+  return bkv::launch_attend(p, nq, splits, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+
+bkv_status bkv_commit_tree(const bkv_config* cfg, void* const* K, void* const* V, const int32_t* cache_lens,
+                           const int32_t* path, const int32_t* count, int32_t n, uint32_t* status,
+                           void* cuda_stream) {
+  NvtxRange nvtx("bkv_commit_tree");
+  const bkv_status st = check(cfg);
+  if (st != BKV_OK) return st;
+  const bkv_config& c = *cfg;
+  if (n < 1 || !K || !V || !cache_lens || !path || !count || !aligned(cache_lens, 4) || !aligned(path, 4) ||
+      !aligned(count, 4) || !aligned(status, 4))
+    return BKV_ERR_INVALID_ARG;
+  for (int l = 0; l < c.layers; ++l)
+    if (!K[l] || !V[l] || !aligned(K[l], 16) || !aligned(V[l], 16)) return BKV_ERR_INVALID_ARG;
+  if (n > bkv::kMaxNodes) return BKV_ERR_UNSUPPORTED;
+  bkv::CommitParams p{};
+  for (int l = 0; l < c.layers; ++l) {
+    p.K[l] = static_cast<uint4*>(K[l]);
+    p.V[l] = static_cast<uint4*>(V[l]);
+  }
+  p.lens = cache_lens;
+  p.path = path;
+  p.count = count;
+  p.status = status;
+  p.batch = c.batch;
+  p.kv_heads = c.kv_heads;
+  p.max_cache = c.max_cache;
+  p.n = n;
+  p.layers = c.layers;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
+  return bkv::launch_commit(p, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,668 @@
+// Softmax attention of packed prompt tokens, or of a tree of drafted tokens,
+// over the caches, on the fifth-generation tensor cores.
+//
+//   o[r] = sum_j p_rj V[j],  p_rj = exp(l_rj - lse_r),  l_rj = q_r . k_j / sqrt(d),
+//   lse_r = ln sum_j exp(l_rj), over the slots j that row r sees.
+//
+// A row is (token, query head of the group); a tile is the 128 rows of
+// tpt = 128 / G consecutive tokens, so that the G query heads that share a KV
+// head read its keys once. One pass over the keys with a running maximum and
+// sum: per 128-key tile S = Q K^T goes to TMEM, one thread per row reads its
+// 128 logits, subtracts its reference maximum, exponentiates and writes P back
+// over S as bf16, and O += P V accumulates in TMEM with P as the TMEM operand.
+//
+// Rounding: l, the maximum, the sum and O are fp32; P is rounded to bf16 for
+// the product with bf16 V (relative 2^-9 per term, like the output's own
+// rounding); the sum adds the unrounded values.
+//
+// The reference maximum only moves when a tile's maximum exceeds it by more
+// than 8 (a factor 256 in P, which costs bf16 and fp32 no precision); O and
+// the sum are rescaled then. The QK^T of a tile is issued after the PV of the
+// tile before, so a row that has its logits may rescale O without further
+// synchronisation.
+//
+// Warps: 4 per 128-row tile for softmax and epilogue, one TMA producer, one
+// MMA issuer. K and V tiles alternate in one ring of 32 KB stages.
+//
+// Few rows: the keys of a row block are split over the CTAs of a cluster; each
+// keeps its own maximum, sum and O, and the partial results are joined through
+// distributed shared memory, in rank order, so results do not vary.
+//
+// Slots at or behind the last visible one may hold anything: their logits are
+// replaced, not added to, and their V rows are zeroed in shared memory.
+#include <atomic>
+
+#include "attend/attend.cuh"
+#include "score_common.cuh"
+
+namespace bkv {
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;  // log2 units by which the reference maximum may lag
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+// A (the 128 x 16 bf16 probabilities) from TMEM, two elements per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// B operand V [keys][d], d contiguous: MN-major SWIZZLE_128B. One atom is 64 d
+// x 8 keys (8 rows of 128 bytes); the next 8 keys follow 1024 bytes on (SBO),
+// the next 64 d one slab on (LBO).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kSlabBytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // instruction descriptor: B is MN-major
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// What one row block works on.
+struct Block {
+  int b, h;      // sequence, KV head
+  int64_t row0;  // packed index of its first token
+  int cnt;       // its tokens
+  int past;      // slots before its first token (causal: token i sees past + i + 1 slots)
+  int L;         // tree: committed slots (every node sees them)
+  int nodes;     // tree: nodes visible in the cache
+  int kv_len;    // slots that some row may see
+  int i0;        // its first token's place in the sequence
+  bool bad;      // a length had to be clamped
+};
+
+// Prompt: row blocks sequence by sequence, the last (longest) first. Every warp
+// runs this; items beyond the last block return cnt = 0.
+__device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int64_t item, int tpi) {
+  const int lane = threadIdx.x & 31;
+  Block k;
+  k.h = (int)(item % P.kv_heads);
+  int64_t at = item / P.kv_heads;
+  k.b = 0;
+  k.row0 = 0;
+  k.cnt = k.past = k.L = k.nodes = k.kv_len = k.i0 = 0;
+  k.bad = false;
+  for (int b0 = 0; b0 < P.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int begin = 0, len = 0, nb = 0;
+    bool bad = false;
+    if (b < P.batch) {
+      const int lo = P.cu[b], hi = P.cu[b + 1];
+      begin = min(max(lo, 0), P.total);
+      const int end = min(max(hi, begin), P.total);
+      len = end - begin;
+      bad = begin != lo || end != hi;
+      nb = (len + tpi - 1) / tpi;
+    }
+    int sum = nb;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kFull, sum, off);
+      if (lane >= off) sum += y;
+    }
+    const unsigned hit = __ballot_sync(kFull, at < sum);
+    const bool any_bad = __any_sync(kFull, bad);
+    k.bad |= any_bad;
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      k.b = b0 + src;
+      const int before = __shfl_sync(kFull, sum - nb, src);
+      const int blocks = __shfl_sync(kFull, nb, src);
+      const int n = __shfl_sync(kFull, len, src);
+      const int beg = __shfl_sync(kFull, begin, src);
+      const int qb = blocks - 1 - ((int)at - before);
+      k.i0 = qb * tpi;
+      k.row0 = (int64_t)beg + k.i0;
+      k.cnt = min(tpi, n - k.i0);
+      const int f = P.first[k.b];
+      const int fc = min(max(f, 0), P.max_cache);
+      k.past = fc + k.i0;  // at most max_cache + total
+      k.L = 0;
+      k.kv_len = (int)min((int64_t)k.past + k.cnt, (int64_t)P.max_cache);
+      k.bad |= fc != f || (int64_t)k.past + k.cnt > P.max_cache;
+      return k;
+    }
+    at -= __shfl_sync(kFull, sum, 31);
+  }
+  return k;
+}
+
+__device__ __forceinline__ Block find_tree_block(const AttendParams& P, int64_t item, int tpi) {
+  Block k;
+  const int qb = (int)(item % P.qblocks);
+  const int64_t u = item / P.qblocks;
+  k.h = (int)(u % P.kv_heads);
+  k.b = (int)(u / P.kv_heads);
+  const int len = P.first[k.b];
+  const int nn = P.nodes ? P.nodes[k.b] : P.n;
+  const int used = min(max(nn, 0), P.n);
+  k.L = min(max(len, 0), P.max_cache);
+  k.nodes = min(used, P.max_cache - k.L);
+  k.kv_len = k.L + k.nodes;
+  k.bad = k.L != len || used != nn || k.nodes != used;
+  k.i0 = qb * tpi;
+  k.row0 = (int64_t)k.b * P.n + k.i0;
+  k.cnt = min(tpi, used - k.i0);
+  k.past = k.L + k.i0;
+  return k;
+}
+
+struct Smem {
+  uint32_t slab_q, q, ring, bars, total;
+};
+// The ring starts behind the rows in use; an MMA reads 128 rows of Q whatever
+// their number, the rest of them from the ring: rows nobody looks at.
+__host__ __device__ inline Smem attend_smem(int nq, int group, int tpt, int stages) {
+  Smem s;
+  s.slab_q = (uint32_t)((group * tpt + 7) / 8) * 1024;
+  s.q = 0;
+  s.ring = s.q + (uint32_t)nq * 2 * s.slab_q;
+  s.bars = s.ring + (uint32_t)stages * kTileBytes;
+  s.total = s.bars + 256 + 1024;  // barriers, and 1 KB to align the base
+  return s;
+}
+
+constexpr int kMaxStages = 6;
+
+template <int NQ>
+__global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
+attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int kProducer = NQ * 4, kIssuer = NQ * 4 + 1;
+  constexpr uint32_t kCols = NQ * 256;  // per tile: 128 columns of S (and P), 128 of O
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % (unsigned)splits);
+  const int64_t item = blockIdx.x / (unsigned)splits;
+  const int tpi = NQ * P.tpt;
+  const Block blk = P.cu ? find_prompt_block(P, item, tpi) : find_tree_block(P, item, tpi);
+  if (blk.bad && tid == 0) latch(P.status, BKV_ERR_INVALID_ARG);
+  if (blk.cnt <= 0) return;  // the whole cluster: all its CTAs have the same item
+
+  const Smem lay = attend_smem(NQ, P.group, P.tpt, P.stages);
+  unsigned char* q_s = smem + lay.q;
+  unsigned char* ring = smem + lay.ring;
+  float2* ml = reinterpret_cast<float2*>(q_s);  // [NQ * 128] partial maximum and sum, once Q is done with
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* full = bars;                      // [stages]
+  uint64_t* empty = bars + kMaxStages;        // [stages]
+  uint64_t* qfull = bars + 2 * kMaxStages;
+  uint64_t* sfull = qfull + 1;                // [NQ] a tile's logits are in TMEM (and the PV before is done)
+  uint64_t* pfull = sfull + 2;                // [NQ] its probabilities are
+  uint64_t* ofull = pfull + 2;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + lay.bars + 224);
+
+  const int S = P.stages;
+  const int T = (blk.kv_len + kTileKeys - 1) / kTileKeys;
+  const int t_lo = (int)((int64_t)T * rank / splits), t_hi = (int)((int64_t)T * (rank + 1) / splits);
+  const int nt = t_hi - t_lo;
+  const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;  // tiles with rows
+  auto rows_of = [&](int q) { return min(blk.cnt - q * P.tpt, P.tpt) * P.group; };
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(ofull, 1);
+    for (int q = 0; q < nq; ++q) {
+      mbar_init(&sfull[q], 1);
+      mbar_init(&pfull[q], (uint32_t)(rows_of(q) + 31) / 32);  // one arrival per warp with rows
+    }
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssuer) tmem_alloc(&ctl->tmem_base, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0 && nt > 0) {
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
+      mbar_expect_tx(qfull, (uint32_t)nq * 2 * qbytes);
+      for (int q = 0; q < nq; ++q)
+        for (int s = 0; s < 2; ++s)
+          tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
+                      (int)(blk.row0 + q * P.tpt), qfull, pol);
+      const int z = blk.b * P.kv_heads + blk.h;
+      int st = 0, g = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; i < 2 * nt; ++i, ++g) {
+        if (g >= S) ok = mbar_wait(&empty[st], ph ^ 1u, ctl, P.status);
+        if (!ok) break;
+        mbar_expect_tx(&full[st], kTileBytes);
+        const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
+        const CUtensorMap* map = (i & 1) ? &P.vmap : &P.kmap;
+        const int y = (t_lo + (i >> 1)) * kTileKeys;
+        tma_load_3d(dst, map, 0, y, z, &full[st], pol);
+        tma_load_3d(dst + kSlabBytes, map, 64, y, z, &full[st], pol);
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) {  // after an abort, loads already issued must land before the CTA exits
+        long long t0 = clock64();
+        while (!mbar_test(qfull, 0u) && clock64() - t0 < kWaitCycles) {
+        }
+        for (int s = 0; s < S && s < g; ++s) {
+          const int last = g - 1 - ((g - 1 - s) % S);
+          t0 = clock64();
+          while (!mbar_test(&full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
+          }
+        }
+      }
+    }
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ MMA issuer
+    if (nt > 0) {
+      const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
+      constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
+      auto issue_qk = [&](int q, int st) {
+        const uint32_t kb = rb + (uint32_t)st * kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (uint32_t)(kk & 3) * 32;
+          umma_bf16(tmem + (uint32_t)q * 256, sw128_desc(qb + (uint32_t)(2 * q + (kk >> 2)) * lay.slab_q + off),
+                    sw128_desc(kb + (uint32_t)(kk >> 2) * kSlabBytes + off), id_qk, kk ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int q, int st, bool acc) {
+        const uint32_t vb = rb + (uint32_t)st * kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(tmem + (uint32_t)q * 256 + 128, tmem + (uint32_t)q * 256 + (uint32_t)kk * 8,
+                       sw128_mn_desc(vb + (uint32_t)kk * 2048), id_pv, (acc || kk) ? 1u : 0u);
+      };
+      bool ok = __all_sync(kFull, mbar_wait(qfull, 0u, ctl, P.status));
+      ok = ok && __all_sync(kFull, mbar_wait(&full[0], 0u, ctl, P.status));
+      bool issued = false;
+      if (ok) {
+        tc_fence_after();
+        if (lane == 0) {
+          for (int q = 0; q < nq; ++q) {
+            issue_qk(q, 0);
+            umma_commit(&sfull[q]);
+          }
+          umma_commit(&empty[0]);
+        }
+        issued = true;
+      }
+      int sv = 1 % S;             // stage of V_j; K_{j+1} follows
+      uint32_t pv = S == 1 ? 1u : 0u;
+      for (int j = 0; j < nt && ok; ++j) {
+        int sk = sv + 1;
+        uint32_t pk = pv;
+        if (sk == S) {
+          sk = 0;
+          pk ^= 1u;
+        }
+        ok = __all_sync(kFull, mbar_wait(&full[sv], pv, ctl, P.status));
+        if (!ok) break;
+        const int live = blk.kv_len - (t_lo + j) * kTileKeys;  // keys of this tile that exist
+        if (live < kTileKeys) {
+          // V rows behind the last slot may hold NaN, and 0 * NaN is NaN
+          uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
+          for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
+            rows[i] = make_uint4(0, 0, 0, 0);
+            rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        const bool more = j + 1 < nt;
+        for (int q = 0; q < nq; ++q) {
+          ok = __all_sync(kFull, mbar_wait(&pfull[q], (uint32_t)(j & 1), ctl, P.status));
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) issue_pv(q, sv, j > 0);
+          if (more) {
+            if (q == 0) ok = __all_sync(kFull, mbar_wait(&full[sk], pk, ctl, P.status));
+            if (!ok) break;
+            if (lane == 0) {
+              issue_qk(q, sk);
+              umma_commit(&sfull[q]);
+            }
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          umma_commit(&empty[sv]);
+          if (more) umma_commit(&empty[sk]);
+          else umma_commit(ofull);
+        }
+        sv = sk + 1;
+        pv = pk;
+        if (sv == S) {
+          sv = 0;
+          pv ^= 1u;
+        }
+      }
+      if (!ok && issued && lane == 0) {
+        // after an abort, let the MMAs already issued finish before the TMEM is freed
+        umma_commit(ofull);
+        const long long t0 = clock64();
+        while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int q = NQ == 1 ? 0 : warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int rows = q < nq ? rows_of(q) : 0;
+    if ((warp & 3) * 32 < rows) {
+      const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
+      const uint32_t t_s = tl + (uint32_t)q * 256, t_o = t_s + 128;
+      const bool valid = row < rows;
+      const int tok = q * P.tpt + (valid ? row / P.group : 0);
+      // slots [0, lim) are visible, and the tree's slots L + i whose bit is set
+      int lim = min(blk.past + tok + 1, blk.kv_len);
+      uint64_t bits = 0;
+      if (P.mask) {
+        lim = blk.L;
+        if (valid) bits = (uint64_t)P.mask[blk.row0 + tok];
+        if (blk.nodes < 64) bits &= (1ull << blk.nodes) - 1ull;
+      }
+      // tiles that end at or below every row's bound need no mask
+      const int lim_min = P.mask ? blk.L : min(blk.past + q * P.tpt + 1, blk.kv_len);
+      float m = kNegInf, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        ok = __all_sync(kFull, mbar_wait(&sfull[q], (uint32_t)(j & 1), ctl, P.status));
+        if (!ok) break;
+        tc_fence_after();
+        float v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + (uint32_t)c * 32, v[c]);
+        tmem_wait_ld();
+        const int base = (t_lo + j) * kTileKeys;
+        if (base + kTileKeys > lim_min) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int lo = base + 32 * c;
+            const int n = min(max(lim - lo, 0), 32);
+            uint32_t see = n >= 32 ? ~0u : (1u << n) - 1u;
+            const int sh = lo - blk.L;
+            if (sh >= 0) see |= sh < 64 ? (uint32_t)(bits >> sh) : 0u;
+            else if (sh > -32) see |= (uint32_t)(bits << -sh);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] = (see >> i) & 1u ? v[c][i] : kNegInf;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = v[c][0];
+#pragma unroll
+          for (int i = 1; i < 31; i += 2) mx[c] = fmaxf(fmaxf(mx[c], v[c][i]), v[c][i + 1]);
+          mx[c] = fmaxf(mx[c], v[c][31]);
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+        const bool move = mt > m + kRescale || (m == kNegInf && mt > kNegInf);
+        if (__any_sync(kFull, move)) {
+          const float m_new = fmaxf(m, mt);
+          const float f = m == kNegInf ? 0.f : fast_exp2(m - m_new);
+          l *= f;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(t_o + (uint32_t)c * 32, o);
+              tmem_wait_ld();
+              uint32_t r[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * f);
+              tmem_st32(t_o + (uint32_t)c * 32, r);
+            }
+          }
+          m = m_new;
+        }
+        const float off = m == kNegInf ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = 2 * half + (i >> 4), e = (i & 15) * 2;
+            const float a = fast_exp2(fmaf(v[c][e], P.scale_log2, off));
+            const float b = fast_exp2(fmaf(v[c][e + 1], P.scale_log2, off));
+            sum[(i & 1) * 2] += a;
+            sum[(i & 1) * 2 + 1] += b;
+            p[i] = pack_bf16(a, b);
+          }
+          tmem_st32(t_s + (uint32_t)half * 32, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[q]);
+      }
+      if (ok && nt > 0) {
+        ok = __all_sync(kFull, mbar_wait(ofull, 0u, ctl, P.status));
+        tc_fence_after();
+      }
+      if (splits > 1) {
+        ml[q * 128 + row] = make_float2(m, l);
+        if (ok && nt > 0) {
+          // partial O, 16-byte chunk c of a row at c ^ (row & 31): no bank conflicts
+          float4* part = reinterpret_cast<float4*>(ring) + (size_t)(q * 128 + row) * 32;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld32(t_o + (uint32_t)c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              part[(c * 8 + i) ^ lane] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      } else if (ok) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no visible slot: 0; NaN stays
+        const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + (row - (row / P.group) * P.group);
+        uint4* dst = reinterpret_cast<uint4*>(P.out) + orow * 16;
+        float check = 0.f;  // stays 0 unless some value is not finite
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          if (nt > 0) {
+            tmem_ld32(t_o + (uint32_t)c * 32, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] = nt > 0 && l != 0.f ? o[i] * inv : 0.f;
+            check = fmaf(o[i], 0.f, check);
+          }
+          if (valid && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[c * 4 + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                          pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+          }
+        }
+        if (valid && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) {
+          const float lse = l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
+          if (P.lse) P.lse[orow] = lse;
+          if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+        }
+      }
+    }
+  }
+
+  if (splits > 1) {
+    // ------------------------------------------------------------ join
+    __syncwarp();
+    cluster_sync();
+    if (!ctl->abort) {
+      const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
+      for (int q = 0; q < nq; ++q) {
+        const int rows = rows_of(q);
+        // rank r joins rows r, r + splits, ...; one warp per row, 4 columns per lane
+        for (int row = rank + warp * splits; row < rows; row += splits * (NQ * 4 + 2)) {
+          float mc = kNegInf, lc = 0.f;
+          if (lane < splits) {
+            const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(q * 128 + row) * 8, (uint32_t)lane));
+            mc = x.x;
+            lc = x.y;
+          }
+          float M = mc;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+          // a share without a visible key has no part in the sums (its O is not written or zero)
+          const float w = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
+          float l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = 0; c < splits; ++c) {
+            const float wc = __shfl_sync(kFull, w, c), lcc = __shfl_sync(kFull, lc, c);
+            if (wc == 0.f) continue;
+            l = fmaf(wc, lcc, l);
+            const float4 x = ld_cluster4(
+                map_rank(part + ((uint32_t)(q * 128 + row) * 32 + (uint32_t)(lane ^ (row & 31))) * 16, (uint32_t)c));
+            o.x = fmaf(wc, x.x, o.x);
+            o.y = fmaf(wc, x.y, o.y);
+            o.z = fmaf(wc, x.z, o.z);
+            o.w = fmaf(wc, x.w, o.w);
+          }
+          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+          o.x *= inv;
+          o.y *= inv;
+          o.z *= inv;
+          o.w *= inv;
+          const int tok = q * P.tpt + row / P.group;
+          const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + row % P.group;
+          if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
+          reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+          const float lse = l > 0.f ? (M + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
+          if (P.lse && lane == 0) P.lse[orow] = lse;
+          const float check = (o.x + o.y + o.z + o.w) * 0.f;
+          if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+        }
+      }
+    }
+    cluster_sync();  // no CTA leaves while another still reads its partial results
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, kCols);
+}
+
+}  // namespace
+
+bool encode_attend_maps(AttendParams& p, const void* q, int64_t q_stride, const void* K, const void* V) {
+  // the driver's encoder, looked up once per process (thread-safe static initialisation)
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult qres;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qres) !=
+            cudaSuccess ||
+        qres != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode) return false;
+  auto one = [&](CUtensorMap* map, const void* base, cuuint64_t d1, cuuint64_t s1, cuuint64_t d2, cuuint64_t s2,
+                 cuuint32_t b1, cuuint32_t b2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, d1, d2};
+    const cuuint64_t strides[2] = {s1, s2};
+    const cuuint32_t box[3] = {64, b1, b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t row = (cuuint64_t)kD * 2;
+  const cuuint64_t heads = (cuuint64_t)p.batch * p.kv_heads, plane = (cuuint64_t)p.max_cache * row;
+  return one(&p.qmap, q, (cuuint64_t)p.heads, row, (cuuint64_t)p.total, (cuuint64_t)q_stride * 2,
+             (cuuint32_t)p.group, (cuuint32_t)p.tpt) &&
+         one(&p.kmap, K, (cuuint64_t)p.max_cache, row, heads, plane, (cuuint32_t)kTileKeys, 1) &&
+         one(&p.vmap, V, (cuuint64_t)p.max_cache, row, heads, plane, (cuuint32_t)kTileKeys, 1);
+}
+
+cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* fn = nq == 1 ? reinterpret_cast<const void*>(attend_kernel<1>) : reinterpret_cast<const void*>(attend_kernel<2>);
+  // once per device and instance (one bit each)
+  static std::atomic<unsigned long long> configured[2] = {{0}, {0}};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(configured[nq - 1].load() & bit)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    configured[nq - 1].fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(items * splits));
+  cfg.blockDim = dim3((unsigned)(nq * 128 + 64));
+  cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)splits;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  return nq == 1 ? cudaLaunchKernelEx(&cfg, attend_kernel<1>, p, splits) : cudaLaunchKernelEx(&cfg, attend_kernel<2>, p, splits);
+}
+
+}  // namespace bkv
