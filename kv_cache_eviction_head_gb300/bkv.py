@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 import numpy as np
@@ -302,22 +303,46 @@ def bkv_score_select_noalloc(cfg: BkvConfig, bq, rq, beacons: int, recents: int,
 
 
 def _check_on_device(t, name: str, dtype, shape, device):
-    """_check_tensor, and that t lives on the current device (kernels launch there)."""
+    """_check_tensor, and that t lives on the current device (kernels launch there).
+    Returns its address. The first test passes without building a message: a decode
+    step's calls are short, and this is most of their host time."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _check_tensor(t, name, dtype, shape)
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+
+
+def _check_caches(ts, name: str, cfg, shape, device):
+    """A _vp array of `layers` bf16 caches of this shape on this device. The attributes of
+    all layers are gathered by C-level maps; on a mismatch the layers are looked at one by
+    one for the message."""
+    import torch
+    T = torch.Tensor
+    n = cfg.layers
+    if len(ts) != n:
+        raise ValueError(f"{name}: expected {n} per-layer tensors, got {len(ts)}")
+    try:
+        if (list(map(T.size, ts)) == [shape] * n and list(map(T.get_device, ts)) == [device] * n
+                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} == {torch.bfloat16}):
+            return (_vp * n).from_buffer(array("Q", map(T.data_ptr, ts)))
+    except (TypeError, AttributeError):
+        pass
+    return (_vp * n)(*[_check_on_device(t, f"{name}[{l}]", torch.bfloat16, shape, device) for l, t in enumerate(ts)])
 
 
 def _check_packed(t, name: str, shape, device):
-    """Raises ValueError unless t is a bf16 CUDA tensor of this shape whose heads and
-    elements are contiguous; returns its address and the elements between two tokens."""
+    """Raises ValueError unless t is a bf16 tensor of this shape on this device whose heads
+    and elements are contiguous and whose tokens are evenly spaced; returns its address and
+    the elements between two tokens."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    ok = t.dtype == torch.bfloat16 and t.is_cuda and tuple(t.shape) == tuple(shape)
+    ok = t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device
     stride = shape[-2] * shape[-1]
-    if ok:
+    if ok and not t.is_contiguous():
         s = t.stride()
         # a dimension of one element may have any stride
         ok = s[-1] == 1 and (s[-2] == shape[-1] or shape[-2] == 1)
@@ -328,10 +353,10 @@ def _check_packed(t, name: str, shape, device):
         if len(shape) == 4 and shape[0] != 1 and shape[1] != 1:
             ok = ok and s[0] == shape[1] * stride
     if not ok:
+        if t.is_cuda and t.get_device() != device:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
         raise ValueError(f"{name}: expected a CUDA torch.bfloat16 tensor of shape {tuple(shape)} with contiguous "
                          f"heads and evenly spaced tokens, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
     return t.data_ptr(), stride
 
 
@@ -424,11 +449,7 @@ def bkv_commit_tree(cfg: BkvConfig, K, V, cache_lens, path, count, *, status=Non
         raise ValueError("path: expected a tensor [batch][n]")
     n = path.shape[1]
     cache = (c.batch, c.kv_heads, c.max_cache, c.d)
-    for name, ts in (("K", K), ("V", V)):
-        if len(ts) != c.layers:
-            raise ValueError(f"{name}: expected {c.layers} per-layer tensors, got {len(ts)}")
-    kp = (_vp * c.layers)(*[_check_on_device(t, f"K[{l}]", torch.bfloat16, cache, dev) for l, t in enumerate(K)])
-    vp = (_vp * c.layers)(*[_check_on_device(t, f"V[{l}]", torch.bfloat16, cache, dev) for l, t in enumerate(V)])
+    kp, vp = _check_caches(K, "K", c, cache, dev), _check_caches(V, "V", c, cache, dev)
     _check(_lib.bkv_commit_tree(
         ctypes.byref(c), kp, vp, _check_on_device(cache_lens, "cache_lens", i32, (c.batch,), dev),
         _check_on_device(path, "path", i32, (c.batch, n), dev),

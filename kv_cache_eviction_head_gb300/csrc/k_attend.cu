@@ -22,7 +22,7 @@
 // synchronisation.
 //
 // Warps: 4 per 128-row tile for softmax and epilogue, one TMA producer, one
-// MMA issuer. K and V tiles alternate in one ring of 32 KB stages.
+// MMA issuer (and two idle ones, so that registers can move by warpgroup). K and V tiles alternate in one ring of 32 KB stages.
 //
 // Few rows: the keys of a row block are split over the CTAs of a cluster; each
 // keeps its own maximum, sum and O, and the partial results are joined through
@@ -83,6 +83,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -211,7 +238,7 @@ __host__ __device__ inline Smem attend_smem(int nq, int group, int tpt, int stag
 constexpr int kMaxStages = 6;
 
 template <int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
+__global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
 attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
@@ -235,8 +262,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   uint64_t* empty = bars + kMaxStages;        // [stages]
   uint64_t* qfull = bars + 2 * kMaxStages;
   uint64_t* sfull = qfull + 1;                // [NQ] a tile's logits are in TMEM (and the PV before is done)
-  uint64_t* pfull = sfull + 2;                // [NQ] its probabilities are
-  uint64_t* ofull = pfull + 2;
+  uint64_t* pfull = sfull + 2;                // [NQ][2] half of its probabilities are
+  uint64_t* ofull = pfull + 4;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + lay.bars + 224);
 
   const int S = P.stages;
@@ -255,7 +282,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     mbar_init(ofull, 1);
     for (int q = 0; q < nq; ++q) {
       mbar_init(&sfull[q], 1);
-      mbar_init(&pfull[q], (uint32_t)(rows_of(q) + 31) / 32);  // one arrival per warp with rows
+      for (int k = 0; k < 2; ++k)
+        mbar_init(&pfull[2 * q + k], (uint32_t)(rows_of(q) + 31) / 32);  // one arrival per warp with rows
     }
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -266,142 +294,157 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && nt > 0) {
-      const uint64_t pol = policy_evict_normal();
-      const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
-      mbar_expect_tx(qfull, (uint32_t)nq * 2 * qbytes);
-      for (int q = 0; q < nq; ++q)
-        for (int s = 0; s < 2; ++s)
-          tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
-                      (int)(blk.row0 + q * P.tpt), qfull, pol);
-      const int z = blk.b * P.kv_heads + blk.h;
-      int st = 0, g = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int i = 0; i < 2 * nt; ++i, ++g) {
-        if (g >= S) ok = mbar_wait(&empty[st], ph ^ 1u, ctl, P.status);
-        if (!ok) break;
-        mbar_expect_tx(&full[st], kTileBytes);
-        const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
-        const CUtensorMap* map = (i & 1) ? &P.vmap : &P.kmap;
-        const int y = (t_lo + (i >> 1)) * kTileKeys;
-        tma_load_3d(dst, map, 0, y, z, &full[st], pol);
-        tma_load_3d(dst + kSlabBytes, map, 64, y, z, &full[st], pol);
-        if (++st == S) {
-          st = 0;
-          ph ^= 1u;
-        }
-      }
-      if (!ok) {  // after an abort, loads already issued must land before the CTA exits
-        long long t0 = clock64();
-        while (!mbar_test(qfull, 0u) && clock64() - t0 < kWaitCycles) {
-        }
-        for (int s = 0; s < S && s < g; ++s) {
-          const int last = g - 1 - ((g - 1 - s) % S);
-          t0 = clock64();
-          while (!mbar_test(&full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
-          }
-        }
-      }
-    }
-  } else if (warp == kIssuer) {
-    // ------------------------------------------------------------ MMA issuer
-    if (nt > 0) {
-      const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
-      constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
-      auto issue_qk = [&](int q, int st) {
-        const uint32_t kb = rb + (uint32_t)st * kTileBytes;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (uint32_t)(kk & 3) * 32;
-          umma_bf16(tmem + (uint32_t)q * 256, sw128_desc(qb + (uint32_t)(2 * q + (kk >> 2)) * lay.slab_q + off),
-                    sw128_desc(kb + (uint32_t)(kk >> 2) * kSlabBytes + off), id_qk, kk ? 1u : 0u);
-        }
-      };
-      auto issue_pv = [&](int q, int st, bool acc) {
-        const uint32_t vb = rb + (uint32_t)st * kTileBytes;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(tmem + (uint32_t)q * 256 + 128, tmem + (uint32_t)q * 256 + (uint32_t)kk * 8,
-                       sw128_mn_desc(vb + (uint32_t)kk * 2048), id_pv, (acc || kk) ? 1u : 0u);
-      };
-      bool ok = __all_sync(kFull, mbar_wait(qfull, 0u, ctl, P.status));
-      ok = ok && __all_sync(kFull, mbar_wait(&full[0], 0u, ctl, P.status));
-      bool issued = false;
-      if (ok) {
-        tc_fence_after();
-        if (lane == 0) {
-          for (int q = 0; q < nq; ++q) {
-            issue_qk(q, 0);
-            umma_commit(&sfull[q]);
-          }
-          umma_commit(&empty[0]);
-        }
-        issued = true;
-      }
-      int sv = 1 % S;             // stage of V_j; K_{j+1} follows
-      uint32_t pv = S == 1 ? 1u : 0u;
-      for (int j = 0; j < nt && ok; ++j) {
-        int sk = sv + 1;
-        uint32_t pk = pv;
-        if (sk == S) {
-          sk = 0;
-          pk ^= 1u;
-        }
-        ok = __all_sync(kFull, mbar_wait(&full[sv], pv, ctl, P.status));
-        if (!ok) break;
-        const int live = blk.kv_len - (t_lo + j) * kTileKeys;  // keys of this tile that exist
-        if (live < kTileKeys) {
-          // V rows behind the last slot may hold NaN, and 0 * NaN is NaN
-          uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
-          for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
-            rows[i] = make_uint4(0, 0, 0, 0);
-            rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        const bool more = j + 1 < nt;
-        for (int q = 0; q < nq; ++q) {
-          ok = __all_sync(kFull, mbar_wait(&pfull[q], (uint32_t)(j & 1), ctl, P.status));
+  // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
+  // issuer, two idle warps) gives them its registers: 40 + 216 = 2 * 128 a
+  // thread for one tile, 40 + 2 * 232 = 3 * 168 for two.
+  if (warp >= NQ * 4) {
+    regs_dec<40>();
+    if (warp == kProducer) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0 && nt > 0) {
+        const uint64_t pol = policy_evict_normal();
+        const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
+        mbar_expect_tx(qfull, (uint32_t)nq * 2 * qbytes);
+        for (int q = 0; q < nq; ++q)
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
+                        (int)(blk.row0 + q * P.tpt), qfull, pol);
+        const int z = blk.b * P.kv_heads + blk.h;
+        int st = 0, g = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int i = 0; i < 2 * nt; ++i, ++g) {
+          if (g >= S) ok = mbar_wait(&empty[st], ph ^ 1u, ctl, P.status);
           if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) issue_pv(q, sv, j > 0);
-          if (more) {
-            if (q == 0) ok = __all_sync(kFull, mbar_wait(&full[sk], pk, ctl, P.status));
-            if (!ok) break;
-            if (lane == 0) {
-              issue_qk(q, sk);
-              umma_commit(&sfull[q]);
+          mbar_expect_tx(&full[st], kTileBytes);
+          const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
+          const CUtensorMap* map = (i & 1) ? &P.vmap : &P.kmap;
+          const int y = (t_lo + (i >> 1)) * kTileKeys;
+          tma_load_3d(dst, map, 0, y, z, &full[st], pol);
+          tma_load_3d(dst + kSlabBytes, map, 64, y, z, &full[st], pol);
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) {  // after an abort, loads already issued must land before the CTA exits
+          long long t0 = clock64();
+          while (!mbar_test(qfull, 0u) && clock64() - t0 < kWaitCycles) {
+          }
+          for (int s = 0; s < S && s < g; ++s) {
+            const int last = g - 1 - ((g - 1 - s) % S);
+            t0 = clock64();
+            while (!mbar_test(&full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
             }
           }
         }
-        if (!ok) break;
-        if (lane == 0) {
-          umma_commit(&empty[sv]);
-          if (more) umma_commit(&empty[sk]);
-          else umma_commit(ofull);
-        }
-        sv = sk + 1;
-        pv = pk;
-        if (sv == S) {
-          sv = 0;
-          pv ^= 1u;
-        }
       }
-      if (!ok && issued && lane == 0) {
-        // after an abort, let the MMAs already issued finish before the TMEM is freed
-        umma_commit(ofull);
-        const long long t0 = clock64();
-        while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
+    } else if (warp == kIssuer) {
+      // ------------------------------------------------------------ MMA issuer
+      if (nt > 0) {
+        const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
+        constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
+        auto issue_qk = [&](int q, int st) {
+          const uint32_t kb = rb + (uint32_t)st * kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (uint32_t)(kk & 3) * 32;
+            umma_bf16(tmem + (uint32_t)q * 256, sw128_desc(qb + (uint32_t)(2 * q + (kk >> 2)) * lay.slab_q + off),
+                      sw128_desc(kb + (uint32_t)(kk >> 2) * kSlabBytes + off), id_qk, kk ? 1u : 0u);
+          }
+        };
+        auto issue_pv = [&](int q, int st, int half, bool acc) {
+          const uint32_t vb = rb + (uint32_t)st * kTileBytes;
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            umma_bf16_ts(tmem + (uint32_t)q * 256 + 128, tmem + (uint32_t)q * 256 + (uint32_t)kk * 8,
+                         sw128_mn_desc(vb + (uint32_t)kk * 2048), id_pv, (acc || kk) ? 1u : 0u);
+        };
+        bool ok = __all_sync(kFull, mbar_wait(qfull, 0u, ctl, P.status));
+        ok = ok && __all_sync(kFull, mbar_wait(&full[0], 0u, ctl, P.status));
+        bool issued = false;
+        if (ok) {
+          tc_fence_after();
+          if (lane == 0) {
+            for (int q = 0; q < nq; ++q) {
+              issue_qk(q, 0);
+              umma_commit(&sfull[q]);
+            }
+            umma_commit(&empty[0]);
+          }
+          issued = true;
         }
+        int sv = 1 % S;             // stage of V_j; K_{j+1} follows
+        uint32_t pv = S == 1 ? 1u : 0u;
+        for (int j = 0; j < nt && ok; ++j) {
+          int sk = sv + 1;
+          uint32_t pk = pv;
+          if (sk == S) {
+            sk = 0;
+            pk ^= 1u;
+          }
+          ok = __all_sync(kFull, mbar_wait(&full[sv], pv, ctl, P.status));
+          if (!ok) break;
+          const int live = blk.kv_len - (t_lo + j) * kTileKeys;  // keys of this tile that exist
+          if (live < kTileKeys) {
+            // V rows behind the last slot may hold NaN, and 0 * NaN is NaN
+            uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
+            for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
+              rows[i] = make_uint4(0, 0, 0, 0);
+              rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          const bool more = j + 1 < nt;
+          for (int q = 0; q < nq; ++q) {
+            for (int k = 0; k < 2 && ok; ++k) {
+              ok = __all_sync(kFull, mbar_wait(&pfull[2 * q + k], (uint32_t)(j & 1), ctl, P.status));
+              if (!ok) break;
+              tc_fence_after();
+              if (lane == 0) issue_pv(q, sv, k, j > 0 || k > 0);
+            }
+            if (!ok) break;
+            if (more) {
+              if (q == 0) ok = __all_sync(kFull, mbar_wait(&full[sk], pk, ctl, P.status));
+              if (!ok) break;
+              if (lane == 0) {
+                issue_qk(q, sk);
+                umma_commit(&sfull[q]);
+              }
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            umma_commit(&empty[sv]);
+            if (more) umma_commit(&empty[sk]);
+            else umma_commit(ofull);
+          }
+          sv = sk + 1;
+          pv = pk;
+          if (sv == S) {
+            sv = 0;
+            pv ^= 1u;
+          }
+        }
+        if (!ok && issued && lane == 0) {
+          // after an abort, let the MMAs already issued finish before the TMEM is freed
+          umma_commit(ofull);
+          const long long t0 = clock64();
+          while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
+          }
+        }
+        __syncwarp();
       }
+    }
+    if (splits > 1) {  // the joins' two barriers, see below
       __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
   } else {
     // ------------------------------------------------------------ softmax
+    regs_inc<NQ == 1 ? 216 : 232>();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int rows = q < nq ? rows_of(q) : 0;
@@ -473,26 +516,30 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           m = m_new;
         }
         const float off = m == kNegInf ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2), off2 = pack2(off, off);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c = 2 * half + (i >> 4), e = (i & 15) * 2;
-            const float a = fast_exp2(fmaf(v[c][e], P.scale_log2, off));
-            const float b = fast_exp2(fmaf(v[c][e + 1], P.scale_log2, off));
-            sum[(i & 1) * 2] += a;
-            sum[(i & 1) * 2 + 1] += b;
+            float a, b;
+            unpack2(fma2(pack2(v[c][e], v[c][e + 1]), scale2, off2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[i & 1] = add2(sum[i & 1], pack2(a, b));
             p[i] = pack_bf16(a, b);
           }
           tmem_st32(t_s + (uint32_t)half * 32, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * q + half]);  // the first 64 keys' PV may start
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[q]);
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       if (ok && nt > 0) {
         ok = __all_sync(kFull, mbar_wait(ofull, 0u, ctl, P.status));
@@ -544,61 +591,60 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         }
       }
     }
-  }
-
-  if (splits > 1) {
-    // ------------------------------------------------------------ join
-    __syncwarp();
-    cluster_sync();
-    if (!ctl->abort) {
-      const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
-      for (int q = 0; q < nq; ++q) {
-        const int rows = rows_of(q);
-        // rank r joins rows r, r + splits, ...; one warp per row, 4 columns per lane
-        for (int row = rank + warp * splits; row < rows; row += splits * (NQ * 4 + 2)) {
-          float mc = kNegInf, lc = 0.f;
-          if (lane < splits) {
-            const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(q * 128 + row) * 8, (uint32_t)lane));
-            mc = x.x;
-            lc = x.y;
-          }
-          float M = mc;
+    if (splits > 1) {
+      // ---------------------------------------------------------- join
+      __syncwarp();
+      cluster_sync();
+      if (!ctl->abort) {
+        const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
+        for (int q = 0; q < nq; ++q) {
+          const int rows = rows_of(q);
+          // rank r joins rows r, r + splits, ...; one warp per row, 4 columns per lane
+          for (int row = rank + warp * splits; row < rows; row += splits * NQ * 4) {
+            float mc = kNegInf, lc = 0.f;
+            if (lane < splits) {
+              const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(q * 128 + row) * 8, (uint32_t)lane));
+              mc = x.x;
+              lc = x.y;
+            }
+            float M = mc;
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-          // a share without a visible key has no part in the sums (its O is not written or zero)
-          const float w = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
-          float l = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = 0; c < splits; ++c) {
-            const float wc = __shfl_sync(kFull, w, c), lcc = __shfl_sync(kFull, lc, c);
-            if (wc == 0.f) continue;
-            l = fmaf(wc, lcc, l);
-            const float4 x = ld_cluster4(
-                map_rank(part + ((uint32_t)(q * 128 + row) * 32 + (uint32_t)(lane ^ (row & 31))) * 16, (uint32_t)c));
-            o.x = fmaf(wc, x.x, o.x);
-            o.y = fmaf(wc, x.y, o.y);
-            o.z = fmaf(wc, x.z, o.z);
-            o.w = fmaf(wc, x.w, o.w);
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+            // a share without a visible key has no part in the sums (its O is not written or zero)
+            const float w = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
+            float l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < splits; ++c) {
+              const float wc = __shfl_sync(kFull, w, c), lcc = __shfl_sync(kFull, lc, c);
+              if (wc == 0.f) continue;
+              l = fmaf(wc, lcc, l);
+              const float4 x = ld_cluster4(
+                  map_rank(part + ((uint32_t)(q * 128 + row) * 32 + (uint32_t)(lane ^ (row & 31))) * 16, (uint32_t)c));
+              o.x = fmaf(wc, x.x, o.x);
+              o.y = fmaf(wc, x.y, o.y);
+              o.z = fmaf(wc, x.z, o.z);
+              o.w = fmaf(wc, x.w, o.w);
+            }
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            o.x *= inv;
+            o.y *= inv;
+            o.z *= inv;
+            o.w *= inv;
+            const int tok = q * P.tpt + row / P.group;
+            const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + row % P.group;
+            if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
+            reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            const float lse = l > 0.f ? (M + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
+            if (P.lse && lane == 0) P.lse[orow] = lse;
+            const float check = (o.x + o.y + o.z + o.w) * 0.f;
+            if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
           }
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-          o.x *= inv;
-          o.y *= inv;
-          o.z *= inv;
-          o.w *= inv;
-          const int tok = q * P.tpt + row / P.group;
-          const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + row % P.group;
-          if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
-          reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-          const float lse = l > 0.f ? (M + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
-          if (P.lse && lane == 0) P.lse[orow] = lse;
-          const float check = (o.x + o.y + o.z + o.w) * 0.f;
-          if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
         }
       }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another still reads its partial results
     }
-    cluster_sync();  // no CTA leaves while another still reads its partial results
   }
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -653,7 +699,7 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * splits));
-  cfg.blockDim = dim3((unsigned)(nq * 128 + 64));
+  cfg.blockDim = dim3((unsigned)(nq * 128 + 128));
   cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
