@@ -50,13 +50,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
-// A (the 128 x 16 bf16 probabilities) from TMEM, two elements per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// One MMA of 16 along K. Shared-memory descriptors travel as their low words
+// plus a constant step added here: made in the loop they stay out of registers
+// (hoisted, the descriptors of a product spilled the issuer's).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // SBO, version, SWIZZLE_128B
+template <uint32_t kAStep, uint32_t kBStep>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 p, %4, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n"
+      " mov.b64 a, {x, %7};\n mov.b64 b, {y, %7};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi));
+}
+// A (the 128 x 16 bf16 probabilities) from TMEM, two elements per 32-bit column.
+template <uint32_t kAStep, uint32_t kBStep>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " setp.ne.b32 p, %4, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n mov.b64 b, {y, %7};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -70,12 +84,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// B operand V [keys][d], d contiguous: MN-major SWIZZLE_128B. One atom is 64 d
-// x 8 keys (8 rows of 128 bytes); the next 8 keys follow 1024 bytes on (SBO),
-// the next 64 d one slab on (LBO).
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kSlabBytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Low words. Q and K [row][d], d contiguous: K-major SWIZZLE_128B (sw128_desc).
+// V [keys][d] as B operand: MN-major SWIZZLE_128B; one atom is 64 d x 8 keys (8
+// rows of 128 bytes), the next 8 keys follow 1024 bytes on (SBO), the next 64 d
+// one slab on (LBO).
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(kSlabBytes >> 4) << 16);
 }
 constexpr uint32_t kIdescBMn = 1u << 16;  // instruction descriptor: B is MN-major
 
@@ -296,9 +311,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 
   // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
   // issuer, two idle warps) gives them its registers: 40 + 216 = 2 * 128 a
-  // thread for one tile, 40 + 2 * 232 = 3 * 168 for two.
+  // thread for one tile, 56 + 2 * 224 = 3 * 168 for two.
   if (warp >= NQ * 4) {
-    regs_dec<40>();
+    regs_dec<NQ == 1 ? 40 : 56>();
     if (warp == kProducer) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0 && nt > 0) {
@@ -341,110 +356,137 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       }
     } else if (warp == kIssuer) {
       // ------------------------------------------------------------ MMA issuer
+      // One lane issues. The tensor core takes few MMAs ahead, so whatever lies
+      // between two of them shows up as idle time: the waits on K and V stages sit
+      // in the middle of a product whose MMAs are queued, and only the waits for
+      // probabilities stand between two products.
       if (nt > 0) {
-        const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
         constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
-        auto issue_qk = [&](int q, int st) {
-          const uint32_t kb = rb + (uint32_t)st * kTileBytes;
+        const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
+        const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
+        // the two 64-column halves of a logit product
+        auto issue_qk = [&](int q, int st, int half) {
+          const uint32_t d = tmem + (uint32_t)q * 256;
+          const uint32_t a = qd + (uint32_t)(2 * q + half) * slab_step;
+          const uint32_t b = kd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)half * (kSlabBytes >> 4);
+          umma_ss<0, 0>(d, a, b, id_qk, (uint32_t)half);
+          umma_ss<2, 2>(d, a, b, id_qk, 1u);
+          umma_ss<4, 4>(d, a, b, id_qk, 1u);
+          umma_ss<6, 6>(d, a, b, id_qk, 1u);
+        };
+        // 32 keys of a PV product
+        auto issue_pv = [&](int q, int st, int quarter, uint32_t acc) {
+          const uint32_t s = tmem + (uint32_t)q * 256, p = s + (uint32_t)quarter * 16;
+          const uint32_t b = vd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)quarter * 256;
+          umma_ts<0, 0>(s + 128, p, b, id_pv, acc);
+          umma_ts<8, 128>(s + 128, p, b, id_pv, 1u);
+        };
+        bool ok = true, issued = false;
+        int sv = 1 % S;  // stage of V_j; K_{j+1} follows
+        uint32_t pv = S == 1 ? 1u : 0u;
+        if (lane == 0) {
+          ok = mbar_wait(qfull, 0u, ctl, P.status) && mbar_wait(&full[0], 0u, ctl, P.status);
+          if (ok) {
+            tc_fence_after();
+            issued = true;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (uint32_t)(kk & 3) * 32;
-            umma_bf16(tmem + (uint32_t)q * 256, sw128_desc(qb + (uint32_t)(2 * q + (kk >> 2)) * lay.slab_q + off),
-                      sw128_desc(kb + (uint32_t)(kk >> 2) * kSlabBytes + off), id_qk, kk ? 1u : 0u);
+            for (int q = 0; q < NQ; ++q)
+              if (q < nq) {
+                issue_qk(q, 0, 0);
+                issue_qk(q, 0, 1);
+                umma_commit(&sfull[q]);
+              }
+            umma_commit(&empty[0]);
+            ok = mbar_wait(&full[sv], pv, ctl, P.status);
           }
-        };
-        auto issue_pv = [&](int q, int st, int half, bool acc) {
-          const uint32_t vb = rb + (uint32_t)st * kTileBytes;
+          for (int j = 0; j + 1 < nt && ok; ++j) {
+            int sk = sv + 1;  // stages of K_{j+1} and V_{j+1}
+            uint32_t pk = pv;
+            if (sk == S) {
+              sk = 0;
+              pk ^= 1u;
+            }
+            int sn = sk + 1;
+            uint32_t pn = pk;
+            if (sn == S) {
+              sn = 0;
+              pn ^= 1u;
+            }
+            const uint32_t par = (uint32_t)(j & 1);
 #pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            umma_bf16_ts(tmem + (uint32_t)q * 256 + 128, tmem + (uint32_t)q * 256 + (uint32_t)kk * 8,
-                         sw128_mn_desc(vb + (uint32_t)kk * 2048), id_pv, (acc || kk) ? 1u : 0u);
-        };
-        bool ok = __all_sync(kFull, mbar_wait(qfull, 0u, ctl, P.status));
-        ok = ok && __all_sync(kFull, mbar_wait(&full[0], 0u, ctl, P.status));
-        bool issued = false;
-        if (ok) {
-          tc_fence_after();
-          if (lane == 0) {
-            for (int q = 0; q < nq; ++q) {
-              issue_qk(q, 0);
+            for (int q = 0; q < NQ; ++q) {
+              if (q >= nq || !ok) break;
+              ok = mbar_wait(&pfull[2 * q], par, ctl, P.status);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(q, sv, 0, j > 0 ? 1u : 0u);
+              issue_pv(q, sv, 1, 1u);
+              ok = mbar_wait(&pfull[2 * q + 1], par, ctl, P.status);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(q, sv, 2, 1u);
+              if (q == 0) ok = mbar_wait(&full[sk], pk, ctl, P.status);
+              issue_pv(q, sv, 3, 1u);
+              if (q == nq - 1) umma_commit(&empty[sv]);
+              if (!ok) break;
+              issue_qk(q, sk, 0);
+              if (q == nq - 1) ok = mbar_wait(&full[sn], pn, ctl, P.status);
+              issue_qk(q, sk, 1);
               umma_commit(&sfull[q]);
             }
-            umma_commit(&empty[0]);
+            umma_commit(&empty[sk]);
+            sv = sn;
+            pv = pn;
           }
-          issued = true;
         }
-        int sv = 1 % S;             // stage of V_j; K_{j+1} follows
-        uint32_t pv = S == 1 ? 1u : 0u;
-        for (int j = 0; j < nt && ok; ++j) {
-          int sk = sv + 1;
-          uint32_t pk = pv;
-          if (sk == S) {
-            sk = 0;
-            pk ^= 1u;
-          }
+        __syncwarp();
+        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+        issued = __shfl_sync(kFull, issued ? 1 : 0, 0) != 0;
+        sv = __shfl_sync(kFull, sv, 0);
+        pv = __shfl_sync(kFull, pv, 0);
+        // the last tile: V rows behind the last slot may hold NaN, and 0 * NaN is NaN
+        const int live = blk.kv_len - (t_hi - 1) * kTileKeys;
+        if (ok && live < kTileKeys) {
           ok = __all_sync(kFull, mbar_wait(&full[sv], pv, ctl, P.status));
-          if (!ok) break;
-          const int live = blk.kv_len - (t_lo + j) * kTileKeys;  // keys of this tile that exist
-          if (live < kTileKeys) {
-            // V rows behind the last slot may hold NaN, and 0 * NaN is NaN
+          if (ok) {
             uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
             for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
               rows[i] = make_uint4(0, 0, 0, 0);
               rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
           }
-          const bool more = j + 1 < nt;
-          for (int q = 0; q < nq; ++q) {
-            for (int k = 0; k < 2 && ok; ++k) {
-              ok = __all_sync(kFull, mbar_wait(&pfull[2 * q + k], (uint32_t)(j & 1), ctl, P.status));
-              if (!ok) break;
-              tc_fence_after();
-              if (lane == 0) issue_pv(q, sv, k, j > 0 || k > 0);
-            }
-            if (!ok) break;
-            if (more) {
-              if (q == 0) ok = __all_sync(kFull, mbar_wait(&full[sk], pk, ctl, P.status));
-              if (!ok) break;
-              if (lane == 0) {
-                issue_qk(q, sk);
-                umma_commit(&sfull[q]);
-              }
-            }
-          }
-          if (!ok) break;
-          if (lane == 0) {
-            umma_commit(&empty[sv]);
-            if (more) umma_commit(&empty[sk]);
-            else umma_commit(ofull);
-          }
-          sv = sk + 1;
-          pv = pk;
-          if (sv == S) {
-            sv = 0;
-            pv ^= 1u;
-          }
+          __syncwarp();
         }
-        if (!ok && issued && lane == 0) {
-          // after an abort, let the MMAs already issued finish before the TMEM is freed
-          umma_commit(ofull);
-          const long long t0 = clock64();
-          while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 2 * NQ; ++i) {
+            if (i >= 2 * nq || !ok) break;
+            ok = mbar_wait(&pfull[i], (uint32_t)((nt - 1) & 1), ctl, P.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(i >> 1, sv, 2 * (i & 1), (i & 1) || nt > 1 ? 1u : 0u);
+            issue_pv(i >> 1, sv, 2 * (i & 1) + 1, 1u);
+          }
+          if (ok || issued) umma_commit(ofull);
+          if (!ok && issued) {
+            // after an abort, let the MMAs already issued finish before the TMEM is freed
+            const long long t0 = clock64();
+            while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
+            }
           }
         }
         __syncwarp();
       }
     }
-    if (splits > 1) {  // the joins' two barriers, see below
+  if (splits > 1) {  // the joins' two barriers, see below
       __syncwarp();
       cluster_sync();
       cluster_sync();
     }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<NQ == 1 ? 216 : 232>();
+    regs_inc<NQ == 1 ? 216 : 224>();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int rows = q < nq ? rows_of(q) : 0;
