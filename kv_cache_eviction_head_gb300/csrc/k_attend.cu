@@ -50,27 +50,45 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
-// One MMA of 16 along K. Shared-memory descriptors travel as their low words
-// plus a constant step added here: made in the loop they stay out of registers
-// (hoisted, the descriptors of a product spilled the issuer's).
+// One lane of the warp, the same one every time (elect.sync).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e;
+}
+// One MMA of 16 along K, issued by the lane with `elected` set. The whole warp
+// runs these, with warp-uniform operands: under a branch on the lane the
+// operands take vector registers and a detour to the uniform ones, and the
+// issuer falls behind the tensor core whenever the softmax warps are busy.
+// Shared-memory descriptors travel as their low words plus a constant step.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // SBO, version, SWIZZLE_128B
 template <uint32_t kAStep, uint32_t kBStep>
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t elected) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
-      " setp.ne.b32 p, %4, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n"
+      "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %8, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n"
       " mov.b64 a, {x, %7};\n mov.b64 b, {y, %7};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi));
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi), "r"(elected));
 }
 // A (the 128 x 16 bf16 probabilities) from TMEM, two elements per 32-bit column.
 template <uint32_t kAStep, uint32_t kBStep>
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 b;\n"
-      " setp.ne.b32 p, %4, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n mov.b64 b, {y, %7};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi));
+      "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %8, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n"
+      " mov.b64 b, {y, %7};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi), "r"(elected));
+}
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -307,7 +325,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);
 
   // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
   // issuer, two idle warps) gives them its registers: 40 + 216 = 2 * 128 a
@@ -356,7 +374,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       }
     } else if (warp == kIssuer) {
       // ------------------------------------------------------------ MMA issuer
-      // One lane issues. The tensor core takes few MMAs ahead, so whatever lies
+      // The tensor core takes few MMAs ahead, so whatever lies
       // between two of them shows up as idle time: the waits on K and V stages sit
       // in the middle of a product whose MMAs are queued, and only the waits for
       // probabilities stand between two products.
@@ -364,116 +382,108 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
         const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
         const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
+        const uint32_t el = elect_one();
         // the two 64-column halves of a logit product
         auto issue_qk = [&](int q, int st, int half) {
           const uint32_t d = tmem + (uint32_t)q * 256;
           const uint32_t a = qd + (uint32_t)(2 * q + half) * slab_step;
           const uint32_t b = kd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)half * (kSlabBytes >> 4);
-          umma_ss<0, 0>(d, a, b, id_qk, (uint32_t)half);
-          umma_ss<2, 2>(d, a, b, id_qk, 1u);
-          umma_ss<4, 4>(d, a, b, id_qk, 1u);
-          umma_ss<6, 6>(d, a, b, id_qk, 1u);
+          umma_ss<0, 0>(d, a, b, id_qk, (uint32_t)half, el);
+          umma_ss<2, 2>(d, a, b, id_qk, 1u, el);
+          umma_ss<4, 4>(d, a, b, id_qk, 1u, el);
+          umma_ss<6, 6>(d, a, b, id_qk, 1u, el);
         };
         // 32 keys of a PV product
         auto issue_pv = [&](int q, int st, int quarter, uint32_t acc) {
           const uint32_t s = tmem + (uint32_t)q * 256, p = s + (uint32_t)quarter * 16;
           const uint32_t b = vd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)quarter * 256;
-          umma_ts<0, 0>(s + 128, p, b, id_pv, acc);
-          umma_ts<8, 128>(s + 128, p, b, id_pv, 1u);
+          umma_ts<0, 0>(s + 128, p, b, id_pv, acc, el);
+          umma_ts<8, 128>(s + 128, p, b, id_pv, 1u, el);
         };
-        bool ok = true, issued = false;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          return __all_sync(kFull, mbar_wait(bar, parity, ctl, P.status));
+        };
+        bool issued = false;
         int sv = 1 % S;  // stage of V_j; K_{j+1} follows
         uint32_t pv = S == 1 ? 1u : 0u;
-        if (lane == 0) {
-          ok = mbar_wait(qfull, 0u, ctl, P.status) && mbar_wait(&full[0], 0u, ctl, P.status);
-          if (ok) {
-            tc_fence_after();
-            issued = true;
+        bool ok = wait(qfull, 0u) && wait(&full[0], 0u);
+        if (ok) {
+          tc_fence_after();
+          issued = true;
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
-              if (q < nq) {
-                issue_qk(q, 0, 0);
-                issue_qk(q, 0, 1);
-                umma_commit(&sfull[q]);
-              }
-            umma_commit(&empty[0]);
-            ok = mbar_wait(&full[sv], pv, ctl, P.status);
-          }
-          for (int j = 0; j + 1 < nt && ok; ++j) {
-            int sk = sv + 1;  // stages of K_{j+1} and V_{j+1}
-            uint32_t pk = pv;
-            if (sk == S) {
-              sk = 0;
-              pk ^= 1u;
+          for (int q = 0; q < NQ; ++q)
+            if (q < nq) {
+              issue_qk(q, 0, 0);
+              issue_qk(q, 0, 1);
+              umma_commit_if(&sfull[q], el);
             }
-            int sn = sk + 1;
-            uint32_t pn = pk;
-            if (sn == S) {
-              sn = 0;
-              pn ^= 1u;
-            }
-            const uint32_t par = (uint32_t)(j & 1);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              if (q >= nq || !ok) break;
-              ok = mbar_wait(&pfull[2 * q], par, ctl, P.status);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(q, sv, 0, j > 0 ? 1u : 0u);
-              issue_pv(q, sv, 1, 1u);
-              ok = mbar_wait(&pfull[2 * q + 1], par, ctl, P.status);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(q, sv, 2, 1u);
-              if (q == 0) ok = mbar_wait(&full[sk], pk, ctl, P.status);
-              issue_pv(q, sv, 3, 1u);
-              if (q == nq - 1) umma_commit(&empty[sv]);
-              if (!ok) break;
-              issue_qk(q, sk, 0);
-              if (q == nq - 1) ok = mbar_wait(&full[sn], pn, ctl, P.status);
-              issue_qk(q, sk, 1);
-              umma_commit(&sfull[q]);
-            }
-            umma_commit(&empty[sk]);
-            sv = sn;
-            pv = pn;
-          }
+          umma_commit_if(&empty[0], el);
+          ok = wait(&full[sv], pv);
         }
-        __syncwarp();
-        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-        issued = __shfl_sync(kFull, issued ? 1 : 0, 0) != 0;
-        sv = __shfl_sync(kFull, sv, 0);
-        pv = __shfl_sync(kFull, pv, 0);
+        for (int j = 0; j + 1 < nt && ok; ++j) {
+          int sk = sv + 1;  // stages of K_{j+1} and V_{j+1}
+          uint32_t pk = pv;
+          if (sk == S) {
+            sk = 0;
+            pk ^= 1u;
+          }
+          int sn = sk + 1;
+          uint32_t pn = pk;
+          if (sn == S) {
+            sn = 0;
+            pn ^= 1u;
+          }
+          const uint32_t par = (uint32_t)(j & 1);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (q >= nq || !ok) break;
+            ok = wait(&pfull[2 * q], par);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(q, sv, 0, j > 0 ? 1u : 0u);
+            issue_pv(q, sv, 1, 1u);
+            ok = wait(&pfull[2 * q + 1], par);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(q, sv, 2, 1u);
+            if (q == 0) ok = wait(&full[sk], pk);
+            issue_pv(q, sv, 3, 1u);
+            if (q == nq - 1) umma_commit_if(&empty[sv], el);
+            if (!ok) break;
+            issue_qk(q, sk, 0);
+            if (q == nq - 1) ok = wait(&full[sn], pn);
+            issue_qk(q, sk, 1);
+            umma_commit_if(&sfull[q], el);
+          }
+          umma_commit_if(&empty[sk], el);
+          sv = sn;
+          pv = pn;
+        }
         // the last tile: V rows behind the last slot may hold NaN, and 0 * NaN is NaN
         const int live = blk.kv_len - (t_hi - 1) * kTileKeys;
         if (ok && live < kTileKeys) {
-          ok = __all_sync(kFull, mbar_wait(&full[sv], pv, ctl, P.status));
-          if (ok) {
-            uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
-            for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
-              rows[i] = make_uint4(0, 0, 0, 0);
-              rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
+          for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
+            rows[i] = make_uint4(0, 0, 0, 0);
+            rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        if (lane == 0) {
 #pragma unroll
-          for (int i = 0; i < 2 * NQ; ++i) {
-            if (i >= 2 * nq || !ok) break;
-            ok = mbar_wait(&pfull[i], (uint32_t)((nt - 1) & 1), ctl, P.status);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(i >> 1, sv, 2 * (i & 1), (i & 1) || nt > 1 ? 1u : 0u);
-            issue_pv(i >> 1, sv, 2 * (i & 1) + 1, 1u);
-          }
-          if (ok || issued) umma_commit(ofull);
-          if (!ok && issued) {
-            // after an abort, let the MMAs already issued finish before the TMEM is freed
-            const long long t0 = clock64();
-            while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
-            }
+        for (int i = 0; i < 2 * NQ; ++i) {
+          if (i >= 2 * nq || !ok) break;
+          ok = wait(&pfull[i], (uint32_t)((nt - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(i >> 1, sv, 2 * (i & 1), (i & 1) || nt > 1 ? 1u : 0u);
+          issue_pv(i >> 1, sv, 2 * (i & 1) + 1, 1u);
+        }
+        if (issued) umma_commit_if(ofull, el);
+        if (!ok && issued) {
+          // after an abort, let the MMAs already issued finish before the TMEM is freed
+          const long long t0 = clock64();
+          while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
           }
         }
         __syncwarp();
