@@ -31,6 +31,8 @@ struct AttendParams {
 // nq: 128-row tiles per CTA (1 or 2); splits: CTAs per row block (1..16, a
 // cluster), each taking a share of the keys; items: row blocks to launch.
 cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s);
+// K/V ring stages that fit beside the rest of a CTA's shared memory.
+int attend_stages(int nq, int group, int tpt);
 // Fills p's tensor maps (host only). False on failure.
 bool encode_attend_maps(AttendParams& p, const void* q, int64_t q_stride, const void* K, const void* V);
 

@@ -41,15 +41,6 @@ bkv_status zero_status(uint32_t* status, cudaStream_t s) {
 constexpr int kSlots1 = 2 * 152;  // CTAs of one tile that GB300 holds at once (two per SM)
 constexpr int kSlots2 = 152;      // CTAs of two tiles
 
-// Ring stages: two CTAs of one tile share an SM's 228 KB; fewer than two would
-// fit three there, and three ask for more TMEM columns (256 each) than it has.
-int stages_for(int nq, int group, int tpt) {
-  const int q = nq * 2 * ((group * tpt + 7) / 8) * 1024;
-  const int room = (nq == 1 ? 113 : 227) * 1024 - 1280 - q;
-  const int n = room / (32 * 1024);
-  return n < 6 ? n : 6;
-}
-
 }  // namespace
 
 extern "C" {
@@ -130,7 +121,7 @@ bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_str
   const int nq = items_of(2) > kSlots2 / 2 && p.tpt < total ? 2 : 1;
   const int64_t items = items_of(nq);
   if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
-  p.stages = stages_for(nq, p.group, p.tpt);
+  p.stages = bkv::attend_stages(nq, p.group, p.tpt);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (total > 0 && !bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
@@ -174,7 +165,7 @@ bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_strid
   const int slots = nq == 1 ? kSlots1 : kSlots2, tiles = (c.max_cache + 127) / 128;
   int splits = 1;
   while (splits < 16 && items * splits * 2 <= slots && splits * 2 <= tiles) splits *= 2;
-  p.stages = stages_for(nq, p.group, p.tpt);
+  p.stages = bkv::attend_stages(nq, p.group, p.tpt);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (!bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;

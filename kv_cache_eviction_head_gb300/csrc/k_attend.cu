@@ -100,7 +100,31 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A value that tcgen05.ld delivers is there only after the wait: this ties the
+// registers to what precedes it, so that no use moves in front of the wait.
+__device__ __forceinline__ void pin(float (&v)[32]) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                    "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                    "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
 
 // Low words. Q and K [row][d], d contiguous: K-major SWIZZLE_128B (sw128_desc).
 // V [keys][d] as B operand: MN-major SWIZZLE_128B; one atom is 64 d x 8 keys (8
@@ -135,6 +159,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// Takes a block of this grid that has not started (its work is then this CTA's):
+// 16 bytes that say which arrive in shared memory.
+__device__ __forceinline__ void take_block(void* result, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(result)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The block taken, or -1: none is left.
+__device__ __forceinline__ int64_t taken_block(const void* result) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z, w;\n .reg .b64 lo, hi;\n"
+      " ld.shared.v2.b64 {lo, hi}, [%2];\n mov.b128 r, {lo, hi};\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.b32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(result))
+      : "memory");
+  return got ? (int64_t)x : -1;
 }
 template <int N>
 __device__ __forceinline__ void regs_dec() {
@@ -253,71 +298,91 @@ __device__ __forceinline__ Block find_tree_block(const AttendParams& P, int64_t 
   return k;
 }
 
+constexpr int kMaxStages = 6;
+constexpr int kWarpOut = 32 * 128;  // staging of a warp's output rows, one 64-column half at a time
+
+// What a row block needs in shared memory, handed from the scheduler to the other warps.
+struct Work {
+  Block blk;      // blk.cnt = 0: no more work
+  int t_lo, nt;   // this CTA's key tiles
+};
+
+struct Control {
+  uint64_t full[kMaxStages], empty[kMaxStages];  // K/V ring
+  uint64_t qfull, qempty;
+  uint64_t sfull[2];      // a tile's logits are in TMEM (and its PV before is done)
+  uint64_t pfull[2][2];   // half of its probabilities are
+  uint64_t ofull[2], ofree[2];  // O is complete; O has been read
+  uint64_t wfull[2], wempty[2];  // work slots
+  uint64_t want, taken;   // the producer runs out of work; a block has been taken
+  uint64_t drain;         // after an abort
+  uint4 block;            // its name
+  Work work[2];
+  Ctl ctl;
+};
+
 struct Smem {
-  uint32_t slab_q, q, ring, bars, total;
+  uint32_t slab_q, q, ring, out, control, total;
 };
 // The ring starts behind the rows in use; an MMA reads 128 rows of Q whatever
 // their number, the rest of them from the ring: rows nobody looks at.
 __host__ __device__ inline Smem attend_smem(int nq, int group, int tpt, int stages) {
   Smem s;
-  s.slab_q = (uint32_t)((group * tpt + 7) / 8) * 1024;
+  const int rows = group * tpt;
+  s.slab_q = (uint32_t)((rows + 7) / 8) * 1024;
   s.q = 0;
   s.ring = s.q + (uint32_t)nq * 2 * s.slab_q;
-  s.bars = s.ring + (uint32_t)stages * kTileBytes;
-  s.total = s.bars + 256 + 1024;  // barriers, and 1 KB to align the base
+  s.out = s.ring + (uint32_t)stages * kTileBytes;
+  s.control = s.out + (uint32_t)(nq * ((rows + 31) / 32)) * kWarpOut;
+  s.total = s.control + (uint32_t)((sizeof(Control) + 15) / 16 * 16);
   return s;
 }
-
-constexpr int kMaxStages = 6;
 
 template <int NQ>
 __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
 attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int kProducer = NQ * 4, kIssuer = NQ * 4 + 1;
+  extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles: 1 KB aligned
+  if (smem_u32(smem) & 1023u) {
+    latch(P.status, BKV_ERR_INTERNAL);
+    return;
+  }
+  constexpr int kSoftmaxWarps = NQ * 4;
+  constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kScheduler = kSoftmaxWarps + 2;
   constexpr uint32_t kCols = NQ * 256;  // per tile: 128 columns of S (and P), 128 of O
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % (unsigned)splits);
-  const int64_t item = blockIdx.x / (unsigned)splits;
   const int tpi = NQ * P.tpt;
-  const Block blk = P.cu ? find_prompt_block(P, item, tpi) : find_tree_block(P, item, tpi);
-  if (blk.bad && tid == 0) latch(P.status, BKV_ERR_INVALID_ARG);
-  if (blk.cnt <= 0) return;  // the whole cluster: all its CTAs have the same item
 
   const Smem lay = attend_smem(NQ, P.group, P.tpt, P.stages);
   unsigned char* q_s = smem + lay.q;
   unsigned char* ring = smem + lay.ring;
   float2* ml = reinterpret_cast<float2*>(q_s);  // [NQ * 128] partial maximum and sum, once Q is done with
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
-  uint64_t* full = bars;                      // [stages]
-  uint64_t* empty = bars + kMaxStages;        // [stages]
-  uint64_t* qfull = bars + 2 * kMaxStages;
-  uint64_t* sfull = qfull + 1;                // [NQ] a tile's logits are in TMEM (and the PV before is done)
-  uint64_t* pfull = sfull + 2;                // [NQ][2] half of its probabilities are
-  uint64_t* ofull = pfull + 4;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + lay.bars + 224);
-
+  Control& C = *reinterpret_cast<Control*>(smem + lay.control);
+  Ctl* ctl = &C.ctl;
   const int S = P.stages;
-  const int T = (blk.kv_len + kTileKeys - 1) / kTileKeys;
-  const int t_lo = (int)((int64_t)T * rank / splits), t_hi = (int)((int64_t)T * (rank + 1) / splits);
-  const int nt = t_hi - t_lo;
-  const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;  // tiles with rows
-  auto rows_of = [&](int q) { return min(blk.cnt - q * P.tpt, P.tpt) * P.group; };
+  const int wpt = (P.group * P.tpt + 31) / 32;  // softmax warps with rows in a full tile
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&C.full[i], 1);
+      mbar_init(&C.empty[i], 1);
     }
-    mbar_init(qfull, 1);
-    mbar_init(ofull, 1);
-    for (int q = 0; q < nq; ++q) {
-      mbar_init(&sfull[q], 1);
-      for (int k = 0; k < 2; ++k)
-        mbar_init(&pfull[2 * q + k], (uint32_t)(rows_of(q) + 31) / 32);  // one arrival per warp with rows
+    mbar_init(&C.qfull, 1);
+    mbar_init(&C.qempty, 1);
+    for (int q = 0; q < NQ; ++q) {
+      mbar_init(&C.sfull[q], 1);
+      mbar_init(&C.pfull[q][0], (uint32_t)wpt);
+      mbar_init(&C.pfull[q][1], (uint32_t)wpt);
+      mbar_init(&C.ofull[q], 1);
+      mbar_init(&C.ofree[q], (uint32_t)wpt);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&C.wfull[i], 1);
+      mbar_init(&C.wempty[i], (uint32_t)(NQ * wpt + 2));
+    }
+    mbar_init(&C.want, 1);
+    mbar_init(&C.taken, 1);
+    mbar_init(&C.drain, 1);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -327,141 +392,230 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);
 
+  // The next piece of work; false: none is left, or a wait ran out. Every lane of
+  // a warp gets it; one arrival per warp frees the slot.
+  int works = 0;
+  auto next_work = [&](Work& w) {
+    const int slot = works & 1;
+    if (!__all_sync(kFull, mbar_wait(&C.wfull[slot], (uint32_t)((works >> 1) & 1), ctl, P.status))) return false;
+    w = C.work[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.wempty[slot]);
+    ++works;
+    return w.blk.cnt > 0;
+  };
+
   // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
-  // issuer, two idle warps) gives them its registers: 40 + 216 = 2 * 128 a
-  // thread for one tile, 56 + 2 * 224 = 3 * 168 for two.
-  if (warp >= NQ * 4) {
+  // issuer, scheduler, one idle warp) gives them its registers: 40 + 216 = 2 * 128
+  // a thread for one tile, 56 + 2 * 224 = 3 * 168 for two.
+  if (warp >= kSoftmaxWarps) {
     regs_dec<NQ == 1 ? 40 : 56>();
-    if (warp == kProducer) {
-      // ------------------------------------------------------------ TMA producer
-      if (lane == 0 && nt > 0) {
-        const uint64_t pol = policy_evict_normal();
-        const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
-        mbar_expect_tx(qfull, (uint32_t)nq * 2 * qbytes);
-        for (int q = 0; q < nq; ++q)
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
-                        (int)(blk.row0 + q * P.tpt), qfull, pol);
-        const int z = blk.b * P.kv_heads + blk.h;
-        int st = 0, g = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int i = 0; i < 2 * nt; ++i, ++g) {
-          if (g >= S) ok = mbar_wait(&empty[st], ph ^ 1u, ctl, P.status);
-          if (!ok) break;
-          mbar_expect_tx(&full[st], kTileBytes);
-          const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
-          const CUtensorMap* map = (i & 1) ? &P.vmap : &P.kmap;
-          const int y = (t_lo + (i >> 1)) * kTileKeys;
-          tma_load_3d(dst, map, 0, y, z, &full[st], pol);
-          tma_load_3d(dst + kSlabBytes, map, 64, y, z, &full[st], pol);
-          if (++st == S) {
-            st = 0;
-            ph ^= 1u;
+    if (warp == kScheduler) {
+      // ---------------------------------------------------------- scheduler
+      // The grid has one CTA per row block, the longest first; a CTA that runs out
+      // of work takes a block that has not started (the hardware hands them out),
+      // so the setup and the pipeline's ends are paid once per SM and the order of
+      // the grid still balances the load. A cluster works on its one block.
+      int64_t item = blockIdx.x / (unsigned)splits;
+      int n = 0, tries = 0;
+      bool ok = true;
+      auto publish = [&](const Work& w) {
+        const int slot = n & 1;
+        if (n >= 2) ok = __all_sync(kFull, mbar_wait(&C.wempty[slot], (uint32_t)(((n >> 1) - 1) & 1), ctl, P.status));
+        if (ok && lane == 0) {
+          C.work[slot] = w;
+          mbar_arrive(&C.wfull[slot]);
+        }
+        ++n;
+      };
+      while (ok) {
+        Work w;
+        w.blk = P.cu ? find_prompt_block(P, item, tpi) : find_tree_block(P, item, tpi);
+        if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
+        if (w.blk.cnt > 0) {
+          const int T = (w.blk.kv_len + kTileKeys - 1) / kTileKeys;
+          w.t_lo = (int)((int64_t)T * rank / splits);
+          w.nt = (int)((int64_t)T * (rank + 1) / splits) - w.t_lo;
+          publish(w);
+          if (ok && splits == 1) ok = __all_sync(kFull, mbar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl, P.status));
+        }
+        if (!ok || splits > 1) break;
+        if (lane == 0) {
+          mbar_expect_tx(&C.taken, 16);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last name has been read
+          take_block(&C.block, &C.taken);
+        }
+        ok = __all_sync(kFull, mbar_wait(&C.taken, (uint32_t)(tries & 1), ctl, P.status));
+        if (!ok) {  // the name must land before the CTA exits
+          const long long t0 = clock64();
+          while (!mbar_test(&C.taken, (uint32_t)(tries & 1)) && clock64() - t0 < kWaitCycles) {
+          }
+          break;
+        }
+        ++tries;
+        item = taken_block(&C.block);
+        __syncwarp();
+        if (item < 0) break;
+      }
+      if (ok) {
+        Work w;
+        w.blk.cnt = 0;
+        publish(w);
+      }
+    } else if (warp == kProducer) {
+      // ---------------------------------------------------------- TMA producer
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
+      int st = 0, items = 0;
+      long long g = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      Work w;
+      while (ok && next_work(w)) {
+        if (lane == 0 && w.nt > 0) {
+          const Block& blk = w.blk;
+          const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;
+          if (items > 0) ok = mbar_wait(&C.qempty, (uint32_t)((items - 1) & 1), ctl, P.status);
+          if (ok) {
+            mbar_expect_tx(&C.qfull, (uint32_t)nq * 2 * qbytes);
+            for (int q = 0; q < nq; ++q)
+              for (int s = 0; s < 2; ++s)
+                tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
+                            (int)(blk.row0 + q * P.tpt), &C.qfull, pol);
+            ++items;
+          }
+          const int z = blk.b * P.kv_heads + blk.h;
+          const int call = 2 * w.nt > 8 ? 2 * w.nt - 8 : 0;  // four tiles before the end
+          for (int i = 0; i < 2 * w.nt && ok; ++i) {
+            if (i == call) mbar_arrive(&C.want);
+            if (g >= S) ok = mbar_wait(&C.empty[st], ph ^ 1u, ctl, P.status);
+            if (!ok) break;
+            mbar_expect_tx(&C.full[st], kTileBytes);
+            const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
+            const CUtensorMap* map = (i & 1) ? &P.vmap : &P.kmap;
+            const int y = (w.t_lo + (i >> 1)) * kTileKeys;
+            tma_load_3d(dst, map, 0, y, z, &C.full[st], pol);
+            tma_load_3d(dst + kSlabBytes, map, 64, y, z, &C.full[st], pol);
+            ++g;
+            if (++st == S) {
+              st = 0;
+              ph ^= 1u;
+            }
           }
         }
-        if (!ok) {  // after an abort, loads already issued must land before the CTA exits
-          long long t0 = clock64();
-          while (!mbar_test(qfull, 0u) && clock64() - t0 < kWaitCycles) {
-          }
-          for (int s = 0; s < S && s < g; ++s) {
-            const int last = g - 1 - ((g - 1 - s) % S);
-            t0 = clock64();
-            while (!mbar_test(&full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
-            }
+        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0 && ctl->abort) {  // loads already issued must land before the CTA exits
+        long long t0 = clock64();
+        while (items > 0 && !mbar_test(&C.qfull, (uint32_t)((items - 1) & 1)) && clock64() - t0 < kWaitCycles) {
+        }
+        for (int s = 0; s < S && s < g; ++s) {
+          const long long last = g - 1 - ((g - 1 - s) % S);
+          t0 = clock64();
+          while (!mbar_test(&C.full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
           }
         }
       }
     } else if (warp == kIssuer) {
-      // ------------------------------------------------------------ MMA issuer
-      // The tensor core takes few MMAs ahead, so whatever lies
-      // between two of them shows up as idle time: the waits on K and V stages sit
-      // in the middle of a product whose MMAs are queued, and only the waits for
-      // probabilities stand between two products.
-      if (nt > 0) {
-        constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
-        const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
-        const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
-        const uint32_t el = elect_one();
-        // the two 64-column halves of a logit product
-        auto issue_qk = [&](int q, int st, int half) {
-          const uint32_t d = tmem + (uint32_t)q * 256;
-          const uint32_t a = qd + (uint32_t)(2 * q + half) * slab_step;
-          const uint32_t b = kd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)half * (kSlabBytes >> 4);
-          umma_ss<0, 0>(d, a, b, id_qk, (uint32_t)half, el);
-          umma_ss<2, 2>(d, a, b, id_qk, 1u, el);
-          umma_ss<4, 4>(d, a, b, id_qk, 1u, el);
-          umma_ss<6, 6>(d, a, b, id_qk, 1u, el);
-        };
-        // 32 keys of a PV product
-        auto issue_pv = [&](int q, int st, int quarter, uint32_t acc) {
-          const uint32_t s = tmem + (uint32_t)q * 256, p = s + (uint32_t)quarter * 16;
-          const uint32_t b = vd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)quarter * 256;
-          umma_ts<0, 0>(s + 128, p, b, id_pv, acc, el);
-          umma_ts<8, 128>(s + 128, p, b, id_pv, 1u, el);
-        };
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          return __all_sync(kFull, mbar_wait(bar, parity, ctl, P.status));
-        };
-        bool issued = false;
-        int sv = 1 % S;  // stage of V_j; K_{j+1} follows
-        uint32_t pv = S == 1 ? 1u : 0u;
-        bool ok = wait(qfull, 0u) && wait(&full[0], 0u);
-        if (ok) {
-          tc_fence_after();
-          issued = true;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            if (q < nq) {
-              issue_qk(q, 0, 0);
-              issue_qk(q, 0, 1);
-              umma_commit_if(&sfull[q], el);
-            }
-          umma_commit_if(&empty[0], el);
-          ok = wait(&full[sv], pv);
+      // ---------------------------------------------------------- MMA issuer
+      // The tensor core takes few MMAs ahead, so whatever lies between two of them
+      // shows up as idle time: the waits on K and V stages sit in the middle of a
+      // product whose MMAs are queued, and only the waits for probabilities stand
+      // between two products.
+      constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
+      const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
+      const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
+      const uint32_t el = elect_one();
+      // the two 64-column halves of a logit product
+      auto issue_qk = [&](int q, int st, int half) {
+        const uint32_t d = tmem + (uint32_t)q * 256;
+        const uint32_t a = qd + (uint32_t)(2 * q + half) * slab_step;
+        const uint32_t b = kd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)half * (kSlabBytes >> 4);
+        umma_ss<0, 0>(d, a, b, id_qk, (uint32_t)half, el);
+        umma_ss<2, 2>(d, a, b, id_qk, 1u, el);
+        umma_ss<4, 4>(d, a, b, id_qk, 1u, el);
+        umma_ss<6, 6>(d, a, b, id_qk, 1u, el);
+      };
+      // 32 keys of a PV product
+      auto issue_pv = [&](int q, int st, int quarter, uint32_t acc) {
+        const uint32_t s = tmem + (uint32_t)q * 256, p = s + (uint32_t)quarter * 16;
+        const uint32_t b = vd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)quarter * 256;
+        umma_ts<0, 0>(s + 128, p, b, id_pv, acc, el);
+        umma_ts<8, 128>(s + 128, p, b, id_pv, 1u, el);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(kFull, mbar_wait(bar, parity, ctl, P.status));
+      };
+      auto step = [&](int& st, uint32_t& ph) {
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
         }
+      };
+      int items = 0, tiles[2] = {0, 0}, outs[2] = {0, 0};  // per row tile: key tiles and row blocks done
+      int st = 0;  // next stage of the ring
+      uint32_t ph = 0;
+      bool ok = true, issued = false;
+      Work w;
+      while (ok && next_work(w)) {
+        if (w.nt == 0) continue;
+        const int nt = w.nt, nq = NQ == 1 || w.blk.cnt <= P.tpt ? 1 : 2;
+        ok = wait(&C.qfull, (uint32_t)(items & 1)) && wait(&C.full[st], ph);
+        ++items;
+        if (!ok) break;
+        tc_fence_after();
+        issued = true;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (q < nq) {
+            issue_qk(q, st, 0);
+            issue_qk(q, st, 1);
+            umma_commit_if(&C.sfull[q], el);
+          }
+        umma_commit_if(&C.empty[st], el);
+        if (nt == 1) umma_commit_if(&C.qempty, el);
+        step(st, ph);
+        int sv = st;  // stage of V_j; K_{j+1} follows
+        ok = wait(&C.full[sv], ph);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)  // the last block's O has been read
+          if (q < nq && outs[q]++ > 0) ok = ok && wait(&C.ofree[q], (uint32_t)(outs[q] & 1));
         for (int j = 0; j + 1 < nt && ok; ++j) {
-          int sk = sv + 1;  // stages of K_{j+1} and V_{j+1}
-          uint32_t pk = pv;
-          if (sk == S) {
-            sk = 0;
-            pk ^= 1u;
-          }
-          int sn = sk + 1;
-          uint32_t pn = pk;
-          if (sn == S) {
-            sn = 0;
-            pn ^= 1u;
-          }
-          const uint32_t par = (uint32_t)(j & 1);
+          step(st, ph);
+          const int sk = st;  // stages of K_{j+1} and V_{j+1}
+          const uint32_t pk = ph;
+          step(st, ph);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= nq || !ok) break;
-            ok = wait(&pfull[2 * q], par);
+            const uint32_t par = (uint32_t)((tiles[q] + j) & 1);
+            ok = wait(&C.pfull[q][0], par);
             if (!ok) break;
             tc_fence_after();
             issue_pv(q, sv, 0, j > 0 ? 1u : 0u);
             issue_pv(q, sv, 1, 1u);
-            ok = wait(&pfull[2 * q + 1], par);
+            ok = wait(&C.pfull[q][1], par);
             if (!ok) break;
             tc_fence_after();
             issue_pv(q, sv, 2, 1u);
-            if (q == 0) ok = wait(&full[sk], pk);
+            if (q == 0) ok = wait(&C.full[sk], pk);
             issue_pv(q, sv, 3, 1u);
-            if (q == nq - 1) umma_commit_if(&empty[sv], el);
+            if (q == nq - 1) umma_commit_if(&C.empty[sv], el);
             if (!ok) break;
             issue_qk(q, sk, 0);
-            if (q == nq - 1) ok = wait(&full[sn], pn);
+            if (q == nq - 1) ok = wait(&C.full[st], ph);
             issue_qk(q, sk, 1);
-            umma_commit_if(&sfull[q], el);
+            umma_commit_if(&C.sfull[q], el);
           }
-          umma_commit_if(&empty[sk], el);
-          sv = sn;
-          pv = pn;
+          umma_commit_if(&C.empty[sk], el);
+          sv = st;
         }
+        if (!ok) break;
+        if (nt > 1) umma_commit_if(&C.qempty, el);
+        step(st, ph);
         // the last tile: V rows behind the last slot may hold NaN, and 0 * NaN is NaN
-        const int live = blk.kv_len - (t_hi - 1) * kTileKeys;
-        if (ok && live < kTileKeys) {
+        const int live = w.blk.kv_len - (w.t_lo + nt - 1) * kTileKeys;
+        if (live < kTileKeys) {
           uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
           for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
             rows[i] = make_uint4(0, 0, 0, 0);
@@ -471,25 +625,34 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           __syncwarp();
         }
 #pragma unroll
-        for (int i = 0; i < 2 * NQ; ++i) {
-          if (i >= 2 * nq || !ok) break;
-          ok = wait(&pfull[i], (uint32_t)((nt - 1) & 1));
+        for (int q = 0; q < NQ; ++q) {
+          if (q >= nq || !ok) break;
+          const uint32_t par = (uint32_t)((tiles[q] + nt - 1) & 1);
+          tiles[q] += nt;
+          ok = wait(&C.pfull[q][0], par);
           if (!ok) break;
           tc_fence_after();
-          issue_pv(i >> 1, sv, 2 * (i & 1), (i & 1) || nt > 1 ? 1u : 0u);
-          issue_pv(i >> 1, sv, 2 * (i & 1) + 1, 1u);
+          issue_pv(q, sv, 0, nt > 1 ? 1u : 0u);
+          issue_pv(q, sv, 1, 1u);
+          ok = wait(&C.pfull[q][1], par);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(q, sv, 2, 1u);
+          issue_pv(q, sv, 3, 1u);
+          umma_commit_if(&C.ofull[q], el);
         }
-        if (issued) umma_commit_if(ofull, el);
-        if (!ok && issued) {
-          // after an abort, let the MMAs already issued finish before the TMEM is freed
-          const long long t0 = clock64();
-          while (!mbar_test(ofull, 0u) && clock64() - t0 < kWaitCycles) {
-          }
-        }
-        __syncwarp();
+        umma_commit_if(&C.empty[sv], el);
       }
+      if (!ok && issued) {
+        // after an abort, let the MMAs already issued finish before the TMEM is freed
+        umma_commit_if(&C.drain, el);
+        const long long t0 = clock64();
+        while (!mbar_test(&C.drain, 0u) && clock64() - t0 < kWaitCycles) {
+        }
+      }
+      __syncwarp();
     }
-  if (splits > 1) {  // the joins' two barriers, see below
+    if (splits > 1) {  // the join's two barriers, see below
       __syncwarp();
       cluster_sync();
       cluster_sync();
@@ -499,12 +662,26 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     regs_inc<NQ == 1 ? 216 : 224>();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const int rows = q < nq ? rows_of(q) : 0;
-    if ((warp & 3) * 32 < rows) {
-      const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
-      const uint32_t t_s = tl + (uint32_t)q * 256, t_o = t_s + 128;
+    const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
+    const uint32_t t_s = tl + (uint32_t)q * 256, t_o = t_s + 128;
+    const int tok_q = row / P.group, g_q = row - tok_q * P.group;  // token in its tile, query head in its group
+    uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)(q * wpt + (warp & 3)) * kWarpOut);
+    const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2);
+    int tiles = 0, outs = 0;
+    bool ok = true;
+    Work w;
+    w.blk.cnt = 0;
+    w.nt = 0;
+    int rows = 0;  // of this row tile in the present block
+    // warps that never have a row take no part
+    while ((warp & 3) < wpt && ok && next_work(w)) {
+      const Block& blk = w.blk;
+      const int nt = w.nt;
+      rows = min(blk.cnt - q * P.tpt, P.tpt) * P.group;
+      if (rows <= 0) continue;
+      const bool active = (warp & 3) * 32 < rows;
       const bool valid = row < rows;
-      const int tok = q * P.tpt + (valid ? row / P.group : 0);
+      const int tok = q * P.tpt + (valid ? tok_q : 0);
       // slots [0, lim) are visible, and the tree's slots L + i whose bit is set
       int lim = min(blk.past + tok + 1, blk.kv_len);
       uint64_t bits = 0;
@@ -516,16 +693,25 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       // tiles that end at or below every row's bound need no mask
       const int lim_min = P.mask ? blk.L : min(blk.past + q * P.tpt + 1, blk.kv_len);
       float m = kNegInf, l = 0.f;
-      bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        ok = __all_sync(kFull, mbar_wait(&sfull[q], (uint32_t)(j & 1), ctl, P.status));
+        ok = __all_sync(kFull, mbar_wait(&C.sfull[q], (uint32_t)(tiles & 1), ctl, P.status));
+        ++tiles;
         if (!ok) break;
+        if (!active) {
+          if (lane == 0) {
+            mbar_arrive(&C.pfull[q][0]);
+            mbar_arrive(&C.pfull[q][1]);
+          }
+          continue;
+        }
         tc_fence_after();
         float v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + (uint32_t)c * 32, v[c]);
         tmem_wait_ld();
-        const int base = (t_lo + j) * kTileKeys;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) pin(v[c]);
+        const int base = (w.t_lo + j) * kTileKeys;
         if (base + kTileKeys > lim_min) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -548,27 +734,29 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           mx[c] = fmaxf(mx[c], v[c][31]);
         }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
-        const bool move = mt > m + kRescale || (m == kNegInf && mt > kNegInf);
-        if (__any_sync(kFull, move)) {
+        if (j == 0) {
+          m = mt;
+        } else if (__any_sync(kFull, mt > m + kRescale || (m == kNegInf && mt > kNegInf))) {
           const float m_new = fmaxf(m, mt);
           const float f = m == kNegInf ? 0.f : fast_exp2(m - m_new);
           l *= f;
-          if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld32(t_o + (uint32_t)c * 32, o);
-              tmem_wait_ld();
-              uint32_t r[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * f);
-              tmem_st32(t_o + (uint32_t)c * 32, r);
-            }
-          }
           m = m_new;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[16];
+            tmem_ld16(t_o + (uint32_t)c * 16, o);
+            tmem_wait_ld();
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              asm volatile("" : "+f"(o[i]));  // as pin()
+              r[i] = __float_as_uint(o[i] * f);
+            }
+            tmem_st16(t_o + (uint32_t)c * 16, r);
+          }
         }
         const float off = m == kNegInf ? 0.f : -m;
-        const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2), off2 = pack2(off, off);
+        const uint64_t off2 = pack2(off, off);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -587,19 +775,25 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[2 * q + half]);  // the first 64 keys' PV may start
+          if (lane == 0) mbar_arrive(&C.pfull[q][half]);  // the first 64 keys' PV may start
         }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
-      if (ok && nt > 0) {
-        ok = __all_sync(kFull, mbar_wait(ofull, 0u, ctl, P.status));
+      if (!ok) break;
+      if (nt > 0) {
+        ok = __all_sync(kFull, mbar_wait(&C.ofull[q], (uint32_t)(outs & 1), ctl, P.status));
+        // a cluster's partial results go where the other tile's V may still be read
+        if (ok && NQ == 2 && splits > 1 && blk.cnt > P.tpt)
+          ok = __all_sync(kFull, mbar_wait(&C.ofull[q ^ 1], (uint32_t)(outs & 1), ctl, P.status));
+        ++outs;
+        if (!ok) break;
         tc_fence_after();
       }
       if (splits > 1) {
         ml[q * 128 + row] = make_float2(m, l);
-        if (ok && nt > 0) {
+        if (nt > 0 && active) {
           // partial O, 16-byte chunk c of a row at c ^ (row & 31): no bank conflicts
           float4* part = reinterpret_cast<float4*>(ring) + (size_t)(q * 128 + row) * 32;
 #pragma unroll
@@ -607,55 +801,81 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             float o[32];
             tmem_ld32(t_o + (uint32_t)c * 32, o);
             tmem_wait_ld();
+            pin(o);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               part[(c * 8 + i) ^ lane] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-      } else if (ok) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no visible slot: 0; NaN stays
-        const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + (row - (row / P.group) * P.group);
-        uint4* dst = reinterpret_cast<uint4*>(P.out) + orow * 16;
-        float check = 0.f;  // stays 0 unless some value is not finite
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          if (nt > 0) {
-            tmem_ld32(t_o + (uint32_t)c * 32, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o[i] = nt > 0 && l != 0.f ? o[i] * inv : 0.f;
-            check = fmaf(o[i], 0.f, check);
-          }
-          if (valid && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[c * 4 + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                          pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-          }
+        continue;
+      }
+      if (!active) {
+        if (lane == 0) mbar_arrive(&C.ofree[q]);
+        continue;
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no visible slot: 0; NaN stays
+      const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
+      const int mine = valid ? tok * P.heads + g_q : -1;  // this lane's row from orow0
+      float check = 0.f;  // stays 0 unless some value is not finite
+      // rows go out through shared memory: 8 lanes write a row's 128 bytes at a time
+      // instead of every lane 16 bytes of its own row
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float o[2][32];
+        tmem_ld32(t_o + (uint32_t)half * 64, o[0]);
+        tmem_ld32(t_o + (uint32_t)half * 64 + 32, o[1]);
+        tmem_wait_ld();
+        pin(o[0]);
+        pin(o[1]);
+        if (half) {  // all of O is in registers or out
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C.ofree[q]);
         }
-        if (valid && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) {
-          const float lse = l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
-          if (P.lse) P.lse[orow] = lse;
-          if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = l != 0.f ? o[i >> 2][(i & 3) * 8 + e] * inv : 0.f;
+            check = fmaf(x[e], 0.f, check);
+          }
+          stage[lane * 8 + (i ^ (lane & 7))] =
+              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const int at = __shfl_sync(kFull, mine, r);
+          const int64_t orow = orow0 + at;
+          if (at >= 0 && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status))
+            reinterpret_cast<uint4*>(P.out)[orow * 16 + half * 8 + (lane & 7)] = stage[r * 8 + ((lane & 7) ^ (r & 7))];
+        }
+        __syncwarp();
+      }
+      if (valid && BKV_IN_RANGE(orow0 + mine >= 0 && orow0 + mine < (int64_t)P.total * P.heads, P.status)) {
+        const float lse = l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
+        if (P.lse) P.lse[orow0 + mine] = lse;
+        if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
       }
     }
     if (splits > 1) {
       // ---------------------------------------------------------- join
       __syncwarp();
       cluster_sync();
-      if (!ctl->abort) {
+      // every CTA of the cluster had the same block; w is the work before the end mark
+      const Block blk = C.work[0].blk;
+      if (!ctl->abort && blk.cnt > 0) {
+        const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;
         const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
-        for (int q = 0; q < nq; ++q) {
-          const int rows = rows_of(q);
+        for (int t = 0; t < nq; ++t) {
+          const int n = min(blk.cnt - t * P.tpt, P.tpt) * P.group;
           // rank r joins rows r, r + splits, ...; one warp per row, 4 columns per lane
-          for (int row = rank + warp * splits; row < rows; row += splits * NQ * 4) {
+          for (int r = rank + warp * splits; r < n; r += splits * kSoftmaxWarps) {
             float mc = kNegInf, lc = 0.f;
             if (lane < splits) {
-              const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(q * 128 + row) * 8, (uint32_t)lane));
+              const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(t * 128 + r) * 8, (uint32_t)lane));
               mc = x.x;
               lc = x.y;
             }
@@ -663,15 +883,15 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
             // a share without a visible key has no part in the sums (its O is not written or zero)
-            const float w = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
+            const float wt = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = 0; c < splits; ++c) {
-              const float wc = __shfl_sync(kFull, w, c), lcc = __shfl_sync(kFull, lc, c);
+              const float wc = __shfl_sync(kFull, wt, c), lcc = __shfl_sync(kFull, lc, c);
               if (wc == 0.f) continue;
               l = fmaf(wc, lcc, l);
               const float4 x = ld_cluster4(
-                  map_rank(part + ((uint32_t)(q * 128 + row) * 32 + (uint32_t)(lane ^ (row & 31))) * 16, (uint32_t)c));
+                  map_rank(part + ((uint32_t)(t * 128 + r) * 32 + (uint32_t)(lane ^ (r & 31))) * 16, (uint32_t)c));
               o.x = fmaf(wc, x.x, o.x);
               o.y = fmaf(wc, x.y, o.y);
               o.z = fmaf(wc, x.z, o.z);
@@ -682,8 +902,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             o.y *= inv;
             o.z *= inv;
             o.w *= inv;
-            const int tok = q * P.tpt + row / P.group;
-            const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + row % P.group;
+            const int tok = t * P.tpt + r / P.group;
+            const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + r % P.group;
             if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
             reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
             const float lse = l > 0.f ? (M + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
@@ -697,6 +917,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       cluster_sync();  // no CTA leaves while another still reads its partial results
     }
   }
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -704,6 +925,16 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 }
 
 }  // namespace
+
+// K/V stages that fit. Two CTAs of one tile share an SM's 228 KB; fewer than the
+// most would fit three there, and three ask for more TMEM columns (256 each) than
+// it has.
+int attend_stages(int nq, int group, int tpt) {
+  const uint32_t room = nq == 1 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
+  int n = kMaxStages;
+  while (n > 0 && attend_smem(nq, group, tpt, n).total > room) --n;
+  return n;
+}
 
 bool encode_attend_maps(AttendParams& p, const void* q, int64_t q_stride, const void* K, const void* V) {
   // the driver's encoder, looked up once per process (thread-safe static initialisation)
@@ -749,6 +980,7 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
     if (e != cudaSuccess) return e;
     configured[nq - 1].fetch_or(bit);
   }
+  if (p.stages < 2) return cudaErrorInvalidConfiguration;  // V_j and K_{j+1}
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * splits));
   cfg.blockDim = dim3((unsigned)(nq * 128 + 128));
