@@ -90,16 +90,6 @@ __device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t elected) 
       "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -180,6 +170,11 @@ __device__ __forceinline__ int64_t taken_block(const void* result) {
       : "r"(smem_u32(result))
       : "memory");
   return got ? (int64_t)x : -1;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 template <int N>
 __device__ __forceinline__ void regs_dec() {
@@ -312,7 +307,8 @@ struct Control {
   uint64_t qfull, qempty;
   uint64_t sfull[2];      // a tile's logits are in TMEM (and its PV before is done)
   uint64_t pfull[2][2];   // half of its probabilities are
-  uint64_t ofull[2], ofree[2];  // O is complete; O has been read
+  uint64_t ofull[2], ofree[2];  // O is complete; O (and the row statistics) have been read
+  uint64_t rfull[2];            // a tile's row statistics are in shared memory
   uint64_t wfull[2], wempty[2];  // work slots
   uint64_t want, taken;   // the producer runs out of work; a block has been taken
   uint64_t drain;         // after an abort
@@ -321,8 +317,13 @@ struct Control {
   Ctl ctl;
 };
 
+// With two tiles per CTA four more warps write the output, so that the softmax
+// warps go on with the next row block at once. With one tile two CTAs share the SM
+// (and its registers), and one's output overlaps the other's work anyway.
+__host__ __device__ constexpr bool output_warps(int nq) { return nq == 2; }
+
 struct Smem {
-  uint32_t slab_q, q, ring, out, control, total;
+  uint32_t slab_q, q, ring, out, stats, control, total;
 };
 // The ring starts behind the rows in use; an MMA reads 128 rows of Q whatever
 // their number, the rest of them from the ring: rows nobody looks at.
@@ -333,13 +334,85 @@ __host__ __device__ inline Smem attend_smem(int nq, int group, int tpt, int stag
   s.q = 0;
   s.ring = s.q + (uint32_t)nq * 2 * s.slab_q;
   s.out = s.ring + (uint32_t)stages * kTileBytes;
-  s.control = s.out + (uint32_t)(nq * ((rows + 31) / 32)) * kWarpOut;
+  s.stats = s.out + (uint32_t)((rows + 31) / 32) * kWarpOut;
+  s.control = s.stats + (output_warps(nq) ? (uint32_t)nq * 128 * 8 : 0);
   s.total = s.control + (uint32_t)((sizeof(Control) + 15) / 16 * 16);
   return s;
 }
 
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);  // no visible slot: -inf; NaN stays
+}
+__device__ __forceinline__ float row_scale(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
+
+// One warp's 32 rows of a tile's O, out of TMEM: normalised, rounded and written.
+// t_o: the warp's lanes and the tile's columns; `mine`: where this lane's row goes,
+// in rows from orow0, or -1. `free_bar` gets the warp's arrival once O is read.
+__device__ __forceinline__ void write_rows(const AttendParams& P, uint32_t t_o, uint4* stage, int64_t orow0, int mine,
+                                           float m, float l, uint64_t* free_bar) {
+  const int lane = threadIdx.x & 31;
+  const float inv = row_scale(l);
+  const uint64_t inv2 = pack2(inv, inv), tiny2 = pack2(0x1p-10f, 0x1p-10f);
+  uint64_t check[2] = {0ull, 0ull};  // finite unless some value is not
+  uint4* dst = reinterpret_cast<uint4*>(P.out) + orow0 * 16 + (lane & 7);
+  // rows go out through shared memory: 8 lanes write 128 bytes of a row at a time
+  // instead of every lane 16 bytes of its own row
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float o[32];
+      tmem_ld32(t_o + (uint32_t)(half * 64 + c * 32), o);
+      tmem_wait_ld();
+      pin(o);
+      if (half && c) {  // all of O is in registers or out
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(free_bar);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t x = mul2(pack2(o[i * 8 + 2 * e], o[i * 8 + 2 * e + 1]), inv2);
+          check[e & 1] = fma2(x, tiny2, check[e & 1]);
+          float a, b;
+          unpack2(x, a, b);
+          y[e] = pack_bf16(a, b);
+        }
+        stage[lane * 8 + ((c * 4 + i) ^ (lane & 7))] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      uint4 y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * (k + i) + (lane >> 3);
+        y[i] = stage[r * 8 + ((lane & 7) ^ (r & 7))];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = __shfl_sync(kFull, mine, 4 * (k + i) + (lane >> 3));
+        if (at >= 0 && BKV_IN_RANGE(orow0 + at >= 0 && orow0 + at < (int64_t)P.total * P.heads, P.status))
+          dst[(int64_t)at * 16 + half * 8] = y[i];
+      }
+    }
+    __syncwarp();
+  }
+  if (mine >= 0 && BKV_IN_RANGE(orow0 + mine >= 0 && orow0 + mine < (int64_t)P.total * P.heads, P.status)) {
+    const float lse = row_lse(m, l);
+    if (P.lse) P.lse[orow0 + mine] = lse;
+    float a, b;
+    unpack2(add2(check[0], check[1]), a, b);
+    if (!(fabsf(a + b) < __builtin_huge_valf()) || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+  }
+}
+
 template <int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
+__global__ void __launch_bounds__(NQ * 128 + (output_warps(NQ) ? 256 : 128), NQ == 1 ? 2 : 1)
 attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles: 1 KB aligned
   if (smem_u32(smem) & 1023u) {
@@ -347,7 +420,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     return;
   }
   constexpr int kSoftmaxWarps = NQ * 4;
-  constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kScheduler = kSoftmaxWarps + 2;
+  constexpr bool kOut = output_warps(NQ);
+  constexpr int kControl = kSoftmaxWarps + (kOut ? 4 : 0);  // first warp of the control warpgroup
+  constexpr int kProducer = kControl, kIssuer = kControl + 1, kScheduler = kControl + 2;
   constexpr uint32_t kCols = NQ * 256;  // per tile: 128 columns of S (and P), 128 of O
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % (unsigned)splits);
@@ -357,6 +432,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   unsigned char* q_s = smem + lay.q;
   unsigned char* ring = smem + lay.ring;
   float2* ml = reinterpret_cast<float2*>(q_s);  // [NQ * 128] partial maximum and sum, once Q is done with
+  float2* stats_s = reinterpret_cast<float2*>(smem + lay.stats);  // [2][128] a finished tile's maximum and sum per row
   Control& C = *reinterpret_cast<Control*>(smem + lay.control);
   Ctl* ctl = &C.ctl;
   const int S = P.stages;
@@ -375,10 +451,11 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       mbar_init(&C.pfull[q][1], (uint32_t)wpt);
       mbar_init(&C.ofull[q], 1);
       mbar_init(&C.ofree[q], (uint32_t)wpt);
+      mbar_init(&C.rfull[q], (uint32_t)wpt);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.wfull[i], 1);
-      mbar_init(&C.wempty[i], (uint32_t)(NQ * wpt + 2));
+      mbar_init(&C.wempty[i], (uint32_t)((NQ + (kOut ? 1 : 0)) * wpt + 2));
     }
     mbar_init(&C.want, 1);
     mbar_init(&C.taken, 1);
@@ -405,11 +482,29 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     return w.blk.cnt > 0;
   };
 
+  // One warp's part of a cluster's partial results: O as it is, 16-byte chunk c of a
+  // row at c ^ (row & 31) against bank conflicts, and the row's maximum and sum.
+  auto write_partial = [&](uint32_t t_o, int q, int row, float m, float l, bool any) {
+    ml[q * 128 + row] = make_float2(m, l);
+    if (!any) return;
+    float4* part = reinterpret_cast<float4*>(ring) + (size_t)(q * 128 + row) * 32;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float o[32];
+      tmem_ld32(t_o + (uint32_t)c * 32, o);
+      tmem_wait_ld();
+      pin(o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        part[(c * 8 + i) ^ lane] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+  };
+
   // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
-  // issuer, scheduler, one idle warp) gives them its registers: 40 + 216 = 2 * 128
-  // a thread for one tile, 56 + 2 * 224 = 3 * 168 for two.
-  if (warp >= kSoftmaxWarps) {
-    regs_dec<NQ == 1 ? 40 : 56>();
+  // issuer, scheduler, one idle warp) and the output warps give them registers:
+  // 40 + 216 = 2 * 128 a thread for one tile, 48 + 96 + 2 * 184 = 4 * 128 for two.
+  if (warp >= kControl) {
+    regs_dec<NQ == 1 ? 40 : 48>();
     if (warp == kScheduler) {
       // ---------------------------------------------------------- scheduler
       // The grid has one CTA per row block, the longest first; a CTA that runs out
@@ -657,15 +752,60 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       cluster_sync();
       cluster_sync();
     }
+  } else if (kOut && warp >= kSoftmaxWarps) {
+    // ------------------------------------------------------------ output
+    regs_dec<96>();
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const int tok_q = row / P.group, g_q = row - tok_q * P.group;  // token in its tile, query head in its group
+    uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)wq * kWarpOut);
+    int outs[2] = {0, 0}, stats[2] = {0, 0};
+    bool ok = true;
+    Work w;
+    while (wq < wpt && ok && next_work(w)) {
+      const Block& blk = w.blk;
+      const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
+      const int nq = blk.cnt <= P.tpt ? 1 : 2;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (q >= nq || !ok) break;
+        const int rows = min(blk.cnt - q * P.tpt, P.tpt) * P.group;
+        const uint32_t t_o = tmem + ((uint32_t)wq << 21) + (uint32_t)q * 256 + 128;
+        ok = __all_sync(kFull, mbar_wait(&C.rfull[q], (uint32_t)(stats[q] & 1), ctl, P.status));
+        ++stats[q];
+        if (ok && w.nt > 0) {
+          ok = __all_sync(kFull, mbar_wait(&C.ofull[q], (uint32_t)(outs[q] & 1), ctl, P.status));
+          // a cluster's partial results go where the other tile's V may still be read
+          if (ok && splits > 1 && nq == 2)
+            ok = __all_sync(kFull, mbar_wait(&C.ofull[q ^ 1], (uint32_t)(outs[q] & 1), ctl, P.status));
+          ++outs[q];
+          tc_fence_after();
+        }
+        if (!ok) break;
+        const float2 x = stats_s[q * 128 + row];
+        const int tok = q * P.tpt + tok_q;
+        if (splits > 1) {
+          write_partial(t_o, q, row, x.x, x.y, w.nt > 0 && wq * 32 < rows);
+        } else if (wq * 32 < rows) {
+          write_rows(P, t_o, stage, orow0, row < rows ? tok * P.heads + g_q : -1, x.x, x.y, &C.ofree[q]);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C.ofree[q]);
+        }
+      }
+    }
+    if (splits > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<NQ == 1 ? 216 : 224>();
+    regs_inc<NQ == 1 ? 216 : 184>();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
     const uint32_t t_s = tl + (uint32_t)q * 256, t_o = t_s + 128;
     const int tok_q = row / P.group, g_q = row - tok_q * P.group;  // token in its tile, query head in its group
-    uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)(q * wpt + (warp & 3)) * kWarpOut);
     const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2);
     int tiles = 0, outs = 0;
     bool ok = true;
@@ -758,106 +898,64 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         const float off = m == kNegInf ? 0.f : -m;
         const uint64_t off2 = pack2(off, off);
         uint64_t sum[2] = {0ull, 0ull};
+        auto exps = [&](int c, uint32_t* p) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c = 2 * half + (i >> 4), e = (i & 15) * 2;
+          for (int i = 0; i < 16; ++i) {
             float a, b;
-            unpack2(fma2(pack2(v[c][e], v[c][e + 1]), scale2, off2), a, b);
+            unpack2(fma2(pack2(v[c][2 * i], v[c][2 * i + 1]), scale2, off2), a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
             sum[i & 1] = add2(sum[i & 1], pack2(a, b));
             p[i] = pack_bf16(a, b);
           }
-          tmem_st32(t_s + (uint32_t)half * 32, p);
+        };
+        auto hand_over = [&](int half) {
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&C.pfull[q][half]);  // the first 64 keys' PV may start
-        }
+          if (lane == 0) mbar_arrive(&C.pfull[q][half]);
+        };
+        uint32_t p[4][16];
+        exps(0, p[0]);
+        tmem_st16(t_s, p[0]);
+        exps(1, p[1]);
+        tmem_st16(t_s + 16, p[1]);
+        exps(2, p[2]);
+        hand_over(0);
+        tmem_st16(t_s + 32, p[2]);
+        exps(3, p[3]);
+        tmem_st16(t_s + 48, p[3]);
+        hand_over(1);
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
       if (!ok) break;
+      if (kOut) {
+        // the output warps have read the last block's statistics
+        if (outs > 0) ok = __all_sync(kFull, mbar_wait(&C.ofree[q], (uint32_t)((outs - 1) & 1), ctl, P.status));
+        ++outs;
+        if (!ok) break;
+        stats_s[q * 128 + row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.rfull[q]);
+        continue;
+      }
       if (nt > 0) {
         ok = __all_sync(kFull, mbar_wait(&C.ofull[q], (uint32_t)(outs & 1), ctl, P.status));
-        // a cluster's partial results go where the other tile's V may still be read
-        if (ok && NQ == 2 && splits > 1 && blk.cnt > P.tpt)
-          ok = __all_sync(kFull, mbar_wait(&C.ofull[q ^ 1], (uint32_t)(outs & 1), ctl, P.status));
         ++outs;
         if (!ok) break;
         tc_fence_after();
       }
       if (splits > 1) {
-        ml[q * 128 + row] = make_float2(m, l);
-        if (nt > 0 && active) {
-          // partial O, 16-byte chunk c of a row at c ^ (row & 31): no bank conflicts
-          float4* part = reinterpret_cast<float4*>(ring) + (size_t)(q * 128 + row) * 32;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32(t_o + (uint32_t)c * 32, o);
-            tmem_wait_ld();
-            pin(o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              part[(c * 8 + i) ^ lane] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        }
-        continue;
-      }
-      if (!active) {
+        write_partial(t_o, q, row, m, l, nt > 0 && active);
+      } else if (active) {
+        uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)(warp & 3) * kWarpOut);
+        write_rows(P, t_o, stage, blk.row0 * P.heads + (int64_t)blk.h * P.group, valid ? tok * P.heads + g_q : -1, m, l,
+                   &C.ofree[q]);
+      } else {
+        __syncwarp();
         if (lane == 0) mbar_arrive(&C.ofree[q]);
-        continue;
-      }
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no visible slot: 0; NaN stays
-      const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
-      const int mine = valid ? tok * P.heads + g_q : -1;  // this lane's row from orow0
-      float check = 0.f;  // stays 0 unless some value is not finite
-      // rows go out through shared memory: 8 lanes write a row's 128 bytes at a time
-      // instead of every lane 16 bytes of its own row
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float o[2][32];
-        tmem_ld32(t_o + (uint32_t)half * 64, o[0]);
-        tmem_ld32(t_o + (uint32_t)half * 64 + 32, o[1]);
-        tmem_wait_ld();
-        pin(o[0]);
-        pin(o[1]);
-        if (half) {  // all of O is in registers or out
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&C.ofree[q]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = l != 0.f ? o[i >> 2][(i & 3) * 8 + e] * inv : 0.f;
-            check = fmaf(x[e], 0.f, check);
-          }
-          stage[lane * 8 + (i ^ (lane & 7))] =
-              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const int at = __shfl_sync(kFull, mine, r);
-          const int64_t orow = orow0 + at;
-          if (at >= 0 && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status))
-            reinterpret_cast<uint4*>(P.out)[orow * 16 + half * 8 + (lane & 7)] = stage[r * 8 + ((lane & 7) ^ (r & 7))];
-        }
-        __syncwarp();
-      }
-      if (valid && BKV_IN_RANGE(orow0 + mine >= 0 && orow0 + mine < (int64_t)P.total * P.heads, P.status)) {
-        const float lse = l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
-        if (P.lse) P.lse[orow0 + mine] = lse;
-        if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
       }
     }
     if (splits > 1) {
@@ -897,7 +995,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
               o.z = fmaf(wc, x.z, o.z);
               o.w = fmaf(wc, x.w, o.w);
             }
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            const float inv = row_scale(l);
             o.x *= inv;
             o.y *= inv;
             o.z *= inv;
@@ -906,7 +1004,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + r % P.group;
             if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
             reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            const float lse = l > 0.f ? (M + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);
+            const float lse = row_lse(M, l);
             if (P.lse && lane == 0) P.lse[orow] = lse;
             const float check = (o.x + o.y + o.z + o.w) * 0.f;
             if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
@@ -983,7 +1081,7 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
   if (p.stages < 2) return cudaErrorInvalidConfiguration;  // V_j and K_{j+1}
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * splits));
-  cfg.blockDim = dim3((unsigned)(nq * 128 + 128));
+  cfg.blockDim = dim3((unsigned)(nq * 128 + (output_warps(nq) ? 256 : 128)));
   cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
