@@ -12,6 +12,7 @@ constexpr int kMaxGroup = 128;   // query heads per KV head: one token's rows fi
 
 struct AttendParams {
   CUtensorMap qmap;        // queries [tokens][heads][d], box (64, group, tpt)
+  CUtensorMap omap;        // out, the same box
   CUtensorMap kmap, vmap;  // caches [batch * kv_heads][max_cache][d], box (64, 128, 1)
   const int32_t* cu;       // prompt: [batch + 1] token offsets; tree: null
   const int32_t* first;    // [batch] slots before the first token / node

@@ -72,6 +72,12 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "r"(kDescHi), "r"(elected));
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
 // A (the 128 x 16 bf16 probabilities) from TMEM, two elements per 32-bit column.
 template <uint32_t kAStep, uint32_t kBStep>
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
@@ -294,7 +300,8 @@ __device__ __forceinline__ Block find_tree_block(const AttendParams& P, int64_t 
 }
 
 constexpr int kMaxStages = 6;
-constexpr int kWarpOut = 32 * 128;  // staging of a warp's output rows, one 64-column half at a time
+constexpr int kWarpOut = 32 * 128;       // staging of a warp's output rows, one 64-column half at a time
+constexpr int kTileOut = 2 * kSlabBytes;  // output warps: both halves of a tile
 
 // What a row block needs in shared memory, handed from the scheduler to the other warps.
 struct Work {
@@ -309,6 +316,7 @@ struct Control {
   uint64_t pfull[2][2];   // half of its probabilities are
   uint64_t ofull[2], ofree[2];  // O is complete; O (and the row statistics) have been read
   uint64_t rfull[2];            // a tile's row statistics are in shared memory
+  uint64_t staged[2], unstaged[2];  // output warps: a half tile is in its buffer; the buffer may be filled
   uint64_t wfull[2], wempty[2];  // work slots
   uint64_t want, taken;   // the producer runs out of work; a block has been taken
   uint64_t drain;         // after an abort
@@ -334,7 +342,7 @@ __host__ __device__ inline Smem attend_smem(int nq, int group, int tpt, int stag
   s.q = 0;
   s.ring = s.q + (uint32_t)nq * 2 * s.slab_q;
   s.out = s.ring + (uint32_t)stages * kTileBytes;
-  s.stats = s.out + (uint32_t)((rows + 31) / 32) * kWarpOut;
+  s.stats = s.out + (output_warps(nq) ? kTileOut : (uint32_t)((rows + 31) / 32) * kWarpOut);
   s.control = s.stats + (output_warps(nq) ? (uint32_t)nq * 128 * 8 : 0);
   s.total = s.control + (uint32_t)((sizeof(Control) + 15) / 16 * 16);
   return s;
@@ -345,70 +353,68 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 __device__ __forceinline__ float row_scale(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
 
-// One warp's 32 rows of a tile's O, out of TMEM: normalised, rounded and written.
-// t_o: the warp's lanes and the tile's columns; `mine`: where this lane's row goes,
-// in rows from orow0, or -1. `free_bar` gets the warp's arrival once O is read.
-__device__ __forceinline__ void write_rows(const AttendParams& P, uint32_t t_o, uint4* stage, int64_t orow0, int mine,
-                                           float m, float l, uint64_t* free_bar) {
+// 64 columns of one warp's 32 rows of O, out of TMEM: normalised, rounded and put
+// into a SWIZZLE_128B slab (row r of the warp at slab + r * 128 bytes). `check`
+// stays finite unless some value is not. `free_bar`, if any, gets the warp's
+// arrival once the columns have been read.
+__device__ __forceinline__ void stage_half(uint32_t t_o, uint4* slab, uint64_t inv2, uint64_t (&check)[2], uint64_t* free_bar) {
   const int lane = threadIdx.x & 31;
-  const float inv = row_scale(l);
-  const uint64_t inv2 = pack2(inv, inv), tiny2 = pack2(0x1p-10f, 0x1p-10f);
-  uint64_t check[2] = {0ull, 0ull};  // finite unless some value is not
-  uint4* dst = reinterpret_cast<uint4*>(P.out) + orow0 * 16 + (lane & 7);
-  // rows go out through shared memory: 8 lanes write 128 bytes of a row at a time
-  // instead of every lane 16 bytes of its own row
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
+  const uint64_t tiny2 = pack2(0x1p-10f, 0x1p-10f);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float o[32];
-      tmem_ld32(t_o + (uint32_t)(half * 64 + c * 32), o);
-      tmem_wait_ld();
-      pin(o);
-      if (half && c) {  // all of O is in registers or out
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(free_bar);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint64_t x = mul2(pack2(o[i * 8 + 2 * e], o[i * 8 + 2 * e + 1]), inv2);
-          check[e & 1] = fma2(x, tiny2, check[e & 1]);
-          float a, b;
-          unpack2(x, a, b);
-          y[e] = pack_bf16(a, b);
-        }
-        stage[lane * 8 + ((c * 4 + i) ^ (lane & 7))] = make_uint4(y[0], y[1], y[2], y[3]);
-      }
+  for (int c = 0; c < 2; ++c) {
+    float o[32];
+    tmem_ld32(t_o + (uint32_t)c * 32, o);
+    tmem_wait_ld();
+    pin(o);
+    if (c == 1 && free_bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(free_bar);
     }
-    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; k += 4) {
-      uint4 y[4];
+    for (int i = 0; i < 4; ++i) {
+      uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * (k + i) + (lane >> 3);
-        y[i] = stage[r * 8 + ((lane & 7) ^ (r & 7))];
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t x = mul2(pack2(o[i * 8 + 2 * e], o[i * 8 + 2 * e + 1]), inv2);
+        check[e & 1] = fma2(x, tiny2, check[e & 1]);
+        float a, b;
+        unpack2(x, a, b);
+        y[e] = pack_bf16(a, b);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = __shfl_sync(kFull, mine, 4 * (k + i) + (lane >> 3));
-        if (at >= 0 && BKV_IN_RANGE(orow0 + at >= 0 && orow0 + at < (int64_t)P.total * P.heads, P.status))
-          dst[(int64_t)at * 16 + half * 8] = y[i];
-      }
+      slab[lane * 8 + ((c * 4 + i) ^ (lane & 7))] = make_uint4(y[0], y[1], y[2], y[3]);
     }
-    __syncwarp();
   }
-  if (mine >= 0 && BKV_IN_RANGE(orow0 + mine >= 0 && orow0 + mine < (int64_t)P.total * P.heads, P.status)) {
-    const float lse = row_lse(m, l);
-    if (P.lse) P.lse[orow0 + mine] = lse;
-    float a, b;
-    unpack2(add2(check[0], check[1]), a, b);
-    if (!(fabsf(a + b) < __builtin_huge_valf()) || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+}
+// The warp's rows of a staged half to memory, 8 lanes per row. `mine`: where this
+// lane's row goes, in rows from orow0, or -1.
+__device__ __forceinline__ void write_half(const AttendParams& P, const uint4* slab, int64_t orow0, int mine, int half) {
+  const int lane = threadIdx.x & 31;
+  uint4* dst = reinterpret_cast<uint4*>(P.out) + orow0 * 16 + half * 8 + (lane & 7);
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    uint4 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * (k + i) + (lane >> 3);
+      y[i] = slab[r * 8 + ((lane & 7) ^ (r & 7))];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = __shfl_sync(kFull, mine, 4 * (k + i) + (lane >> 3));
+      if (at >= 0 && BKV_IN_RANGE(orow0 + at >= 0 && orow0 + at < (int64_t)P.total * P.heads, P.status))
+        dst[(int64_t)at * 16] = y[i];
+    }
   }
+}
+// This lane's log-sum-exp, and the verdict on its row.
+__device__ __forceinline__ void write_lse(const AttendParams& P, int64_t orow, float m, float l, const uint64_t (&check)[2]) {
+  if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) return;
+  const float lse = row_lse(m, l);
+  if (P.lse) P.lse[orow] = lse;
+  float a, b;
+  unpack2(add2(check[0], check[1]), a, b);
+  if (!(fabsf(a + b) < __builtin_huge_valf()) || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
 }
 
 template <int NQ>
@@ -455,6 +461,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.wfull[i], 1);
+      mbar_init(&C.staged[i], (uint32_t)wpt);
+      mbar_init(&C.unstaged[i], 1);
       mbar_init(&C.wempty[i], (uint32_t)((NQ + (kOut ? 1 : 0)) * wpt + 2));
     }
     mbar_init(&C.want, 1);
@@ -464,6 +472,11 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssuer) tmem_alloc(&ctl->tmem_base, kCols);
+  if (warp == kProducer && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.qmap : lane == 1 ? &P.kmap : &P.vmap) : "memory");
+  const int64_t first_item = blockIdx.x / (unsigned)splits;
+  Block first_blk;
+  if (warp == kScheduler) first_blk = P.cu ? find_prompt_block(P, first_item, tpi) : find_tree_block(P, first_item, tpi);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -502,16 +515,16 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 
   // The softmax warps hold a row's 128 logits; the control warpgroup (producer,
   // issuer, scheduler, one idle warp) and the output warps give them registers:
-  // 40 + 216 = 2 * 128 a thread for one tile, 48 + 96 + 2 * 184 = 4 * 128 for two.
+  // 48 + 208 = 2 * 128 a thread for one tile, 56 + 104 + 2 * 176 = 4 * 128 for two.
   if (warp >= kControl) {
-    regs_dec<NQ == 1 ? 40 : 48>();
+    regs_dec<NQ == 1 ? 48 : 56>();
     if (warp == kScheduler) {
       // ---------------------------------------------------------- scheduler
       // The grid has one CTA per row block, the longest first; a CTA that runs out
       // of work takes a block that has not started (the hardware hands them out),
       // so the setup and the pipeline's ends are paid once per SM and the order of
       // the grid still balances the load. A cluster works on its one block.
-      int64_t item = blockIdx.x / (unsigned)splits;
+      int64_t item = first_item;
       int n = 0, tries = 0;
       bool ok = true;
       auto publish = [&](const Work& w) {
@@ -525,7 +538,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       };
       while (ok) {
         Work w;
-        w.blk = P.cu ? find_prompt_block(P, item, tpi) : find_tree_block(P, item, tpi);
+        w.blk = item == first_item ? first_blk
+                : P.cu             ? find_prompt_block(P, item, tpi)
+                                   : find_tree_block(P, item, tpi);
         if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
         if (w.blk.cnt > 0) {
           const int T = (w.blk.kv_len + kTileKeys - 1) / kTileKeys;
@@ -754,11 +769,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     }
   } else if (kOut && warp >= kSoftmaxWarps) {
     // ------------------------------------------------------------ output
-    regs_dec<96>();
+    regs_dec<104>();
     const int wq = warp & 3, row = wq * 32 + lane;
     const int tok_q = row / P.group, g_q = row - tok_q * P.group;  // token in its tile, query head in its group
-    uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)wq * kWarpOut);
-    int outs[2] = {0, 0}, stats[2] = {0, 0};
+    int outs[2] = {0, 0}, stats[2] = {0, 0}, uses = 0;
     bool ok = true;
     Work w;
     while (wq < wpt && ok && next_work(w)) {
@@ -785,14 +799,49 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         const int tok = q * P.tpt + tok_q;
         if (splits > 1) {
           write_partial(t_o, q, row, x.x, x.y, w.nt > 0 && wq * 32 < rows);
-        } else if (wq * 32 < rows) {
-          write_rows(P, t_o, stage, orow0, row < rows ? tok * P.heads + g_q : -1, x.x, x.y, &C.ofree[q]);
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&C.ofree[q]);
+          continue;
         }
+        // A full tile leaves as two tensor stores: written by the warps themselves, its
+        // 32 KB hold up the softmax warps' exponentials in the same queue. A ragged one
+        // may not write behind its last token.
+        const bool whole = rows == P.group * P.tpt;
+        const float inv = row_scale(x.y);
+        const int mine = row < rows ? tok * P.heads + g_q : -1;
+        uint64_t check[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (uses > 0) {
+            if (wq == 0 && lane == 0) {
+              bulk_wait_read<1>();  // the store before the last one is done reading this buffer
+              mbar_arrive(&C.unstaged[half]);
+            }
+            ok = __all_sync(kFull, mbar_wait(&C.unstaged[half], (uint32_t)((uses - 1) & 1), ctl, P.status));
+            if (!ok) break;
+          }
+          uint4* slab = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)half * kSlabBytes) + wq * (kWarpOut / 16);
+          stage_half(t_o + (uint32_t)half * 64, slab, pack2(inv, inv), check, half ? &C.ofree[q] : nullptr);
+          if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (!whole && wq * 32 < rows) write_half(P, slab, orow0, mine, half);
+          if (lane == 0) mbar_arrive(&C.staged[half]);
+          if (wq == 0) {
+            ok = __all_sync(kFull, mbar_wait(&C.staged[half], (uint32_t)(uses & 1), ctl, P.status));
+            if (!ok) break;
+            if (lane == 0) {
+              if (whole)
+                tma_store_3d(&P.omap, smem_u32(smem + lay.out) + (uint32_t)half * kSlabBytes, 64 * half,
+                             blk.h * P.group, (int)(blk.row0 + q * P.tpt));
+              bulk_commit();
+            }
+          }
+        }
+        if (!ok) break;
+        ++uses;
+        if (mine >= 0) write_lse(P, orow0 + mine, x.x, x.y, check);
       }
     }
+    if (wq == 0 && lane == 0) bulk_wait_all();
+    __syncwarp();
     if (splits > 1) {
       __syncwarp();
       cluster_sync();
@@ -800,7 +849,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<NQ == 1 ? 216 : 184>();
+    regs_inc<NQ == 1 ? 208 : 176>();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
@@ -950,9 +999,21 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       if (splits > 1) {
         write_partial(t_o, q, row, m, l, nt > 0 && active);
       } else if (active) {
-        uint4* stage = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)(warp & 3) * kWarpOut);
-        write_rows(P, t_o, stage, blk.row0 * P.heads + (int64_t)blk.h * P.group, valid ? tok * P.heads + g_q : -1, m, l,
-                   &C.ofree[q]);
+        // rows go out through shared memory: 8 lanes write 128 bytes of a row at a time
+        // instead of every lane 16 bytes of its own row
+        uint4* slab = reinterpret_cast<uint4*>(smem + lay.out) + (warp & 3) * (kWarpOut / 16);
+        const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
+        const int mine = valid ? tok * P.heads + g_q : -1;
+        const float inv = row_scale(l);
+        uint64_t check[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          stage_half(t_o + (uint32_t)half * 64, slab, pack2(inv, inv), check, half ? &C.ofree[q] : nullptr);
+          __syncwarp();
+          write_half(P, slab, orow0, mine, half);
+          __syncwarp();
+        }
+        if (valid) write_lse(P, orow0 + mine, m, l, check);
       } else {
         __syncwarp();
         if (lane == 0) mbar_arrive(&C.ofree[q]);
@@ -1059,6 +1120,8 @@ bool encode_attend_maps(AttendParams& p, const void* q, int64_t q_stride, const 
   const cuuint64_t row = (cuuint64_t)kD * 2;
   const cuuint64_t heads = (cuuint64_t)p.batch * p.kv_heads, plane = (cuuint64_t)p.max_cache * row;
   return one(&p.qmap, q, (cuuint64_t)p.heads, row, (cuuint64_t)p.total, (cuuint64_t)q_stride * 2,
+             (cuuint32_t)p.group, (cuuint32_t)p.tpt) &&
+         one(&p.omap, p.out, (cuuint64_t)p.heads, row, (cuuint64_t)p.total, (cuuint64_t)p.heads * row,
              (cuuint32_t)p.group, (cuuint32_t)p.tpt) &&
          one(&p.kmap, K, (cuuint64_t)p.max_cache, row, heads, plane, (cuuint32_t)kTileKeys, 1) &&
          one(&p.vmap, V, (cuuint64_t)p.max_cache, row, heads, plane, (cuuint32_t)kTileKeys, 1);
