@@ -32,6 +32,12 @@ struct AttendParams {
 // nq: 128-row tiles per CTA (1 or 2); splits: CTAs per row block (1..16, a
 // cluster), each taking a share of the keys; items: row blocks to launch.
 cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s);
+constexpr int kSms = 152;  // GB300
+// CTAs that share an SM: with few rows a CTA waits for its keys most of the time,
+// and two hide each other's latencies with three K/V stages each. More rows leave
+// two CTAs only two stages; one CTA with six is faster (64 sequences of 80 rows over
+// 1040 slots: 56.5 against 59.1 us).
+constexpr int attend_ctas_per_sm(int nq, int rows) { return nq == 1 && rows <= 32 ? 2 : 1; }
 // K/V ring stages that fit beside the rest of a CTA's shared memory.
 int attend_stages(int nq, int group, int tpt);
 // Fills p's tensor maps (host only). False on failure.

@@ -38,8 +38,6 @@ bkv_status zero_status(uint32_t* status, cudaStream_t s) {
   return BKV_OK;
 }
 
-constexpr int kSlots1 = 2 * 152;  // CTAs of one tile that GB300 holds at once (two per SM)
-constexpr int kSlots2 = 152;      // CTAs of two tiles
 
 }  // namespace
 
@@ -83,8 +81,14 @@ bkv_status bkv_store_kv(const bkv_config* cfg, const void* q_pre, int64_t q_stri
   p.kv_heads = c.kv_heads;
   p.max_cache = c.max_cache;
   p.total = total;
+  // theta^(-2i/d) as theta^(-16a/d) theta^(-2b/d), i = 8a + b: 16 powers, one more rounding
+  double coarse[8], fine[8];
+  for (int i = 0; i < 8; ++i) {
+    coarse[i] = std::pow(c.rope_theta, -16.0 * i / (double)c.d) * 0.15915494309189535;  // 1 / (2 pi)
+    fine[i] = std::pow(c.rope_theta, -2.0 * i / (double)c.d);
+  }
   for (int i = 0; i < bkv::kRopePairs; ++i) {
-    double turns = std::pow(c.rope_theta, -2.0 * i / (double)c.d) * 0.15915494309189535;  // 1 / (2 pi)
+    double turns = coarse[i / 8] * fine[i % 8];
     turns -= std::floor(turns);
     p.turns[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0ull;
   }
@@ -118,7 +122,7 @@ bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_str
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.d));
   // row blocks of nq tiles: at most total / (nq tpt) full ones and one ragged one per sequence
   auto items_of = [&](int nq) { return ((int64_t)total / (nq * p.tpt) + c.batch) * c.kv_heads; };
-  const int nq = items_of(2) > kSlots2 / 2 && p.tpt < total ? 2 : 1;
+  const int nq = items_of(2) > bkv::kSms / 2 && p.tpt < total ? 2 : 1;
   const int64_t items = items_of(nq);
   if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
   p.stages = bkv::attend_stages(nq, p.group, p.tpt);
@@ -162,7 +166,7 @@ bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_strid
   const int64_t items = (int64_t)c.batch * c.kv_heads * p.qblocks;
   if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
   // keys split over a cluster while CTAs are fewer than the GPU holds
-  const int slots = nq == 1 ? kSlots1 : kSlots2, tiles = (c.max_cache + 127) / 128;
+  const int slots = bkv::kSms * bkv::attend_ctas_per_sm(nq, p.group * p.tpt), tiles = (c.max_cache + 127) / 128;
   int splits = 1;
   while (splits < 16 && items * splits * 2 <= slots && splits * 2 <= tiles) splits *= 2;
   p.stages = bkv::attend_stages(nq, p.group, p.tpt);

@@ -165,7 +165,7 @@ __device__ __forceinline__ void take_block(void* result, uint64_t* bar) {
                : "memory");
 }
 // The block taken, or -1: none is left.
-__device__ __forceinline__ int64_t taken_block(const void* result) {
+__device__ __forceinline__ int taken_block(const void* result) {
   uint32_t got, x;
   asm volatile(
       "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z, w;\n .reg .b64 lo, hi;\n"
@@ -175,7 +175,7 @@ __device__ __forceinline__ int64_t taken_block(const void* result) {
       : "=r"(got), "=r"(x)
       : "r"(smem_u32(result))
       : "memory");
-  return got ? (int64_t)x : -1;
+  return got ? (int)x : -1;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -225,11 +225,11 @@ struct Block {
 
 // Prompt: row blocks sequence by sequence, the last (longest) first. Every warp
 // runs this; items beyond the last block return cnt = 0.
-__device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int64_t item, int tpi) {
+__device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int item, int tpi) {
   const int lane = threadIdx.x & 31;
   Block k;
-  k.h = (int)(item % P.kv_heads);
-  int64_t at = item / P.kv_heads;
+  k.h = item % P.kv_heads;
+  int at = item / P.kv_heads;
   k.b = 0;
   k.row0 = 0;
   k.cnt = k.past = k.L = k.nodes = k.kv_len = k.i0 = 0;
@@ -262,7 +262,7 @@ __device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int64_
       const int blocks = __shfl_sync(kFull, nb, src);
       const int n = __shfl_sync(kFull, len, src);
       const int beg = __shfl_sync(kFull, begin, src);
-      const int qb = blocks - 1 - ((int)at - before);
+      const int qb = blocks - 1 - (at - before);
       k.i0 = qb * tpi;
       k.row0 = (int64_t)beg + k.i0;
       k.cnt = min(tpi, n - k.i0);
@@ -279,12 +279,11 @@ __device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int64_
   return k;
 }
 
-__device__ __forceinline__ Block find_tree_block(const AttendParams& P, int64_t item, int tpi) {
+__device__ __forceinline__ Block find_tree_block(const AttendParams& P, int item, int tpi) {
   Block k;
-  const int qb = (int)(item % P.qblocks);
-  const int64_t u = item / P.qblocks;
-  k.h = (int)(u % P.kv_heads);
-  k.b = (int)(u / P.kv_heads);
+  const int qb = item % P.qblocks, u = item / P.qblocks;
+  k.h = u % P.kv_heads;
+  k.b = u / P.kv_heads;
   const int len = P.first[k.b];
   const int nn = P.nodes ? P.nodes[k.b] : P.n;
   const int used = min(max(nn, 0), P.n);
@@ -474,7 +473,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   if (warp == kIssuer) tmem_alloc(&ctl->tmem_base, kCols);
   if (warp == kProducer && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.qmap : lane == 1 ? &P.kmap : &P.vmap) : "memory");
-  const int64_t first_item = blockIdx.x / (unsigned)splits;
+  const int first_item = (int)(blockIdx.x / (unsigned)splits);
   Block first_blk;
   if (warp == kScheduler) first_blk = P.cu ? find_prompt_block(P, first_item, tpi) : find_tree_block(P, first_item, tpi);
   tc_fence_before();
@@ -524,7 +523,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       // of work takes a block that has not started (the hardware hands them out),
       // so the setup and the pipeline's ends are paid once per SM and the order of
       // the grid still balances the load. A cluster works on its one block.
-      int64_t item = first_item;
+      int item = first_item;
       int n = 0, tries = 0;
       bool ok = true;
       auto publish = [&](const Work& w) {
@@ -544,8 +543,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
         if (w.blk.cnt > 0) {
           const int T = (w.blk.kv_len + kTileKeys - 1) / kTileKeys;
-          w.t_lo = (int)((int64_t)T * rank / splits);
-          w.nt = (int)((int64_t)T * (rank + 1) / splits) - w.t_lo;
+          // splits <= 16 and T < 2^24: no overflow
+          w.t_lo = T * rank / splits;
+          w.nt = T * (rank + 1) / splits - w.t_lo;
           publish(w);
           if (ok && splits == 1) ok = __all_sync(kFull, mbar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl, P.status));
         }
@@ -1041,20 +1041,28 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             float M = mc;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-            // a share without a visible key has no part in the sums (its O is not written or zero)
+            // a share without a visible key has no part in the sums
             const float wt = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
-            float l = 0.f;
+            float l = wt * lc;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < splits; ++c) {
-              const float wc = __shfl_sync(kFull, wt, c), lcc = __shfl_sync(kFull, lc, c);
-              if (wc == 0.f) continue;
-              l = fmaf(wc, lcc, l);
-              const float4 x = ld_cluster4(
-                  map_rank(part + ((uint32_t)(t * 128 + r) * 32 + (uint32_t)(lane ^ (r & 31))) * 16, (uint32_t)c));
-              o.x = fmaf(wc, x.x, o.x);
-              o.y = fmaf(wc, x.y, o.y);
-              o.z = fmaf(wc, x.z, o.z);
-              o.w = fmaf(wc, x.w, o.w);
+            const uint32_t mine = part + ((uint32_t)(t * 128 + r) * 32 + (uint32_t)(lane ^ (r & 31))) * 16;
+            for (int c0 = 0; c0 < splits; c0 += 8) {  // eight loads on their way at a time
+              float4 x[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (c0 + c < splits) x[c] = ld_cluster4(map_rank(mine, (uint32_t)(c0 + c)));
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float wc = __shfl_sync(kFull, wt, (c0 + c) & 31);
+                if (c0 + c < splits && wc != 0.f) {  // a share without weight may not have written its O
+                  o.x = fmaf(wc, x[c].x, o.x);
+                  o.y = fmaf(wc, x[c].y, o.y);
+                  o.z = fmaf(wc, x[c].z, o.z);
+                  o.w = fmaf(wc, x[c].w, o.w);
+                }
+              }
             }
             const float inv = row_scale(l);
             o.x *= inv;
@@ -1085,11 +1093,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 
 }  // namespace
 
-// K/V stages that fit. Two CTAs of one tile share an SM's 228 KB; fewer than the
-// most would fit three there, and three ask for more TMEM columns (256 each) than
-// it has.
+// K/V stages that fit. Two CTAs share an SM's 228 KB; fewer stages than the most
+// would fit three there, and three ask for more TMEM columns (256 each) than it has.
 int attend_stages(int nq, int group, int tpt) {
-  const uint32_t room = nq == 1 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
+  const uint32_t room = attend_ctas_per_sm(nq, group * tpt) == 2 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
   int n = kMaxStages;
   while (n > 0 && attend_smem(nq, group, tpt, n).total > room) --n;
   return n;
