@@ -223,58 +223,73 @@ struct Block {
   bool bad;      // a length had to be clamped
 };
 
-// Prompt: row blocks sequence by sequence, the last (longest) first. Every warp
-// runs this; items beyond the last block return cnt = 0.
-__device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int item, int tpi) {
+// Where a search for a prompt's row block may begin: `before` blocks lie in the
+// sequences before b0.
+struct Cursor {
+  int b0 = 0, before = 0;
+};
+
+// Prompt: row blocks sequence by sequence, the last (longest) first. One warp, 128
+// sequences a step. Items behind the last block return cnt = 0.
+__device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int item, int tpi, Cursor& cur) {
   const int lane = threadIdx.x & 31;
   Block k;
   k.h = item % P.kv_heads;
-  int at = item / P.kv_heads;
+  const int at = item / P.kv_heads;
   k.b = 0;
   k.row0 = 0;
   k.cnt = k.past = k.L = k.nodes = k.kv_len = k.i0 = 0;
   k.bad = false;
-  for (int b0 = 0; b0 < P.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int begin = 0, len = 0, nb = 0;
-    bool bad = false;
-    if (b < P.batch) {
-      const int lo = P.cu[b], hi = P.cu[b + 1];
-      begin = min(max(lo, 0), P.total);
-      const int end = min(max(hi, begin), P.total);
-      len = end - begin;
-      bad = begin != lo || end != hi;
-      nb = (len + tpi - 1) / tpi;
+  if (at < cur.before) cur = Cursor{};
+  for (; cur.b0 < P.batch; cur.b0 += 128) {
+    const int b = cur.b0 + 4 * lane;  // this lane's four sequences
+    int edge[5], nb[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) edge[i] = P.cu[min(b + i, P.batch)];
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int begin = min(max(edge[i], 0), P.total), end = min(max(edge[i + 1], begin), P.total);
+      if (b + i < P.batch) k.bad |= begin != edge[i] || end != edge[i + 1];
+      nb[i] = b + i < P.batch ? (end - begin + tpi - 1) / tpi : 0;
+      sum += nb[i];
     }
-    int sum = nb;
+    int upto = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(kFull, sum, off);
-      if (lane >= off) sum += y;
+      const int y = __shfl_up_sync(kFull, upto, off);
+      if (lane >= off) upto += y;
     }
-    const unsigned hit = __ballot_sync(kFull, at < sum);
-    const bool any_bad = __any_sync(kFull, bad);
-    k.bad |= any_bad;
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      k.b = b0 + src;
-      const int before = __shfl_sync(kFull, sum - nb, src);
-      const int blocks = __shfl_sync(kFull, nb, src);
-      const int n = __shfl_sync(kFull, len, src);
-      const int beg = __shfl_sync(kFull, begin, src);
-      const int qb = blocks - 1 - (at - before);
-      k.i0 = qb * tpi;
-      k.row0 = (int64_t)beg + k.i0;
-      k.cnt = min(tpi, n - k.i0);
-      const int f = P.first[k.b];
-      const int fc = min(max(f, 0), P.max_cache);
-      k.past = fc + k.i0;  // at most max_cache + total
-      k.L = 0;
-      k.kv_len = (int)min((int64_t)k.past + k.cnt, (int64_t)P.max_cache);
-      k.bad |= fc != f || (int64_t)k.past + k.cnt > P.max_cache;
-      return k;
+    k.bad = __any_sync(kFull, k.bad);
+    const unsigned hit = __ballot_sync(kFull, at - cur.before < upto);
+    if (!hit) {
+      cur.before += __shfl_sync(kFull, upto, 31);
+      continue;
     }
-    at -= __shfl_sync(kFull, sum, 31);
+    // the lane that has the block, then which of its four sequences
+    const int src = __ffs(hit) - 1;
+    int left = at - cur.before - (upto - sum), which = 0, blocks = nb[0], beg = edge[0], end = edge[1];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (which == i - 1 && left >= nb[i - 1]) {
+        left -= nb[i - 1];
+        which = i;
+        blocks = nb[i];
+        beg = edge[i];
+        end = edge[i + 1];
+      }
+    k.b = __shfl_sync(kFull, b + which, src);
+    beg = min(max(__shfl_sync(kFull, beg, src), 0), P.total);
+    end = min(max(__shfl_sync(kFull, end, src), beg), P.total);
+    k.i0 = (__shfl_sync(kFull, blocks, src) - 1 - __shfl_sync(kFull, left, src)) * tpi;
+    k.row0 = (int64_t)beg + k.i0;
+    k.cnt = min(tpi, end - beg - k.i0);
+    const int f = P.first[k.b];
+    const int fc = min(max(f, 0), P.max_cache);
+    k.past = fc + k.i0;
+    k.kv_len = (int)min((int64_t)k.past + k.cnt, (int64_t)P.max_cache);
+    k.bad |= fc != f || (int64_t)k.past + k.cnt > P.max_cache;
+    return k;
   }
   return k;
 }
@@ -475,7 +490,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.qmap : lane == 1 ? &P.kmap : &P.vmap) : "memory");
   const int first_item = (int)(blockIdx.x / (unsigned)splits);
   Block first_blk;
-  if (warp == kScheduler) first_blk = P.cu ? find_prompt_block(P, first_item, tpi) : find_tree_block(P, first_item, tpi);
+  Cursor cursor;
+  if (warp == kScheduler)
+    first_blk = P.cu ? find_prompt_block(P, first_item, tpi, cursor) : find_tree_block(P, first_item, tpi);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -538,7 +555,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       while (ok) {
         Work w;
         w.blk = item == first_item ? first_blk
-                : P.cu             ? find_prompt_block(P, item, tpi)
+                : P.cu             ? find_prompt_block(P, item, tpi, cursor)
                                    : find_tree_block(P, item, tpi);
         if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
         if (w.blk.cnt > 0) {
