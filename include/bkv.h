@@ -370,9 +370,10 @@ bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_strid
  * i < count[b], in every layer; other slots stay. The caller adds count[b] to
  * its lengths (and appends the accepted tokens' queries, bkv_append_queries).
  *   K, V:  host arrays of `layers` device pointers, as bkv_evict.
+ *   n:     nodes of the tree, 1 .. 64, as in bkv_attend_tree.
  *   path:  device int32 [batch][n]: node indices 0 .. n - 1 in any order, a node
  *          may appear twice; entries at and behind count[b] are not read.
- *   count: device int32 [batch], 0 .. n; n: 1 .. 64. */
+ *   count: device int32 [batch], 0 .. n. */
 bkv_status bkv_commit_tree(const bkv_config* cfg, void* const* K, void* const* V, const int32_t* cache_lens,
                            const int32_t* path, const int32_t* count, int32_t n, uint32_t* status,
                            void* cuda_stream);
