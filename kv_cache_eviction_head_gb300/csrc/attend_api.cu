@@ -39,6 +39,19 @@ bkv_status zero_status(uint32_t* status, cudaStream_t s) {
 }
 
 
+// CTAs per row block: the keys are split over a cluster while all clusters run at
+// once. GB300's GPCs hold 7 clusters of 16, 15 of 8, 36 of 4 and 76 of 2 at one CTA
+// per SM, twice that at two; one cluster too many waits for a whole other one (one
+// node of 16 KV heads over 2063 slots: 14.9 us in clusters of 16, 10.0 in clusters of
+// 8). Two CTAs per SM take 32 clusters of 8 well (11.5 us, 12.2 in clusters of 4).
+int splits_for(int64_t items, int ctas_per_sm, int max_cache) {
+  const int tiles = (max_cache + 127) / 128;
+  const int64_t most[4] = {7 * ctas_per_sm, ctas_per_sm == 2 ? 32 : 15, 36 * ctas_per_sm, 76 * ctas_per_sm};
+  for (int i = 0; i < 4; ++i)
+    if (items <= most[i] && (16 >> i) <= tiles) return 16 >> i;
+  return 1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,7 +143,9 @@ bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_str
   if (total > 0 && !bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
   if (total == 0) return BKV_OK;
-  return bkv::launch_attend(p, nq, 1, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+  // a few tokens behind a long context leave most of the GPU idle unless their keys are split
+  const int splits = splits_for(items, bkv::attend_ctas_per_sm(nq, p.group * p.tpt), c.max_cache);
+  return bkv::launch_attend(p, nq, splits, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 
 bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K, const void* V,
@@ -165,10 +180,7 @@ bkv_status bkv_attend_tree(const bkv_config* cfg, const void* q, int64_t q_strid
   p.qblocks = (n + nq * p.tpt - 1) / (nq * p.tpt);
   const int64_t items = (int64_t)c.batch * c.kv_heads * p.qblocks;
   if (items > 0x7FFFFFFF / 16) return BKV_ERR_UNSUPPORTED;
-  // keys split over a cluster while CTAs are fewer than the GPU holds
-  const int slots = bkv::kSms * bkv::attend_ctas_per_sm(nq, p.group * p.tpt), tiles = (c.max_cache + 127) / 128;
-  int splits = 1;
-  while (splits < 16 && items * splits * 2 <= slots && splits * 2 <= tiles) splits *= 2;
+  const int splits = splits_for(items, bkv::attend_ctas_per_sm(nq, p.group * p.tpt), c.max_cache);
   p.stages = bkv::attend_stages(nq, p.group, p.tpt);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (!bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;

@@ -91,6 +91,13 @@ def test_prompt_two_tiles_per_block(bkv, heads, kv):
     assert prompt_case(bkv, heads, kv, lens, first, 5, extra=1) <= 0
 
 
+@pytest.mark.parametrize("heads,kv", [(7, 1), (32, 8)])
+@pytest.mark.parametrize("lens,first", [([1], [4000]), ([5, 0, 3], [3000, 900, 0]), ([40, 70], [1500, 127])])
+def test_prompt_chunks_behind_a_long_context(bkv, heads, kv, lens, first):
+    """Few row blocks: their keys are split over clusters."""
+    assert prompt_case(bkv, heads, kv, lens, first, 6, extra=2) <= 0
+
+
 def test_prompt_large_logits(bkv):
     """Logits of some hundreds, whose running maximum moves from tile to tile."""
     assert prompt_case(bkv, 8, 2, [400, 90], [0, 200], 8, scale=40.0) <= 0
