@@ -1038,62 +1038,66 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     }
     if (splits > 1) {
       // ---------------------------------------------------------- join
+      // Rank r joins rows r, r + splits, ...; a warp takes 32 / splits of them at a time,
+      // so that all their statistics come in one load per lane (lane = row, share). The
+      // loops over rows stay loops: in a short call, code is as far away as data.
       __syncwarp();
       cluster_sync();
-      // every CTA of the cluster had the same block; w is the work before the end mark
-      const Block blk = C.work[0].blk;
+      const Block blk = C.work[0].blk;  // every CTA of the cluster had the same block
       if (!ctl->abort && blk.cnt > 0) {
         const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;
         const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
+        const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
+        const int sh = 31 - __clz(splits), share = lane & (splits - 1);  // splits: a power of two
         for (int t = 0; t < nq; ++t) {
           const int n = min(blk.cnt - t * P.tpt, P.tpt) * P.group;
-          // rank r joins rows r, r + splits, ...; one warp per row, 4 columns per lane
-          for (int r = rank + warp * splits; r < n; r += splits * kSoftmaxWarps) {
-            float mc = kNegInf, lc = 0.f;
-            if (lane < splits) {
-              const float2 x = ld_cluster2(map_rank(mls + (uint32_t)(t * 128 + r) * 8, (uint32_t)lane));
-              mc = x.x;
-              lc = x.y;
+          for (int k = warp; rank + k * splits < n; k += kSoftmaxWarps << (5 - sh)) {
+            auto row_at = [&](int i) { return rank + (k + i * kSoftmaxWarps) * splits; };  // i-th of the warp's rows
+            auto out_row = [&](int r) { return orow0 + (int64_t)(t * P.tpt + r / P.group) * P.heads + r % P.group; };
+            const int r = row_at(lane >> sh);
+            float2 x = make_float2(kNegInf, 0.f);
+            if (r < n) x = ld_cluster2(map_rank(mls + (uint32_t)(t * 128 + r) * 8, (uint32_t)share));
+            float M = x.x;
+            for (int off = splits >> 1; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+            // a share without a visible key has no part in the sums (its sum is 0, or NaN)
+            float wt = x.x == kNegInf ? x.y : fast_exp2(x.x - M);
+            float l = wt * x.y;
+            for (int off = splits >> 1; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+            wt = wt == 0.f ? 0.f : wt * row_scale(l);
+            if (r < n && share == 0) {
+              const float lse = row_lse(M, l);
+              const int64_t orow = out_row(r);
+              if (P.lse && BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) P.lse[orow] = lse;
+              if (!(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
             }
-            float M = mc;
+#pragma unroll 1
+            for (int i = 0; i < 32 >> sh && row_at(i) < n; ++i) {
+              const int rr = row_at(i);
+              const uint32_t at = part + ((uint32_t)(t * 128 + rr) * 32 + (uint32_t)(lane ^ (rr & 31))) * 16;
+              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+              for (int c0 = 0; c0 < splits; c0 += 8) {
+                float4 y[8];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-            // a share without a visible key has no part in the sums
-            const float wt = mc == kNegInf ? lc : fast_exp2(mc - M);  // lc: 0, or NaN
-            float l = wt * lc;
+                for (int c = 0; c < 8; ++c)
+                  if (c0 + c < splits) y[c] = ld_cluster4(map_rank(at, (uint32_t)(c0 + c)));
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            const uint32_t mine = part + ((uint32_t)(t * 128 + r) * 32 + (uint32_t)(lane ^ (r & 31))) * 16;
-            for (int c0 = 0; c0 < splits; c0 += 8) {  // eight loads on their way at a time
-              float4 x[8];
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                if (c0 + c < splits) x[c] = ld_cluster4(map_rank(mine, (uint32_t)(c0 + c)));
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float wc = __shfl_sync(kFull, wt, (c0 + c) & 31);
-                if (c0 + c < splits && wc != 0.f) {  // a share without weight may not have written its O
-                  o.x = fmaf(wc, x[c].x, o.x);
-                  o.y = fmaf(wc, x[c].y, o.y);
-                  o.z = fmaf(wc, x[c].z, o.z);
-                  o.w = fmaf(wc, x[c].w, o.w);
+                for (int c = 0; c < 8; ++c) {
+                  const float wc = __shfl_sync(kFull, wt, (i << sh) + ((c0 + c) & (splits - 1)));
+                  if (c0 + c < splits && wc != 0.f) {  // a share without weight may not have written its O
+                    o.x = fmaf(wc, y[c].x, o.x);
+                    o.y = fmaf(wc, y[c].y, o.y);
+                    o.z = fmaf(wc, y[c].z, o.z);
+                    o.w = fmaf(wc, y[c].w, o.w);
+                  }
                 }
               }
+              const int64_t orow = out_row(rr);
+              if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
+              reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+              const float check = (o.x * 0.f + o.y * 0.f) + (o.z * 0.f + o.w * 0.f);
+              if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
             }
-            const float inv = row_scale(l);
-            o.x *= inv;
-            o.y *= inv;
-            o.z *= inv;
-            o.w *= inv;
-            const int tok = t * P.tpt + r / P.group;
-            const int64_t orow = (blk.row0 + tok) * P.heads + (int64_t)blk.h * P.group + r % P.group;
-            if (!BKV_IN_RANGE(orow >= 0 && orow < (int64_t)P.total * P.heads, P.status)) continue;
-            reinterpret_cast<uint2*>(P.out)[orow * 32 + lane] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            const float lse = row_lse(M, l);
-            if (P.lse && lane == 0) P.lse[orow] = lse;
-            const float check = (o.x + o.y + o.z + o.w) * 0.f;
-            if (check != 0.f || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
           }
         }
       }
