@@ -18,18 +18,42 @@
 // The reference maximum only moves when a tile's maximum exceeds it by more
 // than 8 (a factor 256 in P, which costs bf16 and fp32 no precision); O and
 // the sum are rescaled then. The QK^T of a tile is issued after the PV of the
-// tile before, so a row that has its logits may rescale O without further
-// synchronisation.
+// tile before (one thread's MMAs run in the order of issue), so a row that has
+// its logits may rescale O without further synchronisation.
 //
-// Warps: 4 per 128-row tile for softmax and epilogue, one TMA producer, one
-// MMA issuer (and two idle ones, so that registers can move by warpgroup). K and V tiles alternate in one ring of 32 KB stages.
+// Two instances. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
+// 33.5 MMAC, 30 bytes per clock and SM), their MMAs alternate, and 512 TMEM
+// columns hold both S and both O. NQ = 1: one tile, 256 columns, for few rows;
+// up to 32 rows two CTAs share an SM. Warps: 4 per tile for softmax, 4 for the
+// output (NQ = 2; with one tile the softmax warps write it), one TMA producer,
+// one MMA issuer, one scheduler. K and V tiles alternate in one ring of 32 KB
+// stages.
 //
-// Few rows: the keys of a row block are split over the CTAs of a cluster; each
-// keeps its own maximum, sum and O, and the partial results are joined through
-// distributed shared memory, in rank order, so results do not vary.
+// Few row blocks: the keys of a block are split over the CTAs of a cluster;
+// each keeps its own maximum, sum and O, and the partial results are joined
+// through distributed shared memory, in rank order, so results do not vary.
 //
 // Slots at or behind the last visible one may hold anything: their logits are
 // replaced, not added to, and their V rows are zeroed in shared memory.
+//
+// Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16):
+//   two prompts of 8,190 tokens, 28/4 heads       625 us   1.52 PFLOP/s, 0.79
+//   8 prompts of 1,240 - 2,064 tokens, 32/8       173 us   1.14 PFLOP/s, 0.59
+//   64 trees of 64 nodes over 4,112 slots, 28/4   196 us   1.11 PFLOP/s, 0.57
+//   192 sequences decoding over 2,063 slots       234 us   6.60 TB/s,    0.97
+// Decoding is bound by HBM. Prompts: between two key tiles a row tile's products
+// take 2 x 512 clocks; its softmax 1,000 - 1,200 (in isolation 910: 430 of
+// exponentials, 160 maximum, 170 TMEM, 95 sums), the hand-overs 300. The two
+// tiles alternate, so a pair of key tiles takes about 2,450 clocks instead of the
+// products' 2,048. Each row block adds about 6,000 (queries, first logits, ragged
+// last tile, both tiles' softmax at once), which is what short prompts lose. At
+// this rate the board runs at its power limit (1,360 W) and 1.9 GHz.
+// Without the uniform issuer (below) the long prompts took 764 us, with one thread
+// computing descriptors in a branch 882, with the whole row unpacked 995.
+// Measured and not kept (the long prompts, against 625 us): half a row per thread, 691; three
+// hand-overs per tile, 669; two issuers, 832; logits read twice from TMEM in
+// rolled loops (fewer instruction-cache misses), 653; the next block's first
+// product before the other tile's last one, 656.
 #include <atomic>
 
 #include "attend/attend.cuh"
