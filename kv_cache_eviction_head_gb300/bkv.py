@@ -302,10 +302,27 @@ def bkv_score_select_noalloc(cfg: BkvConfig, bq, rq, beacons: int, recents: int,
            "bkv_score_select_noalloc")
 
 
+class _Lazy:
+    """torch and what the short calls below use of it, looked up once: their host time is
+    most of a decode step's, and an import statement or a chain of attributes per argument
+    is a good part of that."""
+    torch = None
+
+
+def _load():
+    import torch
+    _Lazy.bf16, _Lazy.i32, _Lazy.i64, _Lazy.f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+    _Lazy.Tensor, _Lazy.torch = torch.Tensor, torch
+    return _Lazy
+
+
+def _device():
+    return (_Lazy if _Lazy.torch is not None else _load()).torch.cuda.current_device()
+
+
 def _check_on_device(t, name: str, dtype, shape, device):
     """_check_tensor, and that t lives on the current device (kernels launch there).
-    Returns its address. The first test passes without building a message: a decode
-    step's calls are short, and this is most of their host time."""
+    Returns its address. The first test passes without building a message."""
     try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
             return t.data_ptr()
@@ -315,34 +332,34 @@ def _check_on_device(t, name: str, dtype, shape, device):
     raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
 
 
-def _check_caches(ts, name: str, cfg, shape, device):
-    """A _vp array of `layers` bf16 caches of this shape on this device. The attributes of
+def _check_caches(ts, name: str, n: int, shape, device):
+    """A _vp array of n per-layer bf16 caches of this shape on this device. The attributes of
     all layers are gathered by C-level maps; on a mismatch the layers are looked at one by
     one for the message."""
-    import torch
-    T = torch.Tensor
-    n = cfg.layers
+    T = _Lazy.Tensor
     if len(ts) != n:
         raise ValueError(f"{name}: expected {n} per-layer tensors, got {len(ts)}")
     try:
         if (list(map(T.size, ts)) == [shape] * n and list(map(T.get_device, ts)) == [device] * n
-                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} == {torch.bfloat16}):
+                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} == {_Lazy.bf16}):
             return (_vp * n).from_buffer(array("Q", map(T.data_ptr, ts)))
     except (TypeError, AttributeError):
         pass
-    return (_vp * n)(*[_check_on_device(t, f"{name}[{l}]", torch.bfloat16, shape, device) for l, t in enumerate(ts)])
+    return (_vp * n)(*[_check_on_device(t, f"{name}[{l}]", _Lazy.bf16, shape, device) for l, t in enumerate(ts)])
 
 
 def _check_packed(t, name: str, shape, device):
     """Raises ValueError unless t is a bf16 tensor of this shape on this device whose heads
     and elements are contiguous and whose tokens are evenly spaced; returns its address and
     the elements between two tokens."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    ok = t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device
+    try:
+        ok = t.dtype is _Lazy.bf16 and t.shape == shape and t.get_device() == device
+        if ok and t.is_contiguous():
+            return t.data_ptr(), shape[-2] * shape[-1]
+    except AttributeError:
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}") from None
     stride = shape[-2] * shape[-1]
-    if ok and not t.is_contiguous():
+    if ok:
         s = t.stride()
         # a dimension of one element may have any stride
         ok = s[-1] == 1 and (s[-2] == shape[-1] or shape[-2] == 1)
@@ -360,14 +377,12 @@ def _check_packed(t, name: str, shape, device):
     return t.data_ptr(), stride
 
 
-def _optional(t, name: str, dtype, shape, device) -> int:
-    return 0 if t is None else _check_on_device(t, name, dtype, shape, device)
-
-
-def _packed_total(t, name: str) -> int:
-    if getattr(t, "ndim", 0) != 3:
-        raise ValueError(f"{name}: expected a tensor [tokens][heads][d]")
-    return t.shape[0]
+def _dims(t, name: str, shape: str, n: int):
+    """t's shape, if it has n dimensions."""
+    s = getattr(t, "shape", ())
+    if len(s) != n:
+        raise ValueError(f"{name}: expected a tensor {shape}")
+    return s
 
 
 def bkv_store_kv(cfg: BkvConfig, q_pre, k_pre, v, cu_seqlens, first_slot, first_pos, q_rot, K, V, *,
@@ -377,22 +392,23 @@ def bkv_store_kv(cfg: BkvConfig, q_pre, k_pre, v, cu_seqlens, first_slot, first_
     [total][heads][d]; cu_seqlens int32 [batch + 1]; first_slot, first_pos int32 [batch];
     depth: optional int32 [total]; K, V: one layer's bf16 caches
     [batch][kv_heads][max_cache][d]; status: optional int32 of one element."""
-    import torch
-    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
-    total = _packed_total(q_pre, "q_pre")
-    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
-    q, qs = _check_packed(q_pre, "q_pre", (total, c.heads, c.d), dev)
-    k, ks = _check_packed(k_pre, "k_pre", (total, c.kv_heads, c.d), dev)
-    vv, vs = _check_packed(v, "v", (total, c.kv_heads, c.d), dev)
+    dev = _device()
+    bf16, i32 = _Lazy.bf16, _Lazy.i32
+    batch, heads, kv, d = cfg.batch, cfg.heads, cfg.kv_heads, cfg.d
+    total = _dims(q_pre, "q_pre", "[tokens][heads][d]", 3)[0]
+    cache, rows, one = (batch, kv, cfg.max_cache, d), (total, kv, d), (batch,)
+    q, qs = _check_packed(q_pre, "q_pre", (total, heads, d), dev)
+    k, ks = _check_packed(k_pre, "k_pre", rows, dev)
+    vv, vs = _check_packed(v, "v", rows, dev)
     _check(_lib.bkv_store_kv(
-        ctypes.byref(c), q, qs, k, ks, vv, vs, total,
-        _check_on_device(cu_seqlens, "cu_seqlens", i32, (c.batch + 1,), dev),
-        _check_on_device(first_slot, "first_slot", i32, (c.batch,), dev),
-        _check_on_device(first_pos, "first_pos", i32, (c.batch,), dev),
-        _optional(depth, "depth", i32, (total,), dev),
-        _check_on_device(q_rot, "q_rot", torch.bfloat16, (total, c.heads, c.d), dev),
-        _check_on_device(K, "K", torch.bfloat16, cache, dev), _check_on_device(V, "V", torch.bfloat16, cache, dev),
-        _optional(status, "status", i32, (1,), dev), _stream_ptr(stream)), "bkv_store_kv")
+        cfg, q, qs, k, ks, vv, vs, total, _check_on_device(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, one, dev),
+        _check_on_device(first_pos, "first_pos", i32, one, dev),
+        None if depth is None else _check_on_device(depth, "depth", i32, (total,), dev),
+        _check_on_device(q_rot, "q_rot", bf16, (total, heads, d), dev), _check_on_device(K, "K", bf16, cache, dev),
+        _check_on_device(V, "V", bf16, cache, dev),
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_store_kv")
 
 
 def bkv_attend_prompt(cfg: BkvConfig, q, K, V, cu_seqlens, first_slot, out, *, lse=None, status=None,
@@ -401,19 +417,20 @@ def bkv_attend_prompt(cfg: BkvConfig, q, K, V, cu_seqlens, first_slot, out, *, l
     q [total][heads][d]: rotated queries, bf16, tokens any multiple of 8 elements apart;
     out bf16 [total][heads][d]; lse: optional float32 [total][heads]; the others as
     bkv_store_kv."""
-    import torch
-    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
-    total = _packed_total(q, "q")
-    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
-    qp, qs = _check_packed(q, "q", (total, c.heads, c.d), dev)
+    dev = _device()
+    bf16, i32 = _Lazy.bf16, _Lazy.i32
+    batch, heads, d = cfg.batch, cfg.heads, cfg.d
+    total = _dims(q, "q", "[tokens][heads][d]", 3)[0]
+    cache, rows = (batch, cfg.kv_heads, cfg.max_cache, d), (total, heads, d)
+    qp, qs = _check_packed(q, "q", rows, dev)
     _check(_lib.bkv_attend_prompt(
-        ctypes.byref(c), qp, qs, _check_on_device(K, "K", torch.bfloat16, cache, dev),
-        _check_on_device(V, "V", torch.bfloat16, cache, dev),
-        _check_on_device(cu_seqlens, "cu_seqlens", i32, (c.batch + 1,), dev),
-        _check_on_device(first_slot, "first_slot", i32, (c.batch,), dev), total,
-        _check_on_device(out, "out", torch.bfloat16, (total, c.heads, c.d), dev),
-        _optional(lse, "lse", torch.float32, (total, c.heads), dev), _optional(status, "status", i32, (1,), dev),
-        _stream_ptr(stream)), "bkv_attend_prompt")
+        cfg, qp, qs, _check_on_device(K, "K", bf16, cache, dev), _check_on_device(V, "V", bf16, cache, dev),
+        _check_on_device(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, (batch,), dev), total,
+        _check_on_device(out, "out", bf16, rows, dev),
+        None if lse is None else _check_on_device(lse, "lse", _Lazy.f32, (total, heads), dev),
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_attend_prompt")
 
 
 def bkv_attend_tree(cfg: BkvConfig, q, K, V, cache_lens, out, *, mask=None, nodes=None, lse=None, status=None,
@@ -422,39 +439,37 @@ def bkv_attend_tree(cfg: BkvConfig, q, K, V, cache_lens, out, *, mask=None, node
     caches (see include/bkv.h). q: rotated queries, bf16 [batch][n][heads][d]; cache_lens
     int32 [batch]; mask: optional int64 [batch][n]; nodes: optional int32 [batch]; out bf16
     [batch][n][heads][d]; lse: optional float32 [batch][n][heads]."""
-    import torch
-    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
-    if getattr(q, "ndim", 0) != 4:
-        raise ValueError("q: expected a tensor [batch][n][heads][d]")
-    n = q.shape[1]
-    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
-    qp, qs = _check_packed(q, "q", (c.batch, n, c.heads, c.d), dev)
+    dev = _device()
+    bf16, i32 = _Lazy.bf16, _Lazy.i32
+    batch, heads, d = cfg.batch, cfg.heads, cfg.d
+    n = _dims(q, "q", "[batch][n][heads][d]", 4)[1]
+    cache, rows = (batch, cfg.kv_heads, cfg.max_cache, d), (batch, n, heads, d)
+    qp, qs = _check_packed(q, "q", rows, dev)
     _check(_lib.bkv_attend_tree(
-        ctypes.byref(c), qp, qs, _check_on_device(K, "K", torch.bfloat16, cache, dev),
-        _check_on_device(V, "V", torch.bfloat16, cache, dev),
-        _check_on_device(cache_lens, "cache_lens", i32, (c.batch,), dev), n,
-        _optional(mask, "mask", torch.int64, (c.batch, n), dev), _optional(nodes, "nodes", i32, (c.batch,), dev),
-        _check_on_device(out, "out", torch.bfloat16, (c.batch, n, c.heads, c.d), dev),
-        _optional(lse, "lse", torch.float32, (c.batch, n, c.heads), dev),
-        _optional(status, "status", i32, (1,), dev), _stream_ptr(stream)), "bkv_attend_tree")
+        cfg, qp, qs, _check_on_device(K, "K", bf16, cache, dev), _check_on_device(V, "V", bf16, cache, dev),
+        _check_on_device(cache_lens, "cache_lens", i32, (batch,), dev), n,
+        None if mask is None else _check_on_device(mask, "mask", _Lazy.i64, (batch, n), dev),
+        None if nodes is None else _check_on_device(nodes, "nodes", i32, (batch,), dev),
+        _check_on_device(out, "out", bf16, rows, dev),
+        None if lse is None else _check_on_device(lse, "lse", _Lazy.f32, (batch, n, heads), dev),
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_attend_tree")
 
 
 def bkv_commit_tree(cfg: BkvConfig, K, V, cache_lens, path, count, *, status=None, stream=None) -> None:
     """Keeps an accepted path in every layer (see include/bkv.h). K, V: `layers` bf16
     caches [batch][kv_heads][max_cache][d]; cache_lens, count int32 [batch]; path int32
     [batch][n]."""
-    import torch
-    c, dev, i32 = cfg, torch.cuda.current_device(), torch.int32
-    if getattr(path, "ndim", 0) != 2:
-        raise ValueError("path: expected a tensor [batch][n]")
-    n = path.shape[1]
-    cache = (c.batch, c.kv_heads, c.max_cache, c.d)
-    kp, vp = _check_caches(K, "K", c, cache, dev), _check_caches(V, "V", c, cache, dev)
+    dev = _device()
+    i32, batch, layers = _Lazy.i32, cfg.batch, cfg.layers
+    n = _dims(path, "path", "[batch][n]", 2)[1]
+    cache = (batch, cfg.kv_heads, cfg.max_cache, cfg.d)
+    kp, vp = _check_caches(K, "K", layers, cache, dev), _check_caches(V, "V", layers, cache, dev)
     _check(_lib.bkv_commit_tree(
-        ctypes.byref(c), kp, vp, _check_on_device(cache_lens, "cache_lens", i32, (c.batch,), dev),
-        _check_on_device(path, "path", i32, (c.batch, n), dev),
-        _check_on_device(count, "count", i32, (c.batch,), dev), n, _optional(status, "status", i32, (1,), dev),
-        _stream_ptr(stream)), "bkv_commit_tree")
+        cfg, kp, vp, _check_on_device(cache_lens, "cache_lens", i32, (batch,), dev),
+        _check_on_device(path, "path", i32, (batch, n), dev), _check_on_device(count, "count", i32, (batch,), dev), n,
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_commit_tree")
 
 
 def bkv_get_stats(h: Handle) -> BkvStats:

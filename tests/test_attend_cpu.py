@@ -124,6 +124,7 @@ def test_packed_strides_and_devices(bkv):
         f = x.as_subclass(FakeCuda)
         f.at = at
         return f
+    bkv._load()
     wide = torch.zeros((5, 12, 128), dtype=torch.bfloat16)
     assert bkv._check_packed(fake(wide[:, :8]), "q", (5, 8, 128), 0)[1] == 12 * 128
     assert bkv._check_packed(fake(wide[:1, :8]), "q", (1, 8, 128), 0)[1] == 8 * 128  # one token: any spacing
