@@ -10,6 +10,22 @@ namespace bkv {
 constexpr int kMaxNodes = 64;    // one 64-bit ancestor mask per node
 constexpr int kMaxGroup = 128;   // query heads per KV head: one token's rows fit a 128-row tile
 
+// Programmatic dependent launch. These kernels are short and follow one another, so
+// the next one's blocks may start (and set up barriers and TMEM) while the one
+// before still runs: depend_wait() returns when everything before this kernel in
+// its stream is complete and visible, and stands before every access to memory
+// that other kernels may have written or still read; depend_go() lets the next
+// kernel's blocks start once every block of this one has come so far. Between
+// kernels that do not take part, launches are ordered as ever.
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void depend_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+inline cudaLaunchAttribute dependent_launch() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 struct AttendParams {
   CUtensorMap qmap;        // queries [tokens][heads][d], box (64, group, tpt)
   CUtensorMap omap;        // out, the same box

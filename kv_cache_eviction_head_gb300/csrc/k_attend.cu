@@ -460,6 +460,7 @@ __global__ void __launch_bounds__(NQ * 128 + (output_warps(NQ) ? 256 : 128), NQ 
 attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles: 1 KB aligned
   if (smem_u32(smem) & 1023u) {
+    depend_wait();
     latch(P.status, BKV_ERR_INTERNAL);
     return;
   }
@@ -512,6 +513,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   if (warp == kIssuer) tmem_alloc(&ctl->tmem_base, kCols);
   if (warp == kProducer && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.qmap : lane == 1 ? &P.kmap : &P.vmap) : "memory");
+  depend_wait();
   const int first_item = (int)(blockIdx.x / (unsigned)splits);
   Block first_blk;
   Cursor cursor;
@@ -521,6 +523,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);
+  // With its TMEM allocated: a later kernel's block on this SM must not get there first
+  depend_go();
 
   // The next piece of work; false: none is left, or a wait ran out. Every lane of
   // a warp gets it; one arrival per warp frees the slot.
@@ -1199,12 +1203,13 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
   cfg.blockDim = dim3((unsigned)(nq * 128 + (output_warps(nq) ? 256 : 128)));
   cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)splits;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0] = dependent_launch();
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)splits;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
   return nq == 1 ? cudaLaunchKernelEx(&cfg, attend_kernel<1>, p, splits) : cudaLaunchKernelEx(&cfg, attend_kernel<2>, p, splits);
 }
 

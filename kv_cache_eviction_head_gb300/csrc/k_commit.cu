@@ -26,6 +26,8 @@ __global__ void __launch_bounds__(kThreadsCommit) commit_kernel(const __grid_con
   const int tid = threadIdx.x;
   const int part = tid & 15, r = tid >> 5;
   uint4* base = ((tid & 16) ? P.V[layer] : P.K[layer]) + ((int64_t)b * P.kv_heads + h) * P.max_cache * 16 + part;
+  depend_wait();
+  depend_go();
   const int len = P.lens[b], given = P.count[b];
   const int count = min(max(given, 0), P.n);
   bool bad = count != given || len < 0;
@@ -54,8 +56,14 @@ __global__ void __launch_bounds__(kThreadsCommit) commit_kernel(const __grid_con
 
 cudaError_t launch_commit(const CommitParams& p, cudaStream_t s) {
   const int64_t units = (int64_t)p.layers * p.batch * p.kv_heads;
-  commit_kernel<<<(unsigned)units, kThreadsCommit, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3(kThreadsCommit);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, commit_kernel, p);
 }
 
 }  // namespace bkv

@@ -49,6 +49,8 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
   const int rows = P.heads + 2 * P.kv_heads;
   const int part = tid % kRowThreads;  // elements [8 part, 8 part + 8) and their partners 64 on
   uint4 lo[kAhead], hi[kAhead];
+  depend_wait();
+  depend_go();
   auto load = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -123,11 +125,15 @@ cudaError_t launch_store(const StoreParams& p, cudaStream_t s) {
   // a decode step's tokens one to a block with both passes' loads under way at once;
   // long prompts two to a block, eight blocks to an SM (26,700 tokens of 48 rows:
   // 105.7 us, 6.37 TB/s; one pass ahead in four-token blocks 107.8, two passes 113)
-  if (p.total <= 8 * kSms)
-    store_kernel<1, 2><<<(unsigned)p.total, kThreadsStore, 0, s>>>(p);
-  else
-    store_kernel<2, 1><<<(unsigned)((p.total + 1) / 2), kThreadsStore, 0, s>>>(p);
-  return cudaGetLastError();
+  const int per_block = p.total <= 8 * kSms ? 1 : 2;
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((p.total + per_block - 1) / per_block));
+  cfg.blockDim = dim3(kThreadsStore);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return per_block == 1 ? cudaLaunchKernelEx(&cfg, store_kernel<1, 2>, p) : cudaLaunchKernelEx(&cfg, store_kernel<2, 1>, p);
 }
 
 }  // namespace bkv
