@@ -1204,12 +1204,17 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
   cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
-  at[0] = dependent_launch();
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)splits;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
+  if (splits > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = (unsigned)splits;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  // One tile: short calls (one sequence decoding 12.3 -> 9.6 us, 64 trees of 16 nodes
+  // 56.5 -> 54.1). Two tiles keep their order of launch: back to back, 8 prompts took 176 us
+  // without it and 180 with it.
+  if (nq == 1) at[cfg.numAttrs++] = dependent_launch();
   return nq == 1 ? cudaLaunchKernelEx(&cfg, attend_kernel<1>, p, splits) : cudaLaunchKernelEx(&cfg, attend_kernel<2>, p, splits);
 }
 
