@@ -38,7 +38,7 @@
 //
 // Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16):
 //   two prompts of 8,190 tokens, 28/4 heads       625 us   1.52 PFLOP/s, 0.79
-//   8 prompts of 1,240 - 2,064 tokens, 32/8       173 us   1.14 PFLOP/s, 0.59
+//   8 prompts of 1,359 - 2,064 tokens, 32/8       173 us   1.14 PFLOP/s, 0.59
 //   64 trees of 64 nodes over 4,112 slots, 28/4   196 us   1.11 PFLOP/s, 0.57
 //   192 sequences decoding over 2,063 slots       234 us   6.60 TB/s,    0.97
 // Decoding is bound by HBM. Prompts: between two key tiles a row tile's products

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
 
 cudaError_t launch_store(const StoreParams& p, cudaStream_t s) {
   // a decode step's tokens one to a block with both passes' loads under way at once;
-  // long prompts two to a block, eight blocks to an SM (26,700 tokens of 48 rows:
+  // long prompts two to a block, eight blocks to an SM (27,380 tokens of 48 rows:
   // 105.7 us, 6.37 TB/s; one pass ahead in four-token blocks 107.8, two passes 113)
   const int per_block = p.total <= 8 * kSms ? 1 : 2;
   cudaLaunchAttribute at = dependent_launch();
