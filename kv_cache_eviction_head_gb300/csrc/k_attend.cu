@@ -62,6 +62,24 @@
 namespace bkv {
 namespace {
 
+// A wait of this kernel: bounded like mbar_wait, in a third of its instructions
+// (there are forty of them; with the others the kernel was 118 KB of code). A wait
+// that runs out raises the abort flag; the status is latched once, at the end.
+__device__ __forceinline__ uint32_t clock32() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl* ctl) {
+  if (mbar_test(b, parity)) return true;
+  const uint32_t t0 = clock32();
+  do {
+    if (mbar_test(b, parity)) return true;
+  } while (!ctl->abort && clock32() - t0 < (uint32_t)kWaitCycles);
+  ctl->abort = 1;
+  return false;
+}
+
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;  // log2 units by which the reference maximum may lag
@@ -484,12 +502,14 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   const int wpt = (P.group * P.tpt + 31) / 32;  // softmax warps with rows in a full tile
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], 1);
     }
     mbar_init(&C.qfull, 1);
     mbar_init(&C.qempty, 1);
+#pragma unroll 1
     for (int q = 0; q < NQ; ++q) {
       mbar_init(&C.sfull[q], 1);
       mbar_init(&C.pfull[q][0], (uint32_t)wpt);
@@ -498,6 +518,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       mbar_init(&C.ofree[q], (uint32_t)wpt);
       mbar_init(&C.rfull[q], (uint32_t)wpt);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.wfull[i], 1);
       mbar_init(&C.staged[i], (uint32_t)wpt);
@@ -515,23 +536,22 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.qmap : lane == 1 ? &P.kmap : &P.vmap) : "memory");
   depend_wait();
   const int first_item = (int)(blockIdx.x / (unsigned)splits);
-  Block first_blk;
-  Cursor cursor;
-  if (warp == kScheduler)
-    first_blk = P.cu ? find_prompt_block(P, first_item, tpi, cursor) : find_tree_block(P, first_item, tpi);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);
-  // With its TMEM allocated: a later kernel's block on this SM must not get there first
-  depend_go();
+  // Every warp's start: barriers and TMEM are there. The scheduler comes to it with
+  // the first block found.
+  auto start = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    depend_go();  // with the TMEM allocated: a later kernel's block on this SM must not get there first
+    return __shfl_sync(kFull, ctl->tmem_base, 0);
+  };
 
   // The next piece of work; false: none is left, or a wait ran out. Every lane of
   // a warp gets it; one arrival per warp frees the slot.
   int works = 0;
   auto next_work = [&](Work& w) {
     const int slot = works & 1;
-    if (!__all_sync(kFull, mbar_wait(&C.wfull[slot], (uint32_t)((works >> 1) & 1), ctl, P.status))) return false;
+    if (!__all_sync(kFull, bar_wait(&C.wfull[slot], (uint32_t)((works >> 1) & 1), ctl))) return false;
     w = C.work[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&C.wempty[slot]);
@@ -570,10 +590,12 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       // the grid still balances the load. A cluster works on its one block.
       int item = first_item;
       int n = 0, tries = 0;
+      bool started = false;
+      Cursor cursor;
       bool ok = true;
       auto publish = [&](const Work& w) {
         const int slot = n & 1;
-        if (n >= 2) ok = __all_sync(kFull, mbar_wait(&C.wempty[slot], (uint32_t)(((n >> 1) - 1) & 1), ctl, P.status));
+        if (n >= 2) ok = __all_sync(kFull, bar_wait(&C.wempty[slot], (uint32_t)(((n >> 1) - 1) & 1), ctl));
         if (ok && lane == 0) {
           C.work[slot] = w;
           mbar_arrive(&C.wfull[slot]);
@@ -582,9 +604,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       };
       while (ok) {
         Work w;
-        w.blk = item == first_item ? first_blk
-                : P.cu             ? find_prompt_block(P, item, tpi, cursor)
-                                   : find_tree_block(P, item, tpi);
+        w.blk = P.cu ? find_prompt_block(P, item, tpi, cursor) : find_tree_block(P, item, tpi);
+        if (!started) start();
+        started = true;
         if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
         if (w.blk.cnt > 0) {
           const int T = (w.blk.kv_len + kTileKeys - 1) / kTileKeys;
@@ -592,7 +614,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           w.t_lo = T * rank / splits;
           w.nt = T * (rank + 1) / splits - w.t_lo;
           publish(w);
-          if (ok && splits == 1) ok = __all_sync(kFull, mbar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl, P.status));
+          if (ok && splits == 1) ok = __all_sync(kFull, bar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl));
         }
         if (!ok || splits > 1) break;
         if (lane == 0) {
@@ -600,7 +622,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last name has been read
           take_block(&C.block, &C.taken);
         }
-        ok = __all_sync(kFull, mbar_wait(&C.taken, (uint32_t)(tries & 1), ctl, P.status));
+        ok = __all_sync(kFull, bar_wait(&C.taken, (uint32_t)(tries & 1), ctl));
         if (!ok) {  // the name must land before the CTA exits
           const long long t0 = clock64();
           while (!mbar_test(&C.taken, (uint32_t)(tries & 1)) && clock64() - t0 < kWaitCycles) {
@@ -619,6 +641,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       }
     } else if (warp == kProducer) {
       // ---------------------------------------------------------- TMA producer
+      start();
       const uint64_t pol = policy_evict_normal();
       const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
       int st = 0, items = 0;
@@ -630,10 +653,12 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (lane == 0 && w.nt > 0) {
           const Block& blk = w.blk;
           const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;
-          if (items > 0) ok = mbar_wait(&C.qempty, (uint32_t)((items - 1) & 1), ctl, P.status);
+          if (items > 0) ok = bar_wait(&C.qempty, (uint32_t)((items - 1) & 1), ctl);
           if (ok) {
             mbar_expect_tx(&C.qfull, (uint32_t)nq * 2 * qbytes);
+#pragma unroll 1
             for (int q = 0; q < nq; ++q)
+#pragma unroll 1
               for (int s = 0; s < 2; ++s)
                 tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
                             (int)(blk.row0 + q * P.tpt), &C.qfull, pol);
@@ -641,9 +666,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           }
           const int z = blk.b * P.kv_heads + blk.h;
           const int call = 2 * w.nt > 8 ? 2 * w.nt - 8 : 0;  // four tiles before the end
+#pragma unroll 1
           for (int i = 0; i < 2 * w.nt && ok; ++i) {
             if (i == call) mbar_arrive(&C.want);
-            if (g >= S) ok = mbar_wait(&C.empty[st], ph ^ 1u, ctl, P.status);
+            if (g >= S) ok = bar_wait(&C.empty[st], ph ^ 1u, ctl);
             if (!ok) break;
             mbar_expect_tx(&C.full[st], kTileBytes);
             const uint32_t dst = smem_u32(ring) + (uint32_t)st * kTileBytes;
@@ -664,6 +690,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         long long t0 = clock64();
         while (items > 0 && !mbar_test(&C.qfull, (uint32_t)((items - 1) & 1)) && clock64() - t0 < kWaitCycles) {
         }
+#pragma unroll 1
         for (int s = 0; s < S && s < g; ++s) {
           const long long last = g - 1 - ((g - 1 - s) % S);
           t0 = clock64();
@@ -677,6 +704,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       // shows up as idle time: the waits on K and V stages sit in the middle of a
       // product whose MMAs are queued, and only the waits for probabilities stand
       // between two products.
+      const uint32_t tmem = start();
       constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
       const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
       const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
@@ -699,7 +727,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         umma_ts<8, 128>(s + 128, p, b, id_pv, 1u, el);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(kFull, mbar_wait(bar, parity, ctl, P.status));
+        return __all_sync(kFull, bar_wait(bar, parity, ctl));
       };
       auto step = [&](int& st, uint32_t& ph) {
         if (++st == S) {
@@ -707,7 +735,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           ph ^= 1u;
         }
       };
-      int items = 0, tiles[2] = {0, 0}, outs[2] = {0, 0};  // per row tile: key tiles and row blocks done
+      int items = 0;
+      // per row tile, one bit each: parity of the key tiles and of the row blocks done,
+      // and whether there was one
+      uint32_t tiles = 0, outs = 0, any = 0;
       int st = 0;  // next stage of the ring
       uint32_t ph = 0;
       bool ok = true, issued = false;
@@ -720,21 +751,23 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (!ok) break;
         tc_fence_after();
         issued = true;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (q < nq) {
-            issue_qk(q, st, 0);
-            issue_qk(q, st, 1);
-            umma_commit_if(&C.sfull[q], el);
-          }
+#pragma unroll 1
+        for (int q = 0; q < nq; ++q) {
+          issue_qk(q, st, 0);
+          issue_qk(q, st, 1);
+          umma_commit_if(&C.sfull[q], el);
+        }
         umma_commit_if(&C.empty[st], el);
         if (nt == 1) umma_commit_if(&C.qempty, el);
         step(st, ph);
         int sv = st;  // stage of V_j; K_{j+1} follows
         ok = wait(&C.full[sv], ph);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)  // the last block's O has been read
-          if (q < nq && outs[q]++ > 0) ok = ok && wait(&C.ofree[q], (uint32_t)(outs[q] & 1));
+#pragma unroll 1
+        for (int q = 0; q < nq; ++q)  // the last block's O has been read
+          if ((any >> q) & 1u) ok = ok && wait(&C.ofree[q], ((outs >> q) & 1u) ^ 1u);
+        any |= nq == 2 ? 3u : 1u;
+        outs ^= nq == 2 ? 3u : 1u;
+#pragma unroll 1
         for (int j = 0; j + 1 < nt && ok; ++j) {
           step(st, ph);
           const int sk = st;  // stages of K_{j+1} and V_{j+1}
@@ -743,7 +776,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= nq || !ok) break;
-            const uint32_t par = (uint32_t)((tiles[q] + j) & 1);
+            const uint32_t par = ((tiles >> q) ^ (uint32_t)j) & 1u;
             ok = wait(&C.pfull[q][0], par);
             if (!ok) break;
             tc_fence_after();
@@ -772,6 +805,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         const int live = w.blk.kv_len - (w.t_lo + nt - 1) * kTileKeys;
         if (live < kTileKeys) {
           uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
+#pragma unroll 1
           for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
             rows[i] = make_uint4(0, 0, 0, 0);
             rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
@@ -779,11 +813,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q >= nq || !ok) break;
-          const uint32_t par = (uint32_t)((tiles[q] + nt - 1) & 1);
-          tiles[q] += nt;
+#pragma unroll 1
+        for (int q = 0; q < nq; ++q) {
+          const uint32_t par = ((tiles >> q) ^ (uint32_t)(nt - 1)) & 1u;
           ok = wait(&C.pfull[q][0], par);
           if (!ok) break;
           tc_fence_after();
@@ -797,6 +829,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           umma_commit_if(&C.ofull[q], el);
         }
         umma_commit_if(&C.empty[sv], el);
+        if (nt & 1) tiles ^= nq == 2 ? 3u : 1u;
       }
       if (!ok && issued) {
         // after an abort, let the MMAs already issued finish before the TMEM is freed
@@ -806,6 +839,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         }
       }
       __syncwarp();
+    } else {
+      start();
     }
     if (splits > 1) {  // the join's two barriers, see below
       __syncwarp();
@@ -815,28 +850,29 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   } else if (kOut && warp >= kSoftmaxWarps) {
     // ------------------------------------------------------------ output
     regs_dec<104>();
+    const uint32_t tmem = start();
     const int wq = warp & 3, row = wq * 32 + lane;
     const int tok_q = row / P.group, g_q = row - tok_q * P.group;  // token in its tile, query head in its group
-    int outs[2] = {0, 0}, stats[2] = {0, 0}, uses = 0;
+    uint32_t outs = 0, stats = 0;  // parities, one bit per tile
+    int uses = 0;
     bool ok = true;
     Work w;
     while (wq < wpt && ok && next_work(w)) {
       const Block& blk = w.blk;
       const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
       const int nq = blk.cnt <= P.tpt ? 1 : 2;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (q >= nq || !ok) break;
+#pragma unroll 1
+      for (int q = 0; q < nq; ++q) {
         const int rows = min(blk.cnt - q * P.tpt, P.tpt) * P.group;
         const uint32_t t_o = tmem + ((uint32_t)wq << 21) + (uint32_t)q * 256 + 128;
-        ok = __all_sync(kFull, mbar_wait(&C.rfull[q], (uint32_t)(stats[q] & 1), ctl, P.status));
-        ++stats[q];
+        ok = __all_sync(kFull, bar_wait(&C.rfull[q], (stats >> q) & 1u, ctl));
+        stats ^= 1u << q;
         if (ok && w.nt > 0) {
-          ok = __all_sync(kFull, mbar_wait(&C.ofull[q], (uint32_t)(outs[q] & 1), ctl, P.status));
+          ok = __all_sync(kFull, bar_wait(&C.ofull[q], (outs >> q) & 1u, ctl));
           // a cluster's partial results go where the other tile's V may still be read
           if (ok && splits > 1 && nq == 2)
-            ok = __all_sync(kFull, mbar_wait(&C.ofull[q ^ 1], (uint32_t)(outs[q] & 1), ctl, P.status));
-          ++outs[q];
+            ok = __all_sync(kFull, bar_wait(&C.ofull[q ^ 1], (outs >> q) & 1u, ctl));
+          outs ^= 1u << q;
           tc_fence_after();
         }
         if (!ok) break;
@@ -860,7 +896,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
               bulk_wait_read<1>();  // the store before the last one is done reading this buffer
               mbar_arrive(&C.unstaged[half]);
             }
-            ok = __all_sync(kFull, mbar_wait(&C.unstaged[half], (uint32_t)((uses - 1) & 1), ctl, P.status));
+            ok = __all_sync(kFull, bar_wait(&C.unstaged[half], (uint32_t)((uses - 1) & 1), ctl));
             if (!ok) break;
           }
           uint4* slab = reinterpret_cast<uint4*>(smem + lay.out + (uint32_t)half * kSlabBytes) + wq * (kWarpOut / 16);
@@ -870,7 +906,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           if (!whole && wq * 32 < rows) write_half(P, slab, orow0, mine, half);
           if (lane == 0) mbar_arrive(&C.staged[half]);
           if (wq == 0) {
-            ok = __all_sync(kFull, mbar_wait(&C.staged[half], (uint32_t)(uses & 1), ctl, P.status));
+            ok = __all_sync(kFull, bar_wait(&C.staged[half], (uint32_t)(uses & 1), ctl));
             if (!ok) break;
             if (lane == 0) {
               if (whole)
@@ -895,6 +931,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<NQ == 1 ? 208 : 176>();
+    const uint32_t tmem = start();
     const int q = NQ == 1 ? 0 : warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
@@ -927,8 +964,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       // tiles that end at or below every row's bound need no mask
       const int lim_min = P.mask ? blk.L : min(blk.past + q * P.tpt + 1, blk.kv_len);
       float m = kNegInf, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < nt; ++j) {
-        ok = __all_sync(kFull, mbar_wait(&C.sfull[q], (uint32_t)(tiles & 1), ctl, P.status));
+        ok = __all_sync(kFull, bar_wait(&C.sfull[q], (uint32_t)(tiles & 1), ctl));
         ++tiles;
         if (!ok) break;
         if (!active) {
@@ -1027,7 +1065,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       if (!ok) break;
       if (kOut) {
         // the output warps have read the last block's statistics
-        if (outs > 0) ok = __all_sync(kFull, mbar_wait(&C.ofree[q], (uint32_t)((outs - 1) & 1), ctl, P.status));
+        if (outs > 0) ok = __all_sync(kFull, bar_wait(&C.ofree[q], (uint32_t)((outs - 1) & 1), ctl));
         ++outs;
         if (!ok) break;
         stats_s[q * 128 + row] = make_float2(m, l);
@@ -1036,7 +1074,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         continue;
       }
       if (nt > 0) {
-        ok = __all_sync(kFull, mbar_wait(&C.ofull[q], (uint32_t)(outs & 1), ctl, P.status));
+        ok = __all_sync(kFull, bar_wait(&C.ofull[q], (uint32_t)(outs & 1), ctl));
         ++outs;
         if (!ok) break;
         tc_fence_after();
@@ -1077,8 +1115,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         const uint32_t part = smem_u32(ring), mls = smem_u32(ml);
         const int64_t orow0 = blk.row0 * P.heads + (int64_t)blk.h * P.group;
         const int sh = 31 - __clz(splits), share = lane & (splits - 1);  // splits: a power of two
+#pragma unroll 1
         for (int t = 0; t < nq; ++t) {
           const int n = min(blk.cnt - t * P.tpt, P.tpt) * P.group;
+#pragma unroll 1
           for (int k = warp; rank + k * splits < n; k += kSoftmaxWarps << (5 - sh)) {
             auto row_at = [&](int i) { return rank + (k + i * kSoftmaxWarps) * splits; };  // i-th of the warp's rows
             auto out_row = [&](int r) { return orow0 + (int64_t)(t * P.tpt + r / P.group) * P.heads + r % P.group; };
@@ -1086,10 +1126,12 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             float2 x = make_float2(kNegInf, 0.f);
             if (r < n) x = ld_cluster2(map_rank(mls + (uint32_t)(t * 128 + r) * 8, (uint32_t)share));
             float M = x.x;
+#pragma unroll 1
             for (int off = splits >> 1; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
             // a share without a visible key has no part in the sums (its sum is 0, or NaN)
             float wt = x.x == kNegInf ? x.y : fast_exp2(x.x - M);
             float l = wt * x.y;
+#pragma unroll 1
             for (int off = splits >> 1; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
             wt = wt == 0.f ? 0.f : wt * row_scale(l);
             if (r < n && share == 0) {
@@ -1137,7 +1179,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssuer) tmem_dealloc(tmem, kCols);
+  if (warp == kIssuer) tmem_dealloc(ctl->tmem_base, kCols);
+  if (tid == 0 && ctl->abort) latch(P.status, BKV_ERR_TIMEOUT);
 }
 
 }  // namespace
