@@ -473,15 +473,19 @@ __device__ __forceinline__ void write_lse(const AttendParams& P, int64_t orow, f
   if (!(fabsf(a + b) < __builtin_huge_valf()) || !(lse < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
 }
 
-template <int NQ>
+// kTree: node masks and one length per sequence; else packed prompts. kCluster:
+// one row block per cluster of `splits` CTAs; else persistent CTAs, splits = 1. An
+// instance for each keeps the others' code out of the instruction caches.
+template <int NQ, bool kTree, bool kCluster>
 __global__ void __launch_bounds__(NQ * 128 + (output_warps(NQ) ? 256 : 128), NQ == 1 ? 2 : 1)
-attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
+attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
   extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles: 1 KB aligned
   if (smem_u32(smem) & 1023u) {
     depend_wait();
     latch(P.status, BKV_ERR_INTERNAL);
     return;
   }
+  const int splits = kCluster ? splits_given : 1;
   constexpr int kSoftmaxWarps = NQ * 4;
   constexpr bool kOut = output_warps(NQ);
   constexpr int kControl = kSoftmaxWarps + (kOut ? 4 : 0);  // first warp of the control warpgroup
@@ -604,7 +608,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       };
       while (ok) {
         Work w;
-        w.blk = P.cu ? find_prompt_block(P, item, tpi, cursor) : find_tree_block(P, item, tpi);
+        if constexpr (kTree) w.blk = find_tree_block(P, item, tpi);
+        else w.blk = find_prompt_block(P, item, tpi, cursor);
         if (!started) start();
         started = true;
         if (w.blk.bad && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
@@ -614,9 +619,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
           w.t_lo = T * rank / splits;
           w.nt = T * (rank + 1) / splits - w.t_lo;
           publish(w);
-          if (ok && splits == 1) ok = __all_sync(kFull, bar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl));
+          if (ok && !kCluster) ok = __all_sync(kFull, bar_wait(&C.want, (uint32_t)((n - 1) & 1), ctl));
         }
-        if (!ok || splits > 1) break;
+        if (!ok || kCluster) break;
         if (lane == 0) {
           mbar_expect_tx(&C.taken, 16);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last name has been read
@@ -842,7 +847,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     } else {
       start();
     }
-    if (splits > 1) {  // the join's two barriers, see below
+    if constexpr (kCluster) {  // the join's two barriers, see below
       __syncwarp();
       cluster_sync();
       cluster_sync();
@@ -870,7 +875,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (ok && w.nt > 0) {
           ok = __all_sync(kFull, bar_wait(&C.ofull[q], (outs >> q) & 1u, ctl));
           // a cluster's partial results go where the other tile's V may still be read
-          if (ok && splits > 1 && nq == 2)
+          if (kCluster && ok && nq == 2)
             ok = __all_sync(kFull, bar_wait(&C.ofull[q ^ 1], (outs >> q) & 1u, ctl));
           outs ^= 1u << q;
           tc_fence_after();
@@ -878,7 +883,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (!ok) break;
         const float2 x = stats_s[q * 128 + row];
         const int tok = q * P.tpt + tok_q;
-        if (splits > 1) {
+        if constexpr (kCluster) {
           write_partial(t_o, q, row, x.x, x.y, w.nt > 0 && wq * 32 < rows);
           continue;
         }
@@ -923,7 +928,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
     }
     if (wq == 0 && lane == 0) bulk_wait_all();
     __syncwarp();
-    if (splits > 1) {
+    if constexpr (kCluster) {
       __syncwarp();
       cluster_sync();
       cluster_sync();
@@ -955,14 +960,16 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
       const int tok = q * P.tpt + (valid ? tok_q : 0);
       // slots [0, lim) are visible, and the tree's slots L + i whose bit is set
       int lim = min(blk.past + tok + 1, blk.kv_len);
-      uint64_t bits = 0;
-      if (P.mask) {
-        lim = blk.L;
-        if (valid) bits = (uint64_t)P.mask[blk.row0 + tok];
-        if (blk.nodes < 64) bits &= (1ull << blk.nodes) - 1ull;
-      }
       // tiles that end at or below every row's bound need no mask
-      const int lim_min = P.mask ? blk.L : min(blk.past + q * P.tpt + 1, blk.kv_len);
+      int lim_min = min(blk.past + q * P.tpt + 1, blk.kv_len);
+      uint64_t bits = 0;
+      if constexpr (kTree) {
+        if (P.mask) {
+          lim = lim_min = blk.L;
+          if (valid) bits = (uint64_t)P.mask[blk.row0 + tok];
+          if (blk.nodes < 64) bits &= (1ull << blk.nodes) - 1ull;
+        }
+      }
       float m = kNegInf, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < nt; ++j) {
@@ -990,9 +997,11 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
             const int lo = base + 32 * c;
             const int n = min(max(lim - lo, 0), 32);
             uint32_t see = n >= 32 ? ~0u : (1u << n) - 1u;
-            const int sh = lo - blk.L;
-            if (sh >= 0) see |= sh < 64 ? (uint32_t)(bits >> sh) : 0u;
-            else if (sh > -32) see |= (uint32_t)(bits << -sh);
+            if constexpr (kTree) {
+              const int sh = lo - blk.L;
+              if (sh >= 0) see |= sh < 64 ? (uint32_t)(bits >> sh) : 0u;
+              else if (sh > -32) see |= (uint32_t)(bits << -sh);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[c][i] = (see >> i) & 1u ? v[c][i] : kNegInf;
           }
@@ -1079,7 +1088,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (!ok) break;
         tc_fence_after();
       }
-      if (splits > 1) {
+      if constexpr (kCluster) {
         write_partial(t_o, q, row, m, l, nt > 0 && active);
       } else if (active) {
         // rows go out through shared memory: 8 lanes write 128 bytes of a row at a time
@@ -1102,7 +1111,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits) {
         if (lane == 0) mbar_arrive(&C.ofree[q]);
       }
     }
-    if (splits > 1) {
+    if constexpr (kCluster) {
       // ---------------------------------------------------------- join
       // Rank r joins rows r, r + splits, ...; a warp takes 32 / splits of them at a time,
       // so that all their statistics come in one load per lane (lane = row, share). The
@@ -1226,29 +1235,31 @@ bool encode_attend_maps(AttendParams& p, const void* q, int64_t q_stride, const 
          one(&p.vmap, V, (cuuint64_t)p.max_cache, row, heads, plane, (cuuint32_t)kTileKeys, 1);
 }
 
-cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s) {
+namespace {
+
+template <int NQ, bool kTree, bool kCluster>
+cudaError_t launch_instance(const AttendParams& p, int splits, int64_t items, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const void* fn = nq == 1 ? reinterpret_cast<const void*>(attend_kernel<1>) : reinterpret_cast<const void*>(attend_kernel<2>);
-  // once per device and instance (one bit each)
-  static std::atomic<unsigned long long> configured[2] = {{0}, {0}};
+  const auto fn = attend_kernel<NQ, kTree, kCluster>;
+  static std::atomic<unsigned long long> configured{0};  // once per device (one bit each)
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(configured[nq - 1].load() & bit)) {
+  if (!(configured.load() & bit)) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && kCluster) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    configured[nq - 1].fetch_or(bit);
+    configured.fetch_or(bit);
   }
   if (p.stages < 2) return cudaErrorInvalidConfiguration;  // V_j and K_{j+1}
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * splits));
-  cfg.blockDim = dim3((unsigned)(nq * 128 + (output_warps(nq) ? 256 : 128)));
-  cfg.dynamicSmemBytes = attend_smem(nq, p.group, p.tpt, p.stages).total;
+  cfg.blockDim = dim3((unsigned)(NQ * 128 + (output_warps(NQ) ? 256 : 128)));
+  cfg.dynamicSmemBytes = attend_smem(NQ, p.group, p.tpt, p.stages).total;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
-  if (splits > 1) {
+  if (kCluster) {
     at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     at[cfg.numAttrs].val.clusterDim.x = (unsigned)splits;
     at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
@@ -1257,8 +1268,21 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
   // One tile: short calls (one sequence decoding 12.3 -> 9.6 us, 64 trees of 16 nodes
   // 56.5 -> 54.1). Two tiles keep their order of launch: back to back, 8 prompts took 176 us
   // without it and 180 with it.
-  if (nq == 1) at[cfg.numAttrs++] = dependent_launch();
-  return nq == 1 ? cudaLaunchKernelEx(&cfg, attend_kernel<1>, p, splits) : cudaLaunchKernelEx(&cfg, attend_kernel<2>, p, splits);
+  if (NQ == 1) at[cfg.numAttrs++] = dependent_launch();
+  return cudaLaunchKernelEx(&cfg, fn, p, splits);
+}
+
+template <int NQ, bool kTree>
+cudaError_t launch_tiles(const AttendParams& p, int splits, int64_t items, cudaStream_t s) {
+  return splits > 1 ? launch_instance<NQ, kTree, true>(p, splits, items, s)
+                    : launch_instance<NQ, kTree, false>(p, 1, items, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s) {
+  if (p.cu) return nq == 1 ? launch_tiles<1, false>(p, splits, items, s) : launch_tiles<2, false>(p, splits, items, s);
+  return nq == 1 ? launch_tiles<1, true>(p, splits, items, s) : launch_tiles<2, true>(p, splits, items, s);
 }
 
 }  // namespace bkv
