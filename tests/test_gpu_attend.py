@@ -339,3 +339,40 @@ def test_empty_calls(bkv):
     assert bool((out == 7).all())
     bkv.bkv_commit_tree(cfg, [K], [V], i32([4, 4]), i32([[0], [0]]), i32([0, 0]), stream=cs)
     assert torch.equal(K, K0) and torch.equal(V, V0)
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+def test_query_rows_of_nobody_reach_no_other_row(bkv, poison):
+    """Rows of unused nodes, of tokens around the sequences and of a neighbour sequence lie in
+    the same 128-row tiles: whatever they hold, the others' results keep their bits."""
+    cs = torch.cuda.current_stream()
+    for heads, kv, n, used in ((8, 2, 5, [2, 0, 5]), (40, 8, 64, [1, 40, 64])):
+        cfg = config(bkv, heads, kv, 3, 700)
+        K, V, q = randn((3, kv, 700, D), 1), randn((3, kv, 700, D), 2), randn((3, n, heads, D), 3)
+        outs = []
+        for fill in (0.0, poison):
+            x = q.clone()
+            for b, m in enumerate(used):
+                x[b, m:] = fill
+            out, lse, status = torch.full_like(q, 7.0), torch.full((3, n, heads), 7.0, device="cuda"), new_status()
+            bkv.bkv_attend_tree(cfg, x, K, V, i32([0, 300, 620]), out, nodes=i32(used), lse=lse, status=status, stream=cs)
+            assert int(status) == 0
+            outs.append((out, lse))
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        assert all(bool((outs[0][0][b, m:] == 7).all()) for b, m in enumerate(used))
+    for heads, kv, lens in ((8, 2, [20, 11, 30]), (32, 8, [200, 170, 65])):
+        cfg = config(bkv, heads, kv, 3, 700)
+        cu = [3, 3 + lens[0], 3 + lens[0] + lens[1], 3 + sum(lens)]
+        total = cu[-1] + 9
+        K, V, q = randn((3, kv, 700, D), 1), randn((3, kv, 700, D), 2), randn((total, heads, D), 3)
+        outs = []
+        for fill in (0.0, poison):
+            x = q.clone()
+            x[:cu[0]] = fill
+            x[cu[1]:cu[2]] = fill  # the sequence between the two that are compared
+            x[cu[3]:] = fill
+            out, status = torch.full_like(q, 7.0), new_status()
+            bkv.bkv_attend_prompt(cfg, x, K, V, i32(cu), i32([0, 5, 100]), out, status=status, stream=cs)
+            assert int(status) == (0 if fill == 0.0 else bkv.BKV_ERR_NONFINITE)
+            outs.append(torch.cat((out[:cu[1]], out[cu[2]:])))
+        assert torch.equal(*outs)
