@@ -36,24 +36,27 @@
 // Slots at or behind the last visible one may hold anything: their logits are
 // replaced, not added to, and their V rows are zeroed in shared memory.
 //
-// Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16):
-//   two prompts of 8,190 tokens, 28/4 heads       625 us   1.52 PFLOP/s, 0.79
-//   8 prompts of 1,359 - 2,064 tokens, 32/8       173 us   1.14 PFLOP/s, 0.59
-//   64 trees of 64 nodes over 4,112 slots, 28/4   196 us   1.11 PFLOP/s, 0.57
-//   192 sequences decoding over 2,063 slots       234 us   6.60 TB/s,    0.97
-// Decoding is bound by HBM. Prompts: between two key tiles a row tile's products
-// take 2 x 512 clocks; its softmax 1,000 - 1,200 (in isolation 910: 430 of
-// exponentials, 160 maximum, 170 TMEM, 95 sums), the hand-overs 300. The two
-// tiles alternate, so a pair of key tiles takes about 2,450 clocks instead of the
-// products' 2,048. Each row block adds about 6,000 (queries, first logits, ragged
-// last tile, both tiles' softmax at once), which is what short prompts lose. At
-// this rate the board runs at its power limit (1,360 W) and 1.9 GHz.
-// Without the uniform issuer (below) the long prompts took 764 us, with one thread
-// computing descriptors in a branch 882, with the whole row unpacked 995.
-// Measured and not kept (the long prompts, against 625 us): half a row per thread, 691; three
-// hand-overs per tile, 669; two issuers, 832; logits read twice from TMEM in
-// rolled loops (fewer instruction-cache misses), 653; the next block's first
-// product before the other tile's last one, 656.
+// Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16, 1,721 sustained):
+//   two prompts of 8,190 tokens, 28/4 heads       595 us   1.60 PFLOP/s, 0.83 (0.93 of sustained)
+//   8 prompts of 1,359 - 2,064 tokens, 32/8       157 us   1.26 PFLOP/s, 0.65 (0.73)
+//   64 trees of 64 nodes over 4,112 slots, 28/4   189 us   1.15 PFLOP/s, 0.59 (0.67)
+//   192 sequences decoding over 2,063 slots       226 us   6.83 TB/s,    1.01
+// Decoding is bound by HBM, prompts and large trees by the board's power limit: at
+// 1,360 W the SMs run at 1,970 (chunks of 500 tokens), 1,850 (prompts of 2,000) or
+// 1,740 MHz (large trees). Between two key tiles a row tile's products take 2 x 512
+// clocks; its softmax 1,000 - 1,200 (in isolation 910: 430 of exponentials, 160
+// maximum, 170 TMEM, 95 sums), the hand-overs 300. The two tiles alternate, so a pair
+// of key tiles takes 2,340 - 2,400 clocks instead of the products' 2,048, and a row
+// block 4,000 more (first logits, ragged last tile, both tiles' softmax at once).
+// Work left out shows at the power limit (the last tile's products end with its last
+// visible quarter: 160 -> 157 us for the prompts of 2,000, trees 191 -> 187), waiting
+// left out does not: the next block's first product between the last ones of this
+// block cut 1,850 clocks per block and no time.
+// Before: without the uniform issuer (below) the long prompts took 764 us, with one
+// thread computing descriptors in a branch 882, with the whole row unpacked 995.
+// Measured and not kept (the long prompts, against 625 us then): half a row per
+// thread, 691; three hand-overs per tile, 669; two issuers, 832; logits read twice
+// from TMEM in rolled loops, 653.
 #include <atomic>
 
 #include "attend/attend.cuh"
@@ -63,7 +66,8 @@ namespace bkv {
 namespace {
 
 // A wait of this kernel: bounded like mbar_wait, in a third of its instructions
-// (there are forty of them; with the others the kernel was 118 KB of code). A wait
+// (there are forty of them; with the others and all kinds of call in one kernel it was
+// 118 KB of code, 64 - 68 KB an instance now: long prompts 625 -> 600 us). A wait
 // that runs out raises the abort flag; the status is latched once, at the end.
 __device__ __forceinline__ uint32_t clock32() {
   uint32_t t;
@@ -261,6 +265,7 @@ struct Block {
   int L;         // tree: committed slots (every node sees them)
   int nodes;     // tree: nodes visible in the cache
   int kv_len;    // slots that some row may see
+  int v_len;     // slots that some row of the call may see
   int i0;        // its first token's place in the sequence
   bool bad;      // a length had to be clamped
 };
@@ -280,7 +285,7 @@ __device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int it
   const int at = item / P.kv_heads;
   k.b = 0;
   k.row0 = 0;
-  k.cnt = k.past = k.L = k.nodes = k.kv_len = k.i0 = 0;
+  k.cnt = k.past = k.L = k.nodes = k.kv_len = k.v_len = k.i0 = 0;
   k.bad = false;
   if (at < cur.before) cur = Cursor{};
   for (; cur.b0 < P.batch; cur.b0 += 128) {
@@ -330,6 +335,7 @@ __device__ __forceinline__ Block find_prompt_block(const AttendParams& P, int it
     const int fc = min(max(f, 0), P.max_cache);
     k.past = fc + k.i0;
     k.kv_len = (int)min((int64_t)k.past + k.cnt, (int64_t)P.max_cache);
+    k.v_len = (int)min((int64_t)fc + (end - beg), (int64_t)P.max_cache);
     k.bad |= fc != f || (int64_t)k.past + k.cnt > P.max_cache;
     return k;
   }
@@ -346,7 +352,7 @@ __device__ __forceinline__ Block find_tree_block(const AttendParams& P, int item
   const int used = min(max(nn, 0), P.n);
   k.L = min(max(len, 0), P.max_cache);
   k.nodes = min(used, P.max_cache - k.L);
-  k.kv_len = k.L + k.nodes;
+  k.kv_len = k.v_len = k.L + k.nodes;
   k.bad = k.L != len || used != nn || k.nodes != used;
   k.i0 = qb * tpi;
   k.row0 = (int64_t)k.b * P.n + k.i0;
@@ -365,9 +371,18 @@ struct Work {
   int t_lo, nt;   // this CTA's key tiles
 };
 
+// Quarters (32 keys) of the last tile `tile` that row tile q sees some of, at least one.
+// Products stop there: the rows after a block's first ones end inside a tile, and at the
+// board's power limit every MMA left out counts.
+template <bool kTree>
+__device__ __forceinline__ int last_quarters(const Block& k, int q, int tpt, int tile) {
+  const int end = kTree ? k.kv_len : min(k.past + (q + 1) * tpt, k.kv_len);
+  return min(max((end - tile * kTileKeys + 31) >> 5, 1), 4);
+}
+
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];  // K/V ring
-  uint64_t qfull, qempty;
+  uint64_t qfull[2], qempty[2];
   uint64_t sfull[2];      // a tile's logits are in TMEM (and its PV before is done)
   uint64_t pfull[2][2];   // half of its probabilities are
   uint64_t ofull[2], ofree[2];  // O is complete; O (and the row statistics) have been read
@@ -511,10 +526,10 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], 1);
     }
-    mbar_init(&C.qfull, 1);
-    mbar_init(&C.qempty, 1);
 #pragma unroll 1
     for (int q = 0; q < NQ; ++q) {
+      mbar_init(&C.qfull[q], 1);
+      mbar_init(&C.qempty[q], 1);
       mbar_init(&C.sfull[q], 1);
       mbar_init(&C.pfull[q][0], (uint32_t)wpt);
       mbar_init(&C.pfull[q][1], (uint32_t)wpt);
@@ -649,7 +664,8 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
       start();
       const uint64_t pol = policy_evict_normal();
       const uint32_t qbytes = (uint32_t)(P.group * P.tpt) * 128;
-      int st = 0, items = 0;
+      int st = 0;
+      uint32_t loads0 = 0, loads1 = 0;  // of each row tile's queries
       long long g = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -658,17 +674,6 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
         if (lane == 0 && w.nt > 0) {
           const Block& blk = w.blk;
           const int nq = NQ == 1 || blk.cnt <= P.tpt ? 1 : 2;
-          if (items > 0) ok = bar_wait(&C.qempty, (uint32_t)((items - 1) & 1), ctl);
-          if (ok) {
-            mbar_expect_tx(&C.qfull, (uint32_t)nq * 2 * qbytes);
-#pragma unroll 1
-            for (int q = 0; q < nq; ++q)
-#pragma unroll 1
-              for (int s = 0; s < 2; ++s)
-                tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
-                            (int)(blk.row0 + q * P.tpt), &C.qfull, pol);
-            ++items;
-          }
           const int z = blk.b * P.kv_heads + blk.h;
           const int call = 2 * w.nt > 8 ? 2 * w.nt - 8 : 0;  // four tiles before the end
 #pragma unroll 1
@@ -687,13 +692,32 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
               st = 0;
               ph ^= 1u;
             }
+            // Queries behind the first keys, which need not wait for the last block's
+            // products; a tile's own as soon as its last logits are there.
+            if (i == 0) {
+#pragma unroll 1
+              for (int q = 0; q < nq && ok; ++q) {
+                const uint32_t n = q ? loads1 : loads0;
+                if (n > 0) ok = bar_wait(&C.qempty[q], (n - 1) & 1u, ctl);
+                if (!ok) break;
+                if (q) ++loads1;
+                else ++loads0;
+                mbar_expect_tx(&C.qfull[q], 2 * qbytes);
+#pragma unroll 1
+                for (int s = 0; s < 2; ++s)
+                  tma_load_3d(smem_u32(q_s) + (uint32_t)(2 * q + s) * lay.slab_q, &P.qmap, 64 * s, blk.h * P.group,
+                              (int)(blk.row0 + q * P.tpt), &C.qfull[q], pol);
+              }
+            }
           }
         }
         ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
       }
       if (lane == 0 && ctl->abort) {  // loads already issued must land before the CTA exits
         long long t0 = clock64();
-        while (items > 0 && !mbar_test(&C.qfull, (uint32_t)((items - 1) & 1)) && clock64() - t0 < kWaitCycles) {
+        while (loads0 > 0 && !mbar_test(&C.qfull[0], (loads0 - 1) & 1u) && clock64() - t0 < kWaitCycles) {
+        }
+        while (loads1 > 0 && !mbar_test(&C.qfull[1], (loads1 - 1) & 1u) && clock64() - t0 < kWaitCycles) {
         }
 #pragma unroll 1
         for (int s = 0; s < S && s < g; ++s) {
@@ -710,12 +734,12 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
       // product whose MMAs are queued, and only the waits for probabilities stand
       // between two products.
       const uint32_t tmem = start();
-      constexpr uint32_t id_qk = idesc_bf16(128, 128), id_pv = idesc_bf16(128, 128) | kIdescBMn;
+      constexpr uint32_t id_pv = idesc_bf16(128, 128) | kIdescBMn;
       const uint32_t qd = desc_k(smem_u32(q_s)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
       const uint32_t slab_step = lay.slab_q >> 4;  // descriptors count 16 bytes
       const uint32_t el = elect_one();
       // the two 64-column halves of a logit product
-      auto issue_qk = [&](int q, int st, int half) {
+      auto issue_qk = [&](int q, int st, int half, uint32_t id_qk) {
         const uint32_t d = tmem + (uint32_t)q * 256;
         const uint32_t a = qd + (uint32_t)(2 * q + half) * slab_step;
         const uint32_t b = kd + (uint32_t)st * (kTileBytes >> 4) + (uint32_t)half * (kSlabBytes >> 4);
@@ -740,32 +764,61 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
           ph ^= 1u;
         }
       };
-      int items = 0;
-      // per row tile, one bit each: parity of the key tiles and of the row blocks done,
-      // and whether there was one
-      uint32_t tiles = 0, outs = 0, any = 0;
+      // per row tile, one bit each: parity of the queries' loads, of the key tiles and of
+      // the row blocks done, and whether there was one
+      uint32_t loads = 0, tiles = 0, outs = 0, any = 0;
       int st = 0;  // next stage of the ring
       uint32_t ph = 0;
       bool ok = true, issued = false;
+      int nt = 0, nq = 0, sv = 0;  // the present block; stage of V_j, which K_{j+1} follows
+      int last0 = 4, last1 = 4;    // quarters of its last tile
+      auto quarters = [&](int q) { return q ? last1 : last0; };
       Work w;
-      while (ok && next_work(w)) {
-        if (w.nt == 0) continue;
-        const int nt = w.nt, nq = NQ == 1 || w.blk.cnt <= P.tpt ? 1 : 2;
-        ok = wait(&C.qfull, (uint32_t)(items & 1)) && wait(&C.full[st], ph);
-        ++items;
-        if (!ok) break;
-        tc_fence_after();
-        issued = true;
+      // A turn: the last products of one block and the first of the next, row tile by row
+      // tile, so that one tile's softmax has its logits while the other's is still at work.
+      for (;;) {
+        const bool more = next_work(w) && w.nt > 0;
+        const int nq1 = !more ? 0 : NQ == 1 || w.blk.cnt <= P.tpt ? 1 : 2;
 #pragma unroll 1
-        for (int q = 0; q < nq; ++q) {
-          issue_qk(q, st, 0);
-          issue_qk(q, st, 1);
-          umma_commit_if(&C.sfull[q], el);
+        for (int q = 0; q < NQ && ok; ++q) {
+          if (q < nq) {
+            const uint32_t par = ((tiles >> q) ^ (uint32_t)(nt - 1)) & 1u;
+            ok = wait(&C.pfull[q][0], par);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(q, sv, 0, nt > 1 ? 1u : 0u);
+            if (quarters(q) > 1) issue_pv(q, sv, 1, 1u);
+            ok = wait(&C.pfull[q][1], par);
+            if (!ok) break;
+            tc_fence_after();
+            if (quarters(q) > 2) issue_pv(q, sv, 2, 1u);
+            if (quarters(q) > 3) issue_pv(q, sv, 3, 1u);
+            umma_commit_if(&C.ofull[q], el);
+          }
+          if (q < nq1) {
+            ok = (q > 0 || wait(&C.full[st], ph)) && wait(&C.qfull[q], (loads >> q) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            issued = true;
+            const uint32_t id = idesc_bf16(128, w.nt == 1 ? 32 * last_quarters<kTree>(w.blk, q, P.tpt, w.t_lo) : 128);
+            issue_qk(q, st, 0, id);
+            issue_qk(q, st, 1, id);
+            umma_commit_if(&C.sfull[q], el);
+            if (w.nt == 1) umma_commit_if(&C.qempty[q], el);
+          }
         }
+        if (!ok) break;
+        if (nq > 0) umma_commit_if(&C.empty[sv], el);
+        if (nt & 1) tiles ^= nq == 2 ? 3u : 1u;
+        if (!more) break;
         umma_commit_if(&C.empty[st], el);
-        if (nt == 1) umma_commit_if(&C.qempty, el);
+        nt = w.nt;
+        nq = nq1;
+        last0 = last_quarters<kTree>(w.blk, 0, P.tpt, w.t_lo + nt - 1);
+        last1 = last_quarters<kTree>(w.blk, 1, P.tpt, w.t_lo + nt - 1);
+        loads ^= nq == 2 ? 3u : 1u;
         step(st, ph);
-        int sv = st;  // stage of V_j; K_{j+1} follows
+        sv = st;
         ok = wait(&C.full[sv], ph);
 #pragma unroll 1
         for (int q = 0; q < nq; ++q)  // the last block's O has been read
@@ -795,46 +848,30 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
             issue_pv(q, sv, 3, 1u);
             if (q == nq - 1) umma_commit_if(&C.empty[sv], el);
             if (!ok) break;
-            issue_qk(q, sk, 0);
+            const uint32_t id = idesc_bf16(128, j + 2 == nt ? 32 * quarters(q) : 128);
+            issue_qk(q, sk, 0, id);
             if (q == nq - 1) ok = wait(&C.full[st], ph);
-            issue_qk(q, sk, 1);
+            issue_qk(q, sk, 1, id);
             umma_commit_if(&C.sfull[q], el);
+            if (j + 2 == nt) umma_commit_if(&C.qempty[q], el);
           }
           umma_commit_if(&C.empty[sk], el);
           sv = st;
         }
         if (!ok) break;
-        if (nt > 1) umma_commit_if(&C.qempty, el);
         step(st, ph);
-        // the last tile: V rows behind the last slot may hold NaN, and 0 * NaN is NaN
-        const int live = w.blk.kv_len - (w.t_lo + nt - 1) * kTileKeys;
+        // the last tile: V rows behind the sequence may hold NaN, and 0 * NaN is NaN
+        const int live = w.blk.v_len - (w.t_lo + nt - 1) * kTileKeys;
         if (live < kTileKeys) {
           uint4* rows = reinterpret_cast<uint4*>(ring + (size_t)sv * kTileBytes);
 #pragma unroll 1
-          for (int i = live * 8 + lane; i < kTileKeys * 8; i += 32) {
+          for (int i = live * 8 + lane; i < quarters(nq - 1) * 256; i += 32) {
             rows[i] = make_uint4(0, 0, 0, 0);
             rows[kSlabBytes / 16 + i] = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-#pragma unroll 1
-        for (int q = 0; q < nq; ++q) {
-          const uint32_t par = ((tiles >> q) ^ (uint32_t)(nt - 1)) & 1u;
-          ok = wait(&C.pfull[q][0], par);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(q, sv, 0, nt > 1 ? 1u : 0u);
-          issue_pv(q, sv, 1, 1u);
-          ok = wait(&C.pfull[q][1], par);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(q, sv, 2, 1u);
-          issue_pv(q, sv, 3, 1u);
-          umma_commit_if(&C.ofull[q], el);
-        }
-        umma_commit_if(&C.empty[sv], el);
-        if (nt & 1) tiles ^= nq == 2 ? 3u : 1u;
       }
       if (!ok && issued) {
         // after an abort, let the MMAs already issued finish before the TMEM is freed
@@ -970,6 +1007,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
           if (blk.nodes < 64) bits &= (1ull << blk.nodes) - 1ull;
         }
       }
+      const int last = last_quarters<kTree>(blk, q, P.tpt, w.t_lo + nt - 1);
       float m = kNegInf, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < nt; ++j) {
@@ -1061,11 +1099,15 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
         tmem_st16(t_s, p[0]);
         exps(1, p[1]);
         tmem_st16(t_s + 16, p[1]);
-        exps(2, p[2]);
-        hand_over(0);
-        tmem_st16(t_s + 32, p[2]);
-        exps(3, p[3]);
-        tmem_st16(t_s + 48, p[3]);
+        if (j + 1 < nt || last > 2) {
+          exps(2, p[2]);
+          hand_over(0);
+          tmem_st16(t_s + 32, p[2]);
+          exps(3, p[3]);
+          tmem_st16(t_s + 48, p[3]);
+        } else {
+          hand_over(0);
+        }
         hand_over(1);
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
