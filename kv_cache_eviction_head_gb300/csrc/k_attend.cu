@@ -1307,10 +1307,9 @@ cudaError_t launch_instance(const AttendParams& p, int splits, int64_t items, cu
     at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  // One tile: short calls (one sequence decoding 12.3 -> 9.6 us, 64 trees of 16 nodes
-  // 56.5 -> 54.1). Two tiles keep their order of launch: back to back, 8 prompts took 176 us
-  // without it and 180 with it.
-  if (NQ == 1) at[cfg.numAttrs++] = dependent_launch();
+  // one sequence decoding 12.3 -> 9.6 us, 64 trees of 16 nodes 56.5 -> 54.1, prompt
+  // chunks of 500 tokens 74.2 -> 72.6; long calls as without it
+  at[cfg.numAttrs++] = dependent_launch();
   return cudaLaunchKernelEx(&cfg, fn, p, splits);
 }
 
