@@ -376,3 +376,21 @@ def test_query_rows_of_nobody_reach_no_other_row(bkv, poison):
             assert int(status) == (0 if fill == 0.0 else bkv.BKV_ERR_NONFINITE)
             outs.append(torch.cat((out[:cu[1]], out[cu[2]:])))
         assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("heads,kv", [(32, 8), (28, 4), (2, 1), (5, 5)])
+def test_prompt_last_tiles_end_anywhere(bkv, heads, kv):
+    """Blocks of one and of two row tiles, whose keys end in every quarter of a tile, one after
+    the other on the same SM (more row blocks than SMs)."""
+    rng = torch.Generator().manual_seed(heads)
+    lens = [int(x) for x in torch.randint(1, 300, (48,), generator=rng)]
+    first = [int(x) for x in torch.randint(0, 200, (48,), generator=rng)]
+    first[::3] = [0] * len(first[::3])
+    assert prompt_case(bkv, heads, kv, lens, first, 5) <= 0
+
+
+@pytest.mark.parametrize("n,heads,kv", [(1, 8, 2), (9, 8, 2), (40, 28, 4), (64, 28, 4)])
+def test_tree_last_tiles_end_anywhere(bkv, n, heads, kv):
+    ends = [n, 127, 128, 129, 159, 160, 161, 191, 192, 193, 223, 224, 225, 255, 256, 257]
+    lens = [max(e - n, 0) for e in ends] * 4
+    assert tree_case(bkv, heads, kv, n, lens, 6, mask=random_mask(len(lens), n, 7)) <= 0
