@@ -1053,11 +1053,14 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
           mx[c] = fmaxf(mx[c], v[c][31]);
         }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+        // Each row by its own logits alone, or its last bits would vary with its
+        // neighbours', and with what lies in the rows behind the last one.
+        const bool raise = valid && (mt > m + kRescale || (m == kNegInf && mt > kNegInf));
         if (j == 0) {
           m = mt;
-        } else if (__any_sync(kFull, mt > m + kRescale || (m == kNegInf && mt > kNegInf))) {
-          const float m_new = fmaxf(m, mt);
-          const float f = m == kNegInf ? 0.f : fast_exp2(m - m_new);
+        } else if (__any_sync(kFull, raise)) {
+          const float m_new = raise ? mt : m;
+          const float f = !raise ? 1.f : m == kNegInf ? 0.f : fast_exp2(m - m_new);
           l *= f;
           m = m_new;
 #pragma unroll 1

@@ -394,3 +394,23 @@ def test_tree_last_tiles_end_anywhere(bkv, n, heads, kv):
     ends = [n, 127, 128, 129, 159, 160, 161, 191, 192, 193, 223, 224, 225, 255, 256, 257]
     lens = [max(e - n, 0) for e in ends] * 4
     assert tree_case(bkv, heads, kv, n, lens, 6, mask=random_mask(len(lens), n, 7)) <= 0
+
+
+@pytest.mark.parametrize("heads,kv", [(28, 4), (40, 8), (3, 1)])
+def test_results_do_not_depend_on_what_ran_before(bkv, heads, kv):
+    """Rows of a tile behind its last one hold what an earlier call left on the SM; a row
+    keeps its bits whatever they are."""
+    cs = torch.cuda.current_stream()
+    cfg = config(bkv, heads, kv, 20, 900)
+    K, V, q = randn((20, kv, 900, D), 1), randn((20, kv, 900, D), 2), randn((20, 40, heads, D), 3)
+    K2, q2 = randn((20, kv, 900, D), 4, 30.0), randn((20, 40, heads, D), 5, 30.0)
+    lens, cu = i32([40 * b for b in range(20)]), i32([40 * b for b in range(21)])
+    flat = lambda t: t.view(-1, heads, D)
+    tree, prompt = [torch.zeros_like(q) for _ in range(5)], [torch.zeros_like(q) for _ in range(5)]
+    for i in range(4):
+        bkv.bkv_attend_tree(cfg, q, K, V, lens, tree[i], stream=cs)
+        bkv.bkv_attend_prompt(cfg, flat(q), K, V, cu, lens, flat(prompt[i]), stream=cs)
+        if i % 2 == 0:
+            bkv.bkv_attend_tree(cfg, q2, K2, V, lens, tree[4], stream=cs)
+            bkv.bkv_attend_prompt(cfg, flat(q2), K2, V, cu, lens, flat(prompt[4]), stream=cs)
+    assert all(torch.equal(t, tree[0]) for t in tree[1:4]) and all(torch.equal(t, prompt[0]) for t in prompt[1:4])

@@ -292,3 +292,42 @@ def test_checked_build(bkv):
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-m", "gpu"] + ["tests/" + c for c in cases], cwd=ROOT,
                        env={**os.environ, "BKV_LIBRARY": "checked"}, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and f"{len(cases)} passed" in r.stdout, r.stdout[-3000:] + r.stderr[-2000:]
+
+
+def test_two_captured_graphs_replayed_at_once(bkv):
+    """Two-tile kernels behind one another in two graphs, replayed on two streams at a time,
+    give what the same calls give eagerly."""
+    shape = dict(batch=20, heads=28, kv=4, slots=900, n=40)
+
+    def state(seed):
+        s = serving_state(bkv, seed, **shape)
+        s["lens"].copy_(i32([40 * b for b in range(20)]))
+        s["path"] = i32([list(range(3, 40)) + [0, 1, 2]] * 20)
+        s["count"] = i32([b + 1 for b in range(20)])
+        return s
+
+    states, eager = [state(20), state(30)], [state(20), state(30)]
+    streams, graphs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for s, stream in zip(states, streams):
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(stream):
+            serve(bkv, state(1), stream)
+            torch.cuda.synchronize()
+            graph.capture_begin()
+            serve(bkv, s, stream)
+            serve(bkv, s, stream)
+            graph.capture_end()
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    for s in eager:
+        for _ in range(6):
+            serve(bkv, s, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for s, t in zip(states, eager):
+        assert int(s["status"]) == 0
+        assert all(torch.equal(x, y) for x, y in zip(results(s), results(t)))
