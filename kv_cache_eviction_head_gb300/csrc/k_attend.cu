@@ -21,7 +21,9 @@
 // tile before (one thread's MMAs run in the order of issue), so a row that has
 // its logits may rescale O without further synchronisation.
 //
-// Two instances. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
+// Instances by prompts or trees, persistent CTAs or a cluster per row block (an
+// instance each keeps the others' code out of the instruction caches), and one or two
+// row tiles. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
 // 33.5 MMAC, 30 bytes per clock and SM), their MMAs alternate, and 512 TMEM
 // columns hold both S and both O. NQ = 1: one tile, 256 columns, for few rows;
 // up to 32 rows two CTAs share an SM. Warps: 4 per tile for softmax, 4 for the
