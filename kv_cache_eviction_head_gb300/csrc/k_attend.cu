@@ -35,8 +35,9 @@
 // each keeps its own maximum, sum and O, and the partial results are joined
 // through distributed shared memory, in rank order, so results do not vary.
 //
-// Slots at or behind the last visible one may hold anything: their logits are
-// replaced, not added to, and their V rows are zeroed in shared memory.
+// Slots behind a sequence's last one may hold anything: their logits are replaced,
+// not added to, and their V rows are zeroed in shared memory. Slots that only later
+// rows of the call see keep their V, with P = 0.
 //
 // Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16, 1,721 sustained):
 //   two prompts of 8,190 tokens, 28/4 heads       595 us   1.60 PFLOP/s, 0.83 (0.93 of sustained)
