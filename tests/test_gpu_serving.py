@@ -331,3 +331,35 @@ def test_two_captured_graphs_replayed_at_once(bkv):
     for s, t in zip(states, eager):
         assert int(s["status"]) == 0
         assert all(torch.equal(x, y) for x, y in zip(results(s), results(t)))
+
+
+def test_calls_from_several_threads_at_once(bkv):
+    """Four host threads, each with a stream and a state of its own."""
+    import threading
+
+    states, alone = ([serving_state(bkv, 200 + 10 * i, n=4 + 12 * i) for i in range(4)] for _ in range(2))
+    for s in states + alone:
+        s["path"] = i32([list(range(s["n"]))[::-1]] * 3)
+    for s in alone:
+        for _ in range(20):
+            serve(bkv, s, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(s, stream):
+        try:
+            for _ in range(20):
+                serve(bkv, s, stream)
+        except Exception as e:  # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(s, torch.cuda.Stream())) for s in states]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for s, t in zip(states, alone):
+        assert int(s["status"]) == 0
+        assert all(torch.equal(x, y) for x, y in zip(results(s), results(t)))
