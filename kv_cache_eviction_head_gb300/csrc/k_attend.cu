@@ -858,6 +858,9 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
             umma_commit_if(&C.sfull[q], el);
             if (j + 2 == nt) umma_commit_if(&C.qempty[q], el);
           }
+          // Only a stage whose products are issued is given back: without its K the loop
+          // above has left before them, and a second copy would join the one under way.
+          if (!ok) break;
           umma_commit_if(&C.empty[sk], el);
           sv = st;
         }
