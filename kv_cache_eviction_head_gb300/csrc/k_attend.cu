@@ -71,20 +71,49 @@ namespace {
 // A wait of this kernel: bounded like mbar_wait, in a third of its instructions
 // (there are forty of them; with the others and all kinds of call in one kernel it was
 // 118 KB of code, 64 - 68 KB an instance now: long prompts 625 -> 600 us). A wait
-// that runs out raises the abort flag; the status is latched once, at the end.
+// that runs out raises the abort flag; the status is latched once, at the end. In the
+// bounds-checked build a test can lower the bound (bkv_checked_wait_cycles) and see
+// waits run out at any point of a call; its waits do not suspend the thread, which
+// could outlast a short bound.
+#ifdef BKV_CHECKED
+__device__ uint32_t wait_cycles = (uint32_t)kWaitCycles;
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+#else
+constexpr uint32_t wait_cycles = (uint32_t)kWaitCycles;
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) { return mbar_test(b, parity); }
+#endif
 __device__ __forceinline__ uint32_t clock32() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
   return t;
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl* ctl) {
-  if (mbar_test(b, parity)) return true;
+  if (bar_test(b, parity)) return true;
   const uint32_t t0 = clock32();
   do {
-    if (mbar_test(b, parity)) return true;
-  } while (!ctl->abort && clock32() - t0 < (uint32_t)kWaitCycles);
+    if (bar_test(b, parity)) return true;
+  } while (!ctl->abort && clock32() - t0 < wait_cycles);
   ctl->abort = 1;
   return false;
+}
+// Waits for work already handed to the hardware (a copy, an MMA), whatever has become
+// of the call: shared memory and TMEM must not change hands before it is done.
+__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity, Ctl* ctl) {
+  const uint32_t t0 = clock32();
+  while (!mbar_test(b, parity)) {
+    if (clock32() - t0 >= (uint32_t)kWaitCycles) {
+      ctl->abort = 1;
+      return;
+    }
+  }
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -393,7 +422,7 @@ struct Control {
   uint64_t staged[2], unstaged[2];  // output warps: a half tile is in its buffer; the buffer may be filled
   uint64_t wfull[2], wempty[2];  // work slots
   uint64_t want, taken;   // the producer runs out of work; a block has been taken
-  uint64_t drain;         // after an abort
+  uint64_t done;          // every MMA of the CTA is done
   uint4 block;            // its name
   Work work[2];
   Ctl ctl;
@@ -549,7 +578,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
     }
     mbar_init(&C.want, 1);
     mbar_init(&C.taken, 1);
-    mbar_init(&C.drain, 1);
+    mbar_init(&C.done, 1);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -647,9 +676,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
         }
         ok = __all_sync(kFull, bar_wait(&C.taken, (uint32_t)(tries & 1), ctl));
         if (!ok) {  // the name must land before the CTA exits
-          const long long t0 = clock64();
-          while (!mbar_test(&C.taken, (uint32_t)(tries & 1)) && clock64() - t0 < kWaitCycles) {
-          }
+          drain(&C.taken, (uint32_t)(tries & 1), ctl);
           break;
         }
         ++tries;
@@ -716,20 +743,16 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
         }
         ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
       }
-      if (lane == 0 && ctl->abort) {  // loads already issued must land before the CTA exits
-        long long t0 = clock64();
-        while (loads0 > 0 && !mbar_test(&C.qfull[0], (loads0 - 1) & 1u) && clock64() - t0 < kWaitCycles) {
-        }
-        while (loads1 > 0 && !mbar_test(&C.qfull[1], (loads1 - 1) & 1u) && clock64() - t0 < kWaitCycles) {
-        }
+      // The loads land before the CTA exits, also if another warp gives up after this
+      // point. st and ph are the next load's, so the last load of a stage in front of st
+      // was ph's, of one at or behind it the round's before.
+      if (lane == 0) {
+        if (loads0 > 0) drain(&C.qfull[0], (loads0 - 1) & 1u, ctl);
+        if (loads1 > 0) drain(&C.qfull[1], (loads1 - 1) & 1u, ctl);
 #pragma unroll 1
-        for (int s = 0; s < S && s < g; ++s) {
-          const long long last = g - 1 - ((g - 1 - s) % S);
-          t0 = clock64();
-          while (!mbar_test(&C.full[s], (uint32_t)((last / S) & 1)) && clock64() - t0 < kWaitCycles) {
-          }
-        }
+        for (int s = 0; s < S && s < g; ++s) drain(&C.full[s], s < st ? ph : ph ^ 1u, ctl);
       }
+      __syncwarp();
     } else if (warp == kIssuer) {
       // ---------------------------------------------------------- MMA issuer
       // The tensor core takes few MMAs ahead, so whatever lies between two of them
@@ -879,12 +902,11 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
           __syncwarp();
         }
       }
-      if (!ok && issued) {
-        // after an abort, let the MMAs already issued finish before the TMEM is freed
-        umma_commit_if(&C.drain, el);
-        const long long t0 = clock64();
-        while (!mbar_test(&C.drain, 0u) && clock64() - t0 < kWaitCycles) {
-        }
+      if (issued) {
+        // the MMAs, and the arrivals of the commits before this one, before the TMEM is
+        // freed and the CTA exits: after an abort nobody has waited for them
+        umma_commit_if(&C.done, el);
+        drain(&C.done, 0u, ctl);
       }
       __syncwarp();
     } else {
@@ -1336,3 +1358,10 @@ cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t ite
 }
 
 }  // namespace bkv
+
+#ifdef BKV_CHECKED
+// Tests only: the bound of the attention kernels' waits on the current device, in clocks.
+extern "C" bkv_status bkv_checked_wait_cycles(uint32_t cycles) {
+  return cudaMemcpyToSymbol(bkv::wait_cycles, &cycles, sizeof(cycles)) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+#endif

@@ -26,6 +26,11 @@ def test_a_wait_that_runs_out_anywhere_ends_the_call_with_nothing_in_flight():
     assert 500 < gave_up < 1000
 
 
+def test_copies_and_products_are_waited_for_also_when_another_role_gives_up_later():
+    found = faults(range(300), mistakes=("drain",))
+    assert {"exit with copies in flight", "exit with products or commits in flight"} <= found
+
+
 def test_a_stage_whose_products_are_not_issued_is_not_given_back():
     seeds = range(1530, 1960)
     assert not faults(seeds, deep=True)
