@@ -65,6 +65,12 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
     }
   };
   load(tid / kRowThreads);  // the first rows need no answer from below
+  if (blockIdx.x == 0 && warp == kThreadsStore / 32 - 1) {
+    // offsets out of range or order, also those of sequences that no token leads to
+    bool bad = false;
+    for (int k = lane; k < P.batch; k += 32) bad |= P.cu[k] < 0 || P.cu[k + 1] < P.cu[k] || P.cu[k + 1] > P.total;
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
+  }
   if (warp < kTokens) {
     // a token's sequence: the number of sequences that end at or before it
     const int t = t0 + warp;
@@ -74,12 +80,10 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
     const int at = min(b, P.batch - 1);
     const int begin = P.cu[at], first = P.first[at], base = P.pos[at];
     const int i = t - begin;
-    const bool known = t < P.total && b < P.batch && begin >= 0 && i >= 0;
     // in front of the first sequence or behind the last one: not a token of any
-    bool bad = t < P.total && b < P.batch && (begin < 0 || (i < 0 && b > 0));
+    const bool known = t < P.total && b < P.batch && begin >= 0 && i >= 0;
     const int64_t slot = (int64_t)first + i;
     const bool fits = slot >= 0 && slot < P.max_cache;
-    bad |= known && !fits;
     const int64_t where = known ? (int64_t)base + (P.depth ? P.depth[t] : i) : 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
     if (lane == 0) {
       row_of[warp] = known && fits ? (int64_t)b * P.kv_heads * P.max_cache + slot : -1;
       live[warp] = known;
-      if (bad) latch(P.status, BKV_ERR_INVALID_ARG);
+      if (known && !fits) latch(P.status, BKV_ERR_INVALID_ARG);
     }
   }
   __syncthreads();
