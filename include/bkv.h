@@ -340,7 +340,9 @@ bkv_status bkv_store_kv(const bkv_config* cfg, const void* q_pre, int64_t q_stri
  *        exponentials.
  * Slots behind a sequence's last token may hold anything, NaN included. A
  * non-finite value in a visible slot makes rows of its own sequence and KV
- * head non-finite, also such as cannot see that slot. */
+ * head non-finite, also such as cannot see that slot; only a logit of -inf
+ * (an infinite key against a query of the other sign) leaves its slot without
+ * weight, and a row that sees no other slots is NaN. */
 bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_stride, const void* K,
                              const void* V, const int32_t* cu_seqlens, const int32_t* first_slot,
                              int32_t total, void* out, float* lse, uint32_t* status, void* cuda_stream);

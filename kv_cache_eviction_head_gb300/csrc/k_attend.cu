@@ -117,6 +117,7 @@ __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity, Ctl* ctl) {
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kNaN = __builtin_nanf("");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;  // log2 units by which the reference maximum may lag
 
@@ -455,6 +456,13 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? kNegInf : l);  // no visible slot: -inf; NaN stays
 }
 __device__ __forceinline__ float row_scale(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
+
+// Whether a token or node of a block sees any slot. One that does and still has a sum of
+// zero has logits of -inf alone: its softmax is not a number.
+__device__ __forceinline__ bool sees_any(const AttendParams& P, const Block& k, int tok) {
+  if (!P.mask || k.L > 0) return true;
+  return ((uint64_t)P.mask[k.row0 + tok] << (64 - k.nodes)) != 0;  // nodes: 1 .. 64
+}
 
 // 64 columns of one warp's 32 rows of O, out of TMEM: normalised, rounded and put
 // into a SWIZZLE_128B slab (row r of the warp at slab + r * 128 bytes). `check`
@@ -1145,6 +1153,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
         l += s0 + s1;
       }
       if (!ok) break;
+      if (!kCluster && l == 0.f && (lim > 0 || bits != 0)) l = kNaN;  // only logits of -inf
       if (kOut) {
         // the output warps have read the last block's statistics
         if (outs > 0) ok = __all_sync(kFull, bar_wait(&C.ofree[q], (uint32_t)((outs - 1) & 1), ctl));
@@ -1216,6 +1225,7 @@ attend_kernel(const __grid_constant__ AttendParams P, const int splits_given) {
 #pragma unroll 1
             for (int off = splits >> 1; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
             wt = wt == 0.f ? 0.f : wt * row_scale(l);
+            if (r < n && l == 0.f && sees_any(P, blk, t * P.tpt + r / P.group)) wt = l = kNaN;  // only logits of -inf
             if (r < n && share == 0) {
               const float lse = row_lse(M, l);
               const int64_t orow = out_row(r);
