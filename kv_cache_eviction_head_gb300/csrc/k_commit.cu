@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreadsCommit) commit_kernel(const __grid_con
   depend_go();
   const int len = P.lens[b], given = P.count[b];
   const int count = min(max(given, 0), P.n);
-  bool bad = count != given || len < 0;
+  bool bad = count != given || len < 0 || len > P.max_cache;
   uint4 x[kSteps];
   bool move[kSteps];
 #pragma unroll

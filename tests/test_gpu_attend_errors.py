@@ -151,3 +151,14 @@ def test_an_infinite_key_by_the_sign_of_the_query(bkv, kind, batch, slots, poiso
             assert not check_weightless(rest, K[0], V[0], see, weightless, out[0][:, ~up], lse[0][:, ~up])
         assert status == (bkv.BKV_ERR_NONFINITE if bool(up.any()) else 0)
         assert bool(torch.isfinite(out[1:]).all())
+
+
+@pytest.mark.parametrize("length,count,bad", [(32, 0, False), (33, 0, True), (-1, 0, True), (2 ** 31 - 1, 2, True), (31, 1, False), (32, 1, True)])
+def test_commit_latches_lengths_out_of_range(bkv, length, count, bad):
+    cfg = config(bkv, 4, 1, 2, 32)
+    K, V, status = randn((2, 1, 32, D), 1), randn((2, 1, 32, D), 2), new_status()
+    K0, V0 = K.clone(), V.clone()
+    bkv.bkv_commit_tree(cfg, [K], [V], i32([4, length]), i32([[0, 1], [0, 1]]), i32([2, count]), status=status,
+                        stream=torch.cuda.current_stream())
+    assert int(status) == (bkv.BKV_ERR_INVALID_ARG if bad else 0)
+    assert torch.equal(K, K0) and torch.equal(V, V0)  # every path names its own place
