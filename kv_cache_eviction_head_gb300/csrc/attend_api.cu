@@ -143,8 +143,9 @@ bkv_status bkv_attend_prompt(const bkv_config* cfg, const void* q, int64_t q_str
   if (total > 0 && !bkv::encode_attend_maps(p, q, q_stride, K, V)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
   if (total == 0) return BKV_OK;
-  // a few tokens behind a long context leave most of the GPU idle unless their keys are split
-  const int splits = splits_for(items, bkv::attend_ctas_per_sm(nq, p.group * p.tpt), c.max_cache);
+  // a few tokens behind a long context leave most of the GPU idle unless their keys are
+  // split; two tiles per CTA are only taken by row blocks enough for every SM
+  const int splits = nq == 2 ? 1 : splits_for(items, bkv::attend_ctas_per_sm(nq, p.group * p.tpt), c.max_cache);
   return bkv::launch_attend(p, nq, splits, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 

@@ -23,7 +23,7 @@
 //
 // Instances by prompts or trees, persistent CTAs or a cluster per row block (an
 // instance each keeps the others' code out of the instruction caches), and one or two
-// row tiles. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
+// row tiles; prompts of two tiles are many row blocks, so they have no cluster form. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
 // 33.5 MMAC, 30 bytes per clock and SM), their MMAs alternate, and 512 TMEM
 // columns hold both S and both O. NQ = 1: one tile, 256 columns, for few rows;
 // up to 32 rows two CTAs share an SM. Warps: 4 per tile for softmax, 4 for the
@@ -1363,7 +1363,8 @@ cudaError_t launch_tiles(const AttendParams& p, int splits, int64_t items, cudaS
 }  // namespace
 
 cudaError_t launch_attend(const AttendParams& p, int nq, int splits, int64_t items, cudaStream_t s) {
-  if (p.cu) return nq == 1 ? launch_tiles<1, false>(p, splits, items, s) : launch_tiles<2, false>(p, splits, items, s);
+  // prompts take two tiles for many row blocks only, whose keys are never split
+  if (p.cu) return nq == 1 ? launch_tiles<1, false>(p, splits, items, s) : launch_instance<2, false, false>(p, 1, items, s);
   return nq == 1 ? launch_tiles<1, true>(p, splits, items, s) : launch_tiles<2, true>(p, splits, items, s);
 }
 
