@@ -308,7 +308,15 @@ bkv_status bkv_score_select_noalloc(const bkv_config* cfg, const void* bq, const
  *     clamped or its rows are skipped, and nothing outside the tensors is
  *     touched), BKV_ERR_NONFINITE (attention: a row's output or log-sum-exp is
  *     not finite), BKV_ERR_TIMEOUT (a bounded wait ran out; the outputs must
- *     not be used). NULL: such errors go unreported.
+ *     not be used). NULL: such errors go unreported. A call without tokens
+ *     looks at no lengths, and of a packed sequence without tokens only its offsets
+ *     are looked at.
+ *   - Rounding in the attention calls: logits, maxima, sums and the output's
+ *     accumulator are fp32; a probability is rounded to bf16 for its product
+ *     with V (at most 2^-8 relative), the sums add the unrounded ones; the
+ *     output is rounded once. The accumulator is normalised at the end, so
+ *     values whose sum, with weights of up to 2^8 each, leaves fp32's range
+ *     count as non-finite.
  *   - Tensors live on the current device, cuda_stream belongs to it, and
  *     outputs do not overlap inputs unless a call says so.
  *   - Host checks return BKV_ERR_INVALID_ARG / BKV_ERR_UNSUPPORTED /

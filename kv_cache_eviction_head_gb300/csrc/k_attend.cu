@@ -12,7 +12,7 @@
 // over S as bf16, and O += P V accumulates in TMEM with P as the TMEM operand.
 //
 // Rounding: l, the maximum, the sum and O are fp32; P is rounded to bf16 for
-// the product with bf16 V (relative 2^-9 per term, like the output's own
+// the product with bf16 V (at most 2^-8 relative per term, like the output's own
 // rounding); the sum adds the unrounded values.
 //
 // The reference maximum only moves when a tile's maximum exceeds it by more
@@ -23,9 +23,9 @@
 //
 // Instances by prompts or trees, persistent CTAs or a cluster per row block (an
 // instance each keeps the others' code out of the instruction caches), and one or two
-// row tiles; prompts of two tiles are many row blocks, so they have no cluster form. NQ = 2: two tiles per CTA share every K and V tile (64 KB per
-// 33.5 MMAC, 30 bytes per clock and SM), their MMAs alternate, and 512 TMEM
-// columns hold both S and both O. NQ = 1: one tile, 256 columns, for few rows;
+// row tiles; prompts of two tiles are many row blocks, so they have no cluster form.
+// NQ = 2: two tiles per CTA share every K and V tile (64 KB per 8.4 MMAC, 32 bytes
+// per clock and SM), their MMAs alternate, and 512 TMEM columns hold both S and both O. NQ = 1: one tile, 256 columns, for few rows;
 // up to 32 rows two CTAs share an SM. Warps: 4 per tile for softmax, 4 for the
 // output (NQ = 2; with one tile the softmax warps write it), one TMA producer,
 // one MMA issuer, one scheduler. K and V tiles alternate in one ring of 32 KB
@@ -42,19 +42,20 @@
 // Measured on one GB300 (6.78 TB/s copy, 1,933 TFLOP/s cuBLAS bf16, 1,721 sustained):
 //   two prompts of 8,190 tokens, 28/4 heads       595 us   1.60 PFLOP/s, 0.83 (0.93 of sustained)
 //   8 prompts of 1,359 - 2,064 tokens, 32/8       157 us   1.26 PFLOP/s, 0.65 (0.73)
-//   64 trees of 64 nodes over 4,112 slots, 28/4   189 us   1.15 PFLOP/s, 0.59 (0.67)
-//   192 sequences decoding over 2,063 slots       226 us   6.83 TB/s,    1.01
-// Decoding is bound by HBM, prompts and large trees by the board's power limit: at
-// 1,360 W the SMs run at 1,970 (chunks of 500 tokens), 1,850 (prompts of 2,000) or
-// 1,740 MHz (large trees). Between two key tiles a row tile's products take 2 x 512
-// clocks; its softmax 1,000 - 1,200 (in isolation 910: 430 of exponentials, 160
-// maximum, 170 TMEM, 95 sums), the hand-overs 300. The two tiles alternate, so a pair
-// of key tiles takes 2,340 - 2,400 clocks instead of the products' 2,048, and a row
-// block 4,000 more (first logits, ragged last tile, both tiles' softmax at once).
-// Work left out shows at the power limit (the last tile's products end with its last
-// visible quarter: 160 -> 157 us for the prompts of 2,000, trees 191 -> 187), waiting
-// left out does not: the next block's first product between the last ones of this
-// block cut 1,850 clocks per block and no time.
+//   64 trees of 64 nodes over 4,112 slots, 28/4   190 us   1.14 PFLOP/s, 0.59 (0.66)
+//   192 sequences decoding over 2,063 slots       229 us   6.75 TB/s,    1.00
+// Decoding a batch is bound by HBM. Prompts and large trees lose 6 - 9 % to the board's
+// power limit (first 200 calls against steady: prompts of 2,000 tokens 144 and 154 us,
+// trees 170 and 186, the long prompts 551 and 592); the rest lies in the kernel and the
+// launch. Between two key tiles a row tile's products take 2 x 512 clocks; its softmax
+// 1,000 - 1,200 (in isolation 910: 430 of exponentials, 160 maximum, 170 TMEM, 95
+// sums), the hand-overs 300. The two tiles alternate, so a pair of key tiles takes
+// 2,340 - 2,400 clocks instead of the products' 2,048, and a row block 4,000 more
+// (first logits, ragged last tile, both tiles' softmax at once); row blocks are handed
+// out whole, so the last round of them leaves SMs idle (trees: 27 us on average).
+// The last tile's products end with its last visible quarter: 160 -> 157 us for the
+// prompts of 2,000, trees 191 -> 187. The next block's first product between the last
+// ones of this block cut 1,850 clocks per block and, at the power limit, no time.
 // Before: without the uniform issuer (below) the long prompts took 764 us, with one
 // thread computing descriptors in a branch 882, with the whole row unpacked 995.
 // Measured and not kept (the long prompts, against 625 us then): half a row per
@@ -70,7 +71,7 @@ namespace {
 
 // A wait of this kernel: bounded like mbar_wait, in a third of its instructions
 // (there are forty of them; with the others and all kinds of call in one kernel it was
-// 118 KB of code, 64 - 68 KB an instance now: long prompts 625 -> 600 us). A wait
+// 118 KB of code, 47 - 65 KB an instance now: long prompts 625 -> 600 us). A wait
 // that runs out raises the abort flag; the status is latched once, at the end. In the
 // bounds-checked build a test can lower the bound (bkv_checked_wait_cycles) and see
 // waits run out at any point of a call; its waits do not suspend the thread, which

@@ -13,7 +13,7 @@
 // Bound: HBM. Every row is read and written once; a block's cosines and sines
 // sit in shared memory, shared by all heads of a token. A thread's first loads
 // start before its token's sequence is looked up (192 decode tokens: 6.2 -> 4.5 us
-// on the device).
+// on the device, 3.8 a call in a captured graph since calls start dependently).
 #include "attend/attend.cuh"
 
 namespace bkv {
@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreadsStore, kTokens > 1 ? 8 : 1) store_kern
 cudaError_t launch_store(const StoreParams& p, cudaStream_t s) {
   // a decode step's tokens one to a block with both passes' loads under way at once;
   // long prompts two to a block, eight blocks to an SM (27,380 tokens of 48 rows:
-  // 105.7 us, 6.37 TB/s; one pass ahead in four-token blocks 107.8, two passes 113)
+  // 103 us, 6.5 TB/s; at 105.7 one pass ahead in four-token blocks took 107.8, two
+  // passes 113)
   const int per_block = p.total <= 8 * kSms ? 1 : 2;
   cudaLaunchAttribute at = dependent_launch();
   cudaLaunchConfig_t cfg{};
