@@ -61,12 +61,15 @@ CHILD = textwrap.dedent('''
         "prompt, one tile": make("prompt", 32, 8, 1, 300, 700),
         "prompt, two tiles": make("prompt", 32, 8, 12, 300, 500),
         "decode, split": make("tree", 32, 8, 1, 1, 2063),
+        "tree, two tiles, split": make("tree", 28, 4, 2, 64, 2000),
+        "tree, two tiles": make("tree", 28, 4, 24, 64, 1500),
+        "decode": make("tree", 32, 8, 60, 1, 2063),
     }
     for name, call in cases.items():
         want = call()
         assert int(want[2]) == 0, name
         gave_up = []
-        for cycles in (0, 100, 300, 600, 900, 1200, 1600, 2000, 3000, 5000, 10000):
+        for cycles in (0, 100, 300, 600, 900, 1200, 1600, 2000, 3000, 5000, 10000, 20000, 50000):
             bound(cycles)
             short = [call() for _ in range(3)]  # one behind the other on the same SMs
             bound(WHOLE)
