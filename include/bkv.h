@@ -388,6 +388,122 @@ bkv_status bkv_commit_tree(const bkv_config* cfg, void* const* K, void* const* V
                            const int32_t* path, const int32_t* count, int32_t n, uint32_t* status,
                            void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged caches, and eviction by accumulated attention weight.
+ *
+ * A layer's keys and values may lie in the pages of a pool, bf16
+ * [pages][kv_heads][page_size][d]; a table says which pages hold a sequence's
+ * slots. Four calls work on such a pool - and, with `pages` NULL, on the dense
+ * caches of the calls above, which are the pool of one page of max_cache slots
+ * per sequence: bkv_store_paged (rotary positions in any common layout, keys
+ * and values to their slots), bkv_attend_paged (one new token per sequence),
+ * bkv_weigh_prompt and bkv_evict_weight. The last three keep an account for
+ * every slot and KV head, fp32 [pages][kv_heads][page_size] beside the pool:
+ * the attention weight that the slot has received, summed over the KV head's
+ * query heads and over queries. bkv_weigh_prompt opens it with a prompt's
+ * queries, bkv_attend_paged adds every decode step's, and bkv_evict_weight keeps
+ * the slots with the most. No call allocates device memory or keeps anything
+ * between calls; status, strides, packed tokens, streams, graphs and host
+ * checks as in the calls above. */
+typedef struct bkv_pages {
+  int32_t pages;         /* pages of the pool                                          */
+  int32_t page_size;     /* slots of a page, a multiple of 16 (BKV_ERR_UNSUPPORTED)    */
+  int32_t per_seq;       /* entries of a table row; per_seq * page_size slots at most  */
+  const int32_t* table;  /* device int32 [batch][per_seq]: slot j of sequence b lies in
+                            page table[b][j / page_size]. Entries behind a sequence's
+                            last slot are not read. An entry outside [0, pages) is an
+                            error (BKV_ERR_INVALID_ARG in status): its slots get no
+                            weight, are not written and do not move. A page may be in
+                            several tables as long as nothing writes to it: not in
+                            bkv_attend_paged or bkv_weigh_prompt with weights, nor in
+                            bkv_evict_weight, whose results would then depend on the
+                            order of the writes.                                       */
+} bkv_pages;
+
+/* Rotary positions: element pairs (i, i + rotary_dim/2), or (2i, 2i + 1) when
+ * interleaved, i < rotary_dim/2, turn by pos * inv_freq[i] radians and are
+ * multiplied by scale; elements from rotary_dim on stay as they are. Filled in
+ * by bkv_make_rope or by the caller. */
+typedef struct bkv_rope {
+  int32_t rotary_dim;    /* a multiple of 16, at most d; 0: nothing turns               */
+  int32_t interleaved;   /* 0 or 1                                                      */
+  double scale;          /* of the rotated elements; 1 unless a scaling asks for more   */
+  double inv_freq[64];   /* radians per position, rotary_dim / 2 of them                */
+} bkv_rope;
+
+/* Frequencies theta^(-2i/r), r = rotary_dim, and how they are scaled for longer
+ * contexts by `factor` >= 1 (unused with BKV_ROPE_NONE):
+ *   BKV_ROPE_LINEAR  divided by factor;
+ *   BKV_ROPE_NTK     theta * factor^(r / (r - 2)) for theta;
+ *   BKV_ROPE_YARN    pairs that turn more than 32 times within original_len
+ *                    tokens stay, those that turn less than once are divided
+ *                    by factor, linear in the turns between; scale is
+ *                    0.1 ln(factor) + 1 (original_len is unused otherwise).
+ * Host only. */
+enum { BKV_ROPE_NONE = 0, BKV_ROPE_LINEAR = 1, BKV_ROPE_NTK = 2, BKV_ROPE_YARN = 3 };
+bkv_status bkv_make_rope(bkv_rope* out, double theta, int32_t rotary_dim, int32_t interleaved, int32_t scaling,
+                         double factor, double original_len);
+
+/* bkv_store_kv with a rotary layout and pages: rotates packed queries and keys
+ * and writes keys and values to their slots. Arguments as there; cfg's
+ * rope_theta is not used. A token whose slot lies outside its table, or on a
+ * page that the table does not name, gets its q_rot but no cache rows
+ * (BKV_ERR_INVALID_ARG in status). */
+bkv_status bkv_store_paged(const bkv_config* cfg, const bkv_pages* pages, const bkv_rope* rope, const void* q_pre,
+                           int64_t q_stride, const void* k_pre, int64_t k_stride, const void* v, int64_t v_stride,
+                           int32_t total, const int32_t* cu_seqlens, const int32_t* first_slot, const int32_t* first_pos,
+                           const int32_t* depth, void* q_rot, void* K, void* V, uint32_t* status, void* cuda_stream);
+
+/* Device workspace of bkv_attend_paged, 256-byte aligned, with (weighed != 0) or
+ * without weights. Its contents need no preparation and nothing is kept in it
+ * between calls; calls that may overlap on the GPU, captured graphs among them,
+ * need one each. */
+bkv_status bkv_attend_paged_bytes(const bkv_config* cfg, const bkv_pages* pages, int32_t weighed, size_t* bytes);
+
+/* Attention of one new token per sequence: sequence b's query heads see slots
+ * [0, lens[b]), the new token's own the last of them (stored before);
+ * scale 1/sqrt(d), query head h reads KV head h / (heads / kv_heads).
+ *   q:       device bf16 [batch][heads][d], rotated, q_stride between sequences.
+ *   lens:    device int32 [batch]; 0: the sequence takes no part, its rows get
+ *            zeros and a log-sum-exp of -inf.
+ *   out:     device bf16 [batch][heads][d]; lse: optional fp32 [batch][heads].
+ *   weights: optional device fp32 [pages][kv_heads][page_size]. Slot j of a
+ *            sequence gets decay * weights + the sum over the KV head's query
+ *            heads of their probabilities; slot lens[b] - 1 that sum alone, and
+ *            with decay = 0 all slots (what was there is then not read).
+ *            0 <= decay <= 1. Other slots stay.
+ * Rounding as in bkv_attend_prompt; weights are sums of unrounded fp32
+ * probabilities. A row without a finite logit is NaN (BKV_ERR_NONFINITE).
+ * Slots behind lens[b] may hold anything. The keys of one (sequence, KV head)
+ * are split over warps by the lengths of the whole batch: a row's last bits may
+ * depend on the other sequences' lengths, but not on their contents, and equal
+ * calls give equal bits. */
+bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const void* q, int64_t q_stride, const void* K,
+                            const void* V, const int32_t* lens, void* out, float* lse, float* weights, float decay,
+                            void* workspace, size_t workspace_bytes, uint32_t* status, void* cuda_stream);
+
+/* Eviction by accumulated weight. Every (layer, sequence, KV head) whose
+ * sequence holds more than cfg->budget slots keeps the first cfg->prefix slots,
+ * the last cfg->recent and, of the others, those with the largest weights, up to
+ * the budget; of equal weights the lowest slots, and NaN ranks below all
+ * numbers. Keys, values and weights of the kept slots move to slots [0, budget),
+ * in slot order or, with BKV_FLAG_ORDER_FREE, as that flag says. Slots at and
+ * behind the budget are left as they are. Sequences within the budget stay whole.
+ *   K, V, weights: host arrays of `layers` device pointers to that layer's pool;
+ *            the table is the same for all layers.
+ *   cache_lens: device int32 [batch].
+ *   kept:    device int32 [layers][batch][kv_heads][budget]: the slot that slot
+ *            i's row comes from; of sequences within the budget 0 .. length - 1,
+ *            then -1.
+ *   new_lens: optional device int32 [batch], not cache_lens itself: the lengths
+ *            after the call.
+ * With BKV_FLAG_ORDER_FREE a sequence with budget < length < budget + recent is
+ * refused on the device (BKV_ERR_INVALID_ARG in status, kept -1, nothing moves),
+ * and a budget above 2^19 on the host (BKV_ERR_UNSUPPORTED). */
+bkv_status bkv_evict_weight(const bkv_config* cfg, const bkv_pages* pages, void* const* K, void* const* V,
+                            float* const* weights, const int32_t* cache_lens, int32_t* kept, int32_t* new_lens,
+                            uint32_t* status, void* cuda_stream);
+
 /* Self-test of the bounded device-side waits every kernel uses (the timeout
  * latch and the abort of the other waiting warps): enqueues on the handle's
  * stream a kernel whose four warps wait up to wait_cycles SM clock cycles

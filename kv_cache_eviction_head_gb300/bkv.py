@@ -45,6 +45,7 @@ EXPORTED = ["bkv_workspace_bytes", "bkv_create", "bkv_set_stream", "bkv_append_q
             "bkv_get_fps_trace", "bkv_get_scores", "bkv_get_head_state",
             "bkv_profile", "bkv_profile_read", "bkv_score_select_noalloc", "bkv_get_stats",
             "bkv_store_kv", "bkv_attend_prompt", "bkv_attend_tree", "bkv_commit_tree",
+            "bkv_make_rope", "bkv_store_paged", "bkv_attend_paged_bytes", "bkv_attend_paged", "bkv_evict_weight",
             "bkv_destroy", "bkv_status_str"]
 KERNELS = ["append", "rope", "score_select", "fps", "coverage", "prefill"]
 
@@ -67,6 +68,18 @@ class BkvStats(ctypes.Structure):
 class BkvKernelTimes(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * 6), ("launches", ctypes.c_uint64 * 6)]
 
+
+class BkvPages(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("per_seq", ctypes.c_int32),
+                ("table", ctypes.c_void_p)]
+
+
+class BkvRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_double),
+                ("inv_freq", ctypes.c_double * 64)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
 _lib.bkv_workspace_bytes.argtypes = [ctypes.POINTER(BkvConfig), ctypes.POINTER(_sz)]
@@ -93,6 +106,15 @@ _lib.bkv_attend_tree.argtypes = [ctypes.POINTER(BkvConfig), _vp, _i64, _vp, _vp,
                                  _vp]
 _lib.bkv_commit_tree.argtypes = [ctypes.POINTER(BkvConfig), ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _vp,
                                  _i32, _vp, _vp]
+_cfgp, _pagesp, _f32 = ctypes.POINTER(BkvConfig), ctypes.POINTER(BkvPages), ctypes.c_float
+_lib.bkv_make_rope.argtypes = [ctypes.POINTER(BkvRope), ctypes.c_double, _i32, _i32, _i32, ctypes.c_double,
+                               ctypes.c_double]
+_lib.bkv_store_paged.argtypes = [_cfgp, _pagesp, ctypes.POINTER(BkvRope), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp,
+                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.bkv_attend_paged_bytes.argtypes = [_cfgp, _pagesp, _i32, ctypes.POINTER(_sz)]
+_lib.bkv_attend_paged.argtypes = [_cfgp, _pagesp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _sz, _vp, _vp]
+_lib.bkv_evict_weight.argtypes = [_cfgp, _pagesp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp,
+                                  _vp, _vp, _vp, _vp]
 _lib.bkv_destroy.argtypes = [_vp]
 _lib.bkv_destroy.restype = None
 _lib.bkv_status_str.argtypes = [_i32]
@@ -332,20 +354,21 @@ def _check_on_device(t, name: str, dtype, shape, device):
     raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
 
 
-def _check_caches(ts, name: str, n: int, shape, device):
-    """A _vp array of n per-layer bf16 caches of this shape on this device. The attributes of
+def _check_caches(ts, name: str, n: int, shape, device, dtype=None):
+    """A _vp array of n per-layer caches (bf16 unless said) of this shape on this device. The attributes of
     all layers are gathered by C-level maps; on a mismatch the layers are looked at one by
     one for the message."""
     T = _Lazy.Tensor
+    dtype = dtype or _Lazy.bf16
     if len(ts) != n:
         raise ValueError(f"{name}: expected {n} per-layer tensors, got {len(ts)}")
     try:
         if (list(map(T.size, ts)) == [shape] * n and list(map(T.get_device, ts)) == [device] * n
-                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} == {_Lazy.bf16}):
+                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} == {dtype}):
             return (_vp * n).from_buffer(array("Q", map(T.data_ptr, ts)))
     except (TypeError, AttributeError):
         pass
-    return (_vp * n)(*[_check_on_device(t, f"{name}[{l}]", _Lazy.bf16, shape, device) for l, t in enumerate(ts)])
+    return (_vp * n)(*[_check_on_device(t, f"{name}[{l}]", dtype, shape, device) for l, t in enumerate(ts)])
 
 
 def _check_packed(t, name: str, shape, device):
@@ -470,6 +493,111 @@ def bkv_commit_tree(cfg: BkvConfig, K, V, cache_lens, path, count, *, status=Non
         _check_on_device(path, "path", i32, (batch, n), dev), _check_on_device(count, "count", i32, (batch,), dev), n,
         None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
         "bkv_commit_tree")
+
+
+def make_rope(*, theta=1e4, rotary_dim=128, interleaved=False, scaling="none", factor=1.0, original_len=0,
+              inv_freq=None, scale=1.0) -> BkvRope:
+    """Rotary positions (see bkv_make_rope in include/bkv.h); scaling: one of ROPE_SCALINGS.
+    inv_freq: the caller's own rotary_dim / 2 frequencies, with `scale`, instead of theta
+    and a scaling."""
+    r = BkvRope()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: expected one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if inv_freq is not None and (scaling != "none" or len(inv_freq) != rotary_dim // 2):
+        raise ValueError(f"inv_freq: expected {rotary_dim // 2} frequencies and no scaling, got {len(inv_freq)} and {scaling!r}")
+    _check(_lib.bkv_make_rope(ctypes.byref(r), theta, rotary_dim, 1 if interleaved else 0, ROPE_SCALINGS[scaling], factor,
+                              original_len), "bkv_make_rope")
+    if inv_freq is not None:
+        r.inv_freq[:rotary_dim // 2] = [float(f) for f in inv_freq]
+        r.scale = float(scale)
+    return r
+
+
+def _check_pool(cfg, K, table, device, name="K"):
+    """The pool's pages as the library takes them (None: the dense caches), and the shape that
+    goes with them without d."""
+    if table is None:
+        return None, (cfg.batch, cfg.kv_heads, cfg.max_cache)
+    s = _dims(K, name, "[pages][kv_heads][page_size][d]", 4)
+    t = _dims(table, "table", "[batch][per_seq]", 2)
+    p = BkvPages(s[0], s[2], t[1], _check_on_device(table, "table", _Lazy.i32, (cfg.batch, t[1]), device))
+    return p, (s[0], cfg.kv_heads, s[2])
+
+
+def bkv_store_paged(cfg: BkvConfig, rope: BkvRope, q_pre, k_pre, v, cu_seqlens, first_slot, first_pos, q_rot, K, V, *,
+                    table=None, depth=None, status=None, stream=None) -> None:
+    """Rotary positions and the write to the pages (see include/bkv.h). K, V: one layer's bf16
+    pools [pages][kv_heads][page_size][d] with table int32 [batch][per_seq], or without a
+    table the dense caches [batch][kv_heads][max_cache][d]; the others as bkv_store_kv."""
+    dev = _device()
+    bf16, i32 = _Lazy.bf16, _Lazy.i32
+    batch, heads, kv, d = cfg.batch, cfg.heads, cfg.kv_heads, cfg.d
+    pages, shape = _check_pool(cfg, K, table, dev)
+    total = _dims(q_pre, "q_pre", "[tokens][heads][d]", 3)[0]
+    pool, rows, one = shape + (d,), (total, kv, d), (batch,)
+    q, qs = _check_packed(q_pre, "q_pre", (total, heads, d), dev)
+    k, ks = _check_packed(k_pre, "k_pre", rows, dev)
+    vv, vs = _check_packed(v, "v", rows, dev)
+    _check(_lib.bkv_store_paged(
+        cfg, pages, rope, q, qs, k, ks, vv, vs, total, _check_on_device(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, one, dev),
+        _check_on_device(first_pos, "first_pos", i32, one, dev),
+        None if depth is None else _check_on_device(depth, "depth", i32, (total,), dev),
+        _check_on_device(q_rot, "q_rot", bf16, (total, heads, d), dev), _check_on_device(K, "K", bf16, pool, dev),
+        _check_on_device(V, "V", bf16, pool, dev),
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_store_paged")
+
+
+def bkv_attend_paged_bytes(cfg: BkvConfig, K, table=None, *, weighed=False) -> int:
+    """Bytes of bkv_attend_paged's workspace for these pools."""
+    pages, _ = _check_pool(cfg, K, table, _device())
+    n = _sz(0)
+    _check(_lib.bkv_attend_paged_bytes(cfg, pages, 1 if weighed else 0, ctypes.byref(n)), "bkv_attend_paged_bytes")
+    return n.value
+
+
+def bkv_attend_paged(cfg: BkvConfig, q, K, V, lens, out, workspace, *, table=None, lse=None, weights=None, decay=1.0,
+                     status=None, stream=None) -> None:
+    """Attention of one new token per sequence over pages or dense caches (see include/bkv.h).
+    q, out: bf16 [batch][heads][d]; lens int32 [batch]; workspace: uint8, at least
+    bkv_attend_paged_bytes; lse: optional float32 [batch][heads]; weights: optional float32
+    [pages][kv_heads][page_size], updated with `decay`."""
+    dev = _device()
+    bf16, i32, f32 = _Lazy.bf16, _Lazy.i32, _Lazy.f32
+    batch, heads, d = cfg.batch, cfg.heads, cfg.d
+    pages, shape = _check_pool(cfg, K, table, dev)
+    pool, rows = shape + (d,), (batch, heads, d)
+    qp, qs = _check_packed(q, "q", rows, dev)
+    size = _dims(workspace, "workspace", "[bytes]", 1)[0]
+    _check(_lib.bkv_attend_paged(
+        cfg, pages, qp, qs, _check_on_device(K, "K", bf16, pool, dev), _check_on_device(V, "V", bf16, pool, dev),
+        _check_on_device(lens, "lens", i32, (batch,), dev), _check_on_device(out, "out", bf16, rows, dev),
+        None if lse is None else _check_on_device(lse, "lse", f32, (batch, heads), dev),
+        None if weights is None else _check_on_device(weights, "weights", f32, shape, dev), decay,
+        _check_on_device(workspace, "workspace", _Lazy.torch.uint8, (size,), dev), size,
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_attend_paged")
+
+
+def bkv_evict_weight(cfg: BkvConfig, K, V, weights, cache_lens, kept, *, table=None, new_lens=None, status=None,
+                     stream=None) -> None:
+    """Eviction by accumulated weight, in every layer (see include/bkv.h). K, V: `layers` bf16
+    pools, weights: `layers` float32 [pages][kv_heads][page_size]; cache_lens int32 [batch];
+    kept int32 [layers][batch][kv_heads][budget]; new_lens: optional int32 [batch]."""
+    dev = _device()
+    i32, batch, layers = _Lazy.i32, cfg.batch, cfg.layers
+    if len(K) != layers:
+        raise ValueError(f"K: expected {layers} per-layer tensors, got {len(K)}")
+    pages, shape = _check_pool(cfg, K[0], table, dev, "K[0]")
+    kp, vp = _check_caches(K, "K", layers, shape + (cfg.d,), dev), _check_caches(V, "V", layers, shape + (cfg.d,), dev)
+    wp = _check_caches(weights, "weights", layers, shape, dev, _Lazy.f32)
+    _check(_lib.bkv_evict_weight(
+        cfg, pages, kp, vp, wp, _check_on_device(cache_lens, "cache_lens", i32, (batch,), dev),
+        _check_on_device(kept, "kept", i32, (layers, batch, cfg.kv_heads, cfg.budget), dev),
+        None if new_lens is None else _check_on_device(new_lens, "new_lens", i32, (batch,), dev),
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_evict_weight")
 
 
 def bkv_get_stats(h: Handle) -> BkvStats:

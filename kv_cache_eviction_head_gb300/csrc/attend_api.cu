@@ -3,41 +3,12 @@
 // launches. No handle, no workspace, no device allocation.
 #include <cmath>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "attend/attend.cuh"
+#include "attend/host.cuh"
 
 namespace {
 
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// The checks of bkv_create's config, and what these kernels need of it.
-bkv_status check(const bkv_config* c) {
-  size_t bytes = 0;
-  const bkv_status st = bkv_workspace_bytes(c, &bytes);
-  if (st != BKV_OK) return st;
-  if (c->heads / c->kv_heads > bkv::kMaxGroup) return BKV_ERR_UNSUPPORTED;
-  return BKV_OK;
-}
-
-// A packed [tokens][heads][d] tensor whose tokens lie `stride` elements apart
-// (no tokens: the pointer is not looked at).
-bool strided_ok(const void* p, int64_t stride, int heads, int d, int tokens) {
-  return (tokens == 0 || p) && aligned(p, 16) && stride >= (int64_t)heads * d && stride % 8 == 0 && stride < (1ll << 38);
-}
-
-bkv_status zero_status(uint32_t* status, cudaStream_t s) {
-  if (status && cudaMemsetAsync(status, 0, sizeof(uint32_t), s) != cudaSuccess) return BKV_ERR_CUDA;
-  return BKV_OK;
-}
-
+using namespace bkv::host;
 
 // CTAs per row block: the keys are split over a cluster while all clusters run at
 // once. GB300's GPCs hold 7 clusters of 16, 15 of 8, 36 of 4 and 76 of 2 at one CTA
