@@ -482,6 +482,23 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
                             const void* V, const int32_t* lens, void* out, float* lse, float* weights, float decay,
                             void* workspace, size_t workspace_bytes, uint32_t* status, void* cuda_stream);
 
+/* The attention weight that packed prompts (or chunks of them) give to every
+ * slot: for slot j of sequence b and each KV head,
+ *   S_j = sum over its query heads and the tokens i with first_slot[b] + i >= j
+ *         of exp(q_i . k_j / sqrt(d) - lse_i);
+ * slots before first_slot[b] get decay * weights + S_j, the call's own slots
+ * S_j alone. A window of the last tokens of a prompt is a call with those
+ * tokens' rows and their first slot (and decay 0 for a new account).
+ *   q, q_stride, cu_seqlens, first_slot, total: as bkv_attend_prompt;
+ *   lse:     device fp32 [total][heads], as it left it (a row of -inf gives nothing).
+ *   weights, decay: as bkv_attend_paged; sequences without tokens and slots
+ *            behind the last token stay.
+ * BKV_ERR_UNSUPPORTED if heads / kv_heads > 96. A weight that is not finite is
+ * latched as BKV_ERR_NONFINITE. */
+bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const void* q, int64_t q_stride, const float* lse,
+                            const void* K, const int32_t* cu_seqlens, const int32_t* first_slot, int32_t total,
+                            float* weights, float decay, uint32_t* status, void* cuda_stream);
+
 /* Eviction by accumulated weight. Every (layer, sequence, KV head) whose
  * sequence holds more than cfg->budget slots keeps the first cfg->prefix slots,
  * the last cfg->recent and, of the others, those with the largest weights, up to

@@ -45,7 +45,8 @@ EXPORTED = ["bkv_workspace_bytes", "bkv_create", "bkv_set_stream", "bkv_append_q
             "bkv_get_fps_trace", "bkv_get_scores", "bkv_get_head_state",
             "bkv_profile", "bkv_profile_read", "bkv_score_select_noalloc", "bkv_get_stats",
             "bkv_store_kv", "bkv_attend_prompt", "bkv_attend_tree", "bkv_commit_tree",
-            "bkv_make_rope", "bkv_store_paged", "bkv_attend_paged_bytes", "bkv_attend_paged", "bkv_evict_weight",
+            "bkv_make_rope", "bkv_store_paged", "bkv_attend_paged_bytes", "bkv_attend_paged", "bkv_weigh_prompt",
+            "bkv_evict_weight",
             "bkv_destroy", "bkv_status_str"]
 KERNELS = ["append", "rope", "score_select", "fps", "coverage", "prefill"]
 
@@ -113,6 +114,7 @@ _lib.bkv_store_paged.argtypes = [_cfgp, _pagesp, ctypes.POINTER(BkvRope), _vp, _
                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 _lib.bkv_attend_paged_bytes.argtypes = [_cfgp, _pagesp, _i32, ctypes.POINTER(_sz)]
 _lib.bkv_attend_paged.argtypes = [_cfgp, _pagesp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _sz, _vp, _vp]
+_lib.bkv_weigh_prompt.argtypes = [_cfgp, _pagesp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _vp]
 _lib.bkv_evict_weight.argtypes = [_cfgp, _pagesp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp,
                                   _vp, _vp, _vp, _vp]
 _lib.bkv_destroy.argtypes = [_vp]
@@ -578,6 +580,27 @@ def bkv_attend_paged(cfg: BkvConfig, q, K, V, lens, out, workspace, *, table=Non
         _check_on_device(workspace, "workspace", _Lazy.torch.uint8, (size,), dev), size,
         None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
         "bkv_attend_paged")
+
+
+def bkv_weigh_prompt(cfg: BkvConfig, q, lse, K, cu_seqlens, first_slot, weights, *, table=None, decay=1.0, status=None,
+                     stream=None) -> None:
+    """The attention weight of packed prompts' queries, summed per slot (see include/bkv.h).
+    q: rotated queries, bf16 [total][heads][d]; lse float32 [total][heads] as
+    bkv_attend_prompt left it; weights float32 [pages][kv_heads][page_size] beside K."""
+    dev = _device()
+    i32, f32 = _Lazy.i32, _Lazy.f32
+    batch, heads, d = cfg.batch, cfg.heads, cfg.d
+    pages, shape = _check_pool(cfg, K, table, dev)
+    total = _dims(q, "q", "[tokens][heads][d]", 3)[0]
+    qp, qs = _check_packed(q, "q", (total, heads, d), dev)
+    _check(_lib.bkv_weigh_prompt(
+        cfg, pages, qp, qs, _check_on_device(lse, "lse", f32, (total, heads), dev),
+        _check_on_device(K, "K", _Lazy.bf16, shape + (d,), dev),
+        _check_on_device(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
+        _check_on_device(first_slot, "first_slot", i32, (batch,), dev), total,
+        _check_on_device(weights, "weights", f32, shape, dev), decay,
+        None if status is None else _check_on_device(status, "status", i32, (1,), dev), _stream_ptr(stream)),
+        "bkv_weigh_prompt")
 
 
 def bkv_evict_weight(cfg: BkvConfig, K, V, weights, cache_lens, kept, *, table=None, new_lens=None, status=None,

@@ -1,0 +1,428 @@
+// The attention weight that packed prompt queries give to every slot, summed over the
+// queries and the query heads of a KV head, on the fifth-generation tensor cores.
+//
+//   S_j = sum_{i, g: first + i >= j} exp(q_ig . k_j / sqrt(d) - lse_ig)
+//   weights[j] = decay weights[j] + S_j (j < first), S_j (j >= first)
+//
+// The product is taken transposed: the 128 slots of a tile are the rows (TMEM lanes) and
+// the queries the columns, so a thread owns a slot and adds up its row in registers;
+// no reduction over lanes, no atomics, the same bits every time. The tile's keys stay in
+// TMEM as operand A for all queries (every thread loads its own slot's 256 bytes, whatever
+// page they are in), so a product reads only the queries from shared memory: 64 bytes
+// per clock and SM, with as much again from TMA writing the next ones.
+//
+// A tile of columns is tpt = 96 / G tokens with the G query heads of the KV head. Two
+// buffers of 96 columns and the keys' 64 take 256 columns of TMEM, so that two CTAs
+// share an SM and one's set-up, ends and hand-overs lie under the other's products.
+// CTA: 4 warps that exponentiate and add, a TMA producer, an MMA issuer. Blocks of the
+// grid take the slots' tiles in order, those that most queries see first.
+//
+// Rounding: products and sums are fp32, nothing is rounded to fewer bits.
+#include <cstddef>
+
+#include "paged/paged.cuh"
+#include "score_common.cuh"
+
+namespace bkv {
+namespace {
+
+constexpr int kCols = kWeighRows;
+constexpr int kQSlab = kCols * 128;              // 96 rows x 64 bf16
+constexpr int kQTile = 2 * kQSlab;               // 24 KB
+constexpr int kQStages = 4;
+constexpr int kWeighThreads = 192;
+constexpr int kProducer = 4, kIssuer = 5;        // warps; 0 - 3 add up
+constexpr uint32_t kTmemCols = 256, kTmemKeys = 192;  // two buffers of 96 columns, the keys behind them
+constexpr int kWeighSmem = kQStages * kQTile + 1024;
+
+struct WeighControl {
+  uint64_t full[kQStages], empty[kQStages];
+  uint64_t keys, keys_free;       // the keys are in TMEM; its products are done
+  uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM; they have been read
+  Ctl ctl;
+  // -lse log2(e) of a tile's columns, a copy per adding warp: no barrier among them
+  alignas(16) float col[4][2][kCols];
+};
+static_assert(offsetof(WeighControl, col) % 16 == 0 && (kCols * sizeof(float)) % 16 == 0, "read as float4");
+
+__device__ __forceinline__ uint32_t lane_elected() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e;
+}
+// A bounded wait, with one answer for the warp.
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, Ctl* ctl, uint32_t* status) {
+  return __all_sync(kFull, mbar_wait(b, parity, ctl, status));
+}
+// Waits for work handed to the hardware, whatever has become of the call.
+__device__ __forceinline__ void wait_done(uint64_t* b, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_test(b, parity))
+    if (clock64() - t0 > kWaitCycles) return;
+}
+// A (128 slots x 16 bf16) from TMEM, B (96 query rows) from shared memory.
+template <uint32_t kAStep, uint32_t kBStep>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+  constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // SBO, version, SWIZZLE_128B
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %8, 0;\n add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n"
+      " mov.b64 b, {y, %7};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep), "n"(kHi), "r"(elected));
+}
+__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// A value that tcgen05.ld delivers is there only after the wait: ties the registers to it.
+__device__ __forceinline__ void tie(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// What a CTA works on: one tile of slots of one (sequence, KV head).
+struct WeighItem {
+  int b, h;
+  int j0;         // first slot
+  int i0, n;      // first token that sees a slot of the tile, tokens of the sequence
+  int begin;      // packed index of the sequence's first token
+  int first;      // slots before the first token
+  int slots;      // slots of the sequence: first + n, at most what its table holds
+  int tiles;      // tiles of query rows; 0: nothing to do
+};
+// A sequence as the call may read it; `bad`: something had to be clamped.
+__device__ __forceinline__ void read_sequence(const WeighParams& P, int b, int& begin, int& n, int& first, int& slots, bool& bad) {
+  const int x = P.cu[b], y = P.cu[b + 1], f = P.first[b];
+  begin = min(max(x, 0), P.total);
+  const int end = min(max(y, begin), P.total);
+  n = end - begin;
+  first = min(max(f, 0), P.pg.cap);
+  const int64_t most = (int64_t)first + n;
+  slots = n == 0 ? 0 : (int)min(most, (int64_t)P.pg.cap);
+  bad = begin != x || end != y || (n > 0 && (first != f || most > P.pg.cap));
+}
+__device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item) {
+  WeighItem w;
+  const int per = P.batch * P.kv_heads;
+  const int64_t tile = item / per;
+  const int u = (int)(item - tile * per);
+  w.b = u / P.kv_heads;
+  w.h = u - w.b * P.kv_heads;
+  bool bad;
+  read_sequence(P, w.b, w.begin, w.n, w.first, w.slots, bad);
+  w.j0 = (int)min(tile * 128, (int64_t)0x7FFFFF00);
+  w.tiles = 0;
+  w.i0 = 0;
+  if (w.j0 < w.slots) {
+    w.i0 = max(0, w.j0 - w.first);
+    w.tiles = (w.n - w.i0 + P.tpt - 1) / P.tpt;
+  }
+  return w;
+}
+
+__global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_constant__ WeighParams P) {
+  extern __shared__ unsigned char raw[];
+  __shared__ WeighControl C;
+  __shared__ int64_t items;
+  unsigned char* qring = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Ctl* ctl = &C.ctl;
+  if (tid == 0) {
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(&C.full[i], 1);
+      mbar_init(&C.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&C.sfull[i], 1);
+      mbar_init(&C.sempty[i], 4);
+    }
+    mbar_init(&C.keys, 4);
+    mbar_init(&C.keys_free, 1);
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssuer) tmem_alloc(&ctl->tmem_base, kTmemCols);
+  // rows that no token fills are zero in every stage: their logits are finite
+  const int filled = P.tpt * P.group;
+  for (int i = tid; i < kQStages * 2 * (kCols - filled) * 8; i += kWeighThreads) {
+    const int slab = i / ((kCols - filled) * 8), in = i - slab * (kCols - filled) * 8;
+    *reinterpret_cast<uint4*>(qring + slab * kQSlab + filled * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  depend_wait();
+  depend_go();
+  if (warp == 0) {
+    // tiles of slots of the longest sequence: the order of items is tile by tile
+    int most = 0;
+    bool bad = false;
+    for (int b = lane; b < P.batch; b += 32) {
+      int begin, n, first, slots;
+      bool clamped;
+      read_sequence(P, b, begin, n, first, slots, clamped);
+      bad |= clamped;
+      most = max(most, slots);
+    }
+    most = __reduce_max_sync(kFull, most);
+    if (__any_sync(kFull, bad) && lane == 0 && blockIdx.x == 0) latch(P.status, BKV_ERR_INVALID_ARG);
+    if (lane == 0) items = ((int64_t)most + 127) / 128 * P.batch * P.kv_heads;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int64_t total = items;
+
+  if (warp == kProducer) {
+    const uint64_t keep = policy_evict_last();  // queries are read once per tile of slots
+    uint32_t it = 0;
+    bool go = true;
+    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
+      const WeighItem w = item_of(P, item);
+      for (int k = 0; k < w.tiles; ++k, ++it) {
+        const int s = it % kQStages;
+        go = wait(&C.empty[s], (it / kQStages & 1) ^ 1, ctl, P.status);
+        if (!go) break;
+        if (lane == 0) {
+          mbar_expect_tx(&C.full[s], (uint32_t)(2 * filled * 128));
+          const int t = w.begin + w.i0 + k * P.tpt;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            tma_rows(smem_u32(qring + s * kQTile + x * kQSlab), &P.qmap, x * 64, w.h * P.group, t, &C.full[s], keep);
+        }
+        __syncwarp();
+      }
+    }
+    // copies under way land before the CTA's shared memory goes
+    for (uint32_t k = it > kQStages ? it - kQStages : 0; k < it; ++k)
+      wait_done(&C.full[k % kQStages], k / kQStages & 1);
+  } else if (warp == kIssuer) {
+    const uint32_t e = lane_elected();
+    const uint32_t idesc = idesc_bf16(128, kCols);
+    uint32_t it = 0, nth = 0;
+    bool go = true;
+    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
+      const WeighItem w = item_of(P, item);
+      if (w.tiles == 0) continue;
+      go = wait(&C.keys, nth & 1, ctl, P.status);
+      tc_fence_after();
+      for (int k = 0; go && k < w.tiles; ++k, ++it) {
+        const int s = it % kQStages, x = it & 1;
+        go = wait(&C.full[s], it / kQStages & 1, ctl, P.status) && wait(&C.sempty[x], (it / 2 & 1) ^ 1, ctl, P.status);
+        if (!go) break;
+        tc_fence_after();
+        const uint32_t q = smem_u32(qring + s * kQTile);
+        const uint32_t b0 = ((q & 0x3FFFFu) >> 4) | (1u << 16), b1 = (((q + kQSlab) & 0x3FFFFu) >> 4) | (1u << 16);
+        const uint32_t d = tmem + x * kCols, a = tmem + kTmemKeys;
+        mma_ts<0, 0>(d, a, b0, idesc, 0, e);
+        mma_ts<8, 2>(d, a, b0, idesc, 1, e);
+        mma_ts<16, 4>(d, a, b0, idesc, 1, e);
+        mma_ts<24, 6>(d, a, b0, idesc, 1, e);
+        mma_ts<32, 0>(d, a, b1, idesc, 1, e);
+        mma_ts<40, 2>(d, a, b1, idesc, 1, e);
+        mma_ts<48, 4>(d, a, b1, idesc, 1, e);
+        mma_ts<56, 6>(d, a, b1, idesc, 1, e);
+        commit_if(&C.empty[s], e);
+        commit_if(&C.sfull[x], e);
+      }
+      commit_if(&C.keys_free, e);
+      ++nth;
+    }
+    // products under way are done before TMEM goes
+    if (nth > 0) wait_done(&C.keys_free, (nth - 1) & 1);
+  } else {
+    uint32_t it = 0, nth = 0;
+    bool go = true;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    int ct[3], cg[3];  // this lane's columns of a tile: token and head
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      ct[p] = (lane + 32 * p) / P.group;
+      cg[p] = lane + 32 * p - ct[p] * P.group;
+    }
+    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
+      const WeighItem w = item_of(P, item);
+      if (w.tiles == 0) continue;
+      // this thread's key, into its lane of TMEM
+      const int slot = w.j0 + tid;
+      const int64_t row = slot < w.slots ? pool_row(P.pg, P.kv_heads, w.b, w.h, slot) : -1;
+      if (slot < w.slots && row < 0) latch(P.status, BKV_ERR_INVALID_ARG);
+      const bool in = row >= 0 && BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status);
+      if (nth > 0) go = wait(&C.keys_free, (nth - 1) & 1, ctl, P.status);
+      if (!go) break;
+      tc_fence_after();
+      uint32_t odd = 0;  // the key holds an infinity or NaN: rows that no token fills would make NaN of it
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t r[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = in ? P.K[row * 16 + x * 4 + k] : make_uint4(0, 0, 0, 0);
+          r[4 * k] = v.x;
+          r[4 * k + 1] = v.y;
+          r[4 * k + 2] = v.z;
+          r[4 * k + 3] = v.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) odd |= ((r[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+        tmem_store16(tmem + lanes + kTmemKeys + x * 16, r);
+      }
+      const bool finite = !__any_sync(kFull, odd != 0);
+      tmem_stored();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C.keys);
+      ++nth;
+
+      // columns: this thread sees query rows from G * (slot - first - token of the tile's first row) on
+      const uint64_t scale = pair(P.scale_log2, P.scale_log2);
+      uint64_t sum[2] = {0ull, 0ull};
+      auto column = [&](int k, int part) {
+        const int i = w.i0 + k * P.tpt + ct[part];
+        if (lane + 32 * part >= filled || i >= w.n) return -__builtin_huge_valf();
+        const float x = P.row_lse[((int64_t)w.begin + i) * P.heads + w.h * P.group + cg[part]];
+        return x == -__builtin_huge_valf() ? x : -x * kLog2e;  // a row that sees nothing gives nothing
+      };
+      float next[3] = {column(0, 0), column(0, 1), column(0, 2)};
+      for (int k = 0; k < w.tiles; ++k, ++it) {
+        const int x = it & 1;
+        float* col = C.col[warp][x];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) col[lane + 32 * p] = next[p];
+        __syncwarp();  // also: the tile before's columns are read
+        if (k + 1 < w.tiles) {
+#pragma unroll
+          for (int p = 0; p < 3; ++p) next[p] = column(k + 1, p);
+        }
+        go = wait(&C.sfull[x], it / 2 & 1, ctl, P.status);
+        if (!go) break;
+        tc_fence_after();
+        const int i = w.i0 + k * P.tpt;
+        const int from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
+        const int to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
+        // whole tiles of columns that all slots of the tile see
+        const bool whole = finite && w.j0 + 127 <= w.first + i && w.n - i >= P.tpt;
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          float v[32];
+          tmem_ld32(tmem + lanes + x * kCols + c0, v);
+          tmem_wait_ld();
+          tie(v);
+          if (c0 + 32 == kCols) {  // read: the buffer may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&C.sempty[x]);
+          }
+          const float4* cols = reinterpret_cast<const float4*>(col + c0);
+          if (whole) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 c = cols[q];
+              float a0, a1, a2, a3;
+              unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a0, a1);
+              unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a2, a3);
+              sum[0] = add_pair(sum[0], pair(fast_exp2(a0), fast_exp2(a1)));
+              sum[1] = add_pair(sum[1], pair(fast_exp2(a2), fast_exp2(a3)));
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float a = fmaf(v[q], P.scale_log2, col[c0 + q]);
+              const float p = c0 + q >= from && c0 + q < to ? fast_exp2(a) : 0.f;
+              sum[q >> 1 & 1] = add_pair(sum[q >> 1 & 1], q & 1 ? pair(0.f, p) : pair(p, 0.f));
+            }
+          }
+        }
+      }
+      if (go && in) {
+        float a0, a1, a2, a3;
+        unpair(sum[0], a0, a1);
+        unpair(sum[1], a2, a3);
+        const float s = (a0 + a1) + (a2 + a3);
+        float old = 0.f;
+        if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
+        P.weights[row] = old + s;
+        if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace
+
+bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride) {
+  // the driver's encoder, looked up once per process (thread-safe static initialisation)
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult qres;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qres) != cudaSuccess ||
+        qres != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.heads, (cuuint64_t)p.total};
+  const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.tpt};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(&p.qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_weigh(const WeighParams& p, int grid, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeighSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kWeighThreads);
+  cfg.dynamicSmemBytes = kWeighSmem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weigh_kernel, p);
+}
+
+}  // namespace bkv

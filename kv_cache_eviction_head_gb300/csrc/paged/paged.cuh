@@ -1,6 +1,7 @@
 // Declarations of the calls over paged caches: rotary store (k_store_paged.cu),
-// attention of one new token (k_attend_paged.cu), eviction by accumulated weight
-// (k_evict_weight.cu). Host checks and launches: paged_api.cu.
+// attention of one new token (k_attend_paged.cu), prompt weights (k_weigh.cu),
+// eviction by accumulated weight (k_evict_weight.cu). Host checks and launches:
+// paged_api.cu.
 #pragma once
 
 #include "attend/attend.cuh"
@@ -93,6 +94,25 @@ struct AttendPagedParams {
   float* logits;           // [tile][group][16], log2 units; with weights only
 };
 cudaError_t launch_attend_paged(const AttendPagedParams& p, cudaStream_t s);
+
+constexpr int kWeighRows = 96;  // query rows per tile: query heads per KV head, at most
+struct WeighParams {
+  CUtensorMap qmap;        // queries [tokens][heads][d], box (64, group, tpt)
+  Pages pg;
+  const uint4* K;
+  const float* row_lse;    // [total][heads]
+  const int32_t* cu;       // [batch + 1]
+  const int32_t* first;    // [batch]
+  float* weights;
+  uint32_t* status;
+  float decay;
+  float scale_log2;
+  int batch, heads, kv_heads, group, total;
+  int tpt;                 // tokens per tile of query rows
+};
+cudaError_t launch_weigh(const WeighParams& p, int grid, cudaStream_t s);
+// Fills p's tensor map (host only). False on failure.
+bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride);
 
 struct EvictWeightParams {
   Pages pg;

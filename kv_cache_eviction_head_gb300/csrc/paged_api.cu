@@ -202,6 +202,46 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
   return bkv::launch_attend_paged(p, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 
+bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const void* q, int64_t q_stride, const float* lse,
+                            const void* K, const int32_t* cu_seqlens, const int32_t* first_slot, int32_t total,
+                            float* weights, float decay, uint32_t* status, void* cuda_stream) {
+  NvtxRange nvtx("bkv_weigh_prompt");
+  bkv_status st = check(cfg);
+  if (st != BKV_OK) return st;
+  const bkv_config& c = *cfg;
+  bkv::WeighParams p{};
+  st = take_pages(c, pages, p.pg);
+  if (st != BKV_OK) return st;
+  if (total < 0 || !K || !weights || !cu_seqlens || !first_slot || (total > 0 && !lse) || !aligned(K, 16) || !aligned(weights, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(first_slot, 4) || !aligned(lse, 4) || !aligned(status, 4) ||
+      !strided_ok(q, q_stride, c.heads, c.d, total) || !decay_ok(decay))
+    return BKV_ERR_INVALID_ARG;
+  p.group = c.heads / c.kv_heads;
+  if (p.group > bkv::kWeighRows) return BKV_ERR_UNSUPPORTED;
+  p.K = static_cast<const uint4*>(K);
+  p.row_lse = lse;
+  p.cu = cu_seqlens;
+  p.first = first_slot;
+  p.weights = weights;
+  p.status = status;
+  p.decay = decay;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.d));
+  p.batch = c.batch;
+  p.heads = c.heads;
+  p.kv_heads = c.kv_heads;
+  p.total = total;
+  p.tpt = bkv::kWeighRows / p.group;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (total > 0 && !bkv::encode_weigh_map(p, q, q_stride)) return BKV_ERR_CUDA;
+  if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
+  if (total == 0) return BKV_OK;
+  // a block for every tile of 128 slots there can be, up to eight rounds of two per SM;
+  // blocks walk on from there
+  const int64_t items = (int64_t)c.batch * c.kv_heads * ((p.pg.cap + 127) / 128);
+  const int grid = (int)std::min<int64_t>(items, 8 * 2 * bkv::kSms);
+  return bkv::launch_weigh(p, grid, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+}
+
 bkv_status bkv_evict_weight(const bkv_config* cfg, const bkv_pages* pages, void* const* K, void* const* V,
                             float* const* weights, const int32_t* cache_lens, int32_t* kept, int32_t* new_lens,
                             uint32_t* status, void* cuda_stream) {

@@ -1,5 +1,5 @@
-"""The calls over paged caches (bkv_store_paged, bkv_attend_paged, bkv_evict_weight) against
-64-bit statements of them."""
+"""The calls over paged caches (bkv_store_paged, bkv_attend_paged, bkv_weigh_prompt,
+bkv_evict_weight) against 64-bit statements of them."""
 
 from __future__ import annotations
 
@@ -113,6 +113,74 @@ def test_attend_large_logits(bkv):
 
 def test_attend_contiguous_queries(bkv):
     assert attend_case(bkv, 8, 8, [12, 400], 16, 9, strided=False) <= 0
+
+
+# ---------------------------------------------------------------- prompt weights
+
+def weigh_case(bkv, heads, kv, lens, first, page, seed, *, decay=1.0, scale=1.0, extra=2):
+    slots = [a + b for a, b in zip(lens, first)]
+    pool = Pool(len(lens), kv, slots, page, seed)
+    cfg = pool.config(bkv, heads)
+    K = pool.fresh(slots, seed + 100)
+    total = sum(lens) + extra
+    wide = randn((total, heads + 3, D), seed + 500, scale)
+    wide[sum(lens):] = math.nan  # tokens of no sequence
+    q = wide[:, 2:2 + heads]
+    lse = torch.full((total, heads), math.nan, dtype=torch.float32, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    weights = torch.rand(pool.shape(), device="cuda") + 0.01
+    want = []
+    for b, (n, f) in enumerate(zip(lens, first)):
+        want.append(None)
+        if not n:
+            continue
+        see = torch.arange(f + n, device="cuda")[None] <= f + torch.arange(n, device="cuda")[:, None]
+        p, rel, wlse = probabilities(q[cu[b]:cu[b + 1]], pool.get(K, b, f + n), see)
+        lse[cu[b]:cu[b + 1]] = wlse.float()
+        want[b] = weight_sums(p, rel + 2.0 ** -22 * wlse.abs(), kv)
+        page_, place = pool.at(b, f + n, 0 if decay == 0 else f)
+        weights[page_, :, place] = math.nan
+    before = weights.clone()
+    status = new_status()
+    bkv.bkv_weigh_prompt(cfg, q, lse, K, i32(cu), i32(first), weights, table=pool.table, decay=decay, status=status,
+                         stream=stream())
+    assert int(status) == 0
+    worst, touched = -math.inf, torch.zeros(pool.shape(), dtype=torch.bool, device="cuda")
+    for b, (n, f) in enumerate(zip(lens, first)):
+        if not n:
+            continue
+        s, tol = want[b]
+        old = pool.get(before, b, f + n).double()
+        old = torch.zeros_like(old) if decay == 0 else torch.where(torch.arange(f + n, device="cuda") >= f, 0.0, old)
+        worst = max(worst, ref.close(pool.get(weights, b, f + n), decay * old + s, tol + 2.0 ** -22 * (old + s)))
+        page_, place = pool.at(b, f + n)
+        touched[page_, :, place] = True
+    assert torch.equal(weights[~touched].view(torch.int32), before[~touched].view(torch.int32))
+    return worst
+
+
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("heads,kv", SHAPES + [(96, 1), (52, 1), (11, 1)])
+def test_weigh_groups_and_pages(bkv, heads, kv, page):
+    lens = [33, 0, 1, 127, 128, 0, 129, 97]
+    first = [0, 5, 0, 1, 0, 0, 130, 127]
+    assert weigh_case(bkv, heads, kv, lens, first, page, 10 + heads) <= 0
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("lens,first", [([1], [0]), ([1], [300]), ([700], [0]), ([3, 1200], [900, 100]), ([24] * 40, [9] * 40)])
+def test_weigh_few_and_many_sequences(bkv, lens, first, decay):
+    assert weigh_case(bkv, 32, 8, lens, first, 16, 3, decay=decay) <= 0
+
+
+def test_weigh_large_logits(bkv):
+    assert weigh_case(bkv, 8, 2, [400, 90], [0, 200], 64, 8, scale=40.0) <= 0
+
+
+def test_weigh_more_tiles_than_blocks(bkv):
+    """More tiles of slots than a launch has blocks: blocks take several."""
+    lens = [130] * 320
+    assert weigh_case(bkv, 4, 4, lens, [0] * 320, None, 9) <= 0
 
 
 # ---------------------------------------------------------------- eviction by weight

@@ -36,12 +36,14 @@ p, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c
 KINDS = {
     "bkv_store_paged": [p, i64, p, i64, p, i64, i32] + [p] * 9,
     "bkv_attend_paged": [p, i64, p, p, p, p, p, p, f32, p, sz, p, p],
+    "bkv_weigh_prompt": [p, i64, p, p, p, p, i32, p, f32, p, p],
     "bkv_evict_weight": [p] * 8,
 }
 GOOD = {
     "bkv_store_paged": dict(q=A, qs=1024, k=A, ks=256, v=A, vs=256, total=5, cu=A, first=A, pos=A, depth=0, q_rot=A, K=A, V=A,
                             status=0, stream=0),
     "bkv_attend_paged": dict(q=A, qs=1024, K=A, V=A, lens=A, out=A, lse=0, weights=A, decay=1.0, ws=A, size=1 << 40, status=0, stream=0),
+    "bkv_weigh_prompt": dict(q=A, qs=1024, lse=A, K=A, cu=A, first=A, total=5, weights=A, decay=1.0, status=0, stream=0),
     "bkv_evict_weight": dict(K=layers(A, A), V=layers(A, A), W=layers(A, A), lens=A, kept=A, new=0, status=0, stream=0),
 }
 BAD = {
@@ -51,6 +53,8 @@ BAD = {
     "bkv_attend_paged": [dict(q=0), dict(q=A + 8), dict(qs=512), dict(qs=1025), dict(K=0), dict(V=A + 8), dict(lens=0), dict(lens=A + 1),
                          dict(out=0), dict(out=A + 4), dict(lse=A + 2), dict(weights=A + 2), dict(decay=-0.1), dict(decay=1.5),
                          dict(decay=math.nan), dict(status=A + 1)],
+    "bkv_weigh_prompt": [dict(q=0), dict(qs=1025), dict(lse=0), dict(lse=A + 2), dict(K=0), dict(cu=0), dict(first=A + 2), dict(total=-1),
+                         dict(weights=0), dict(weights=A + 1), dict(decay=2.0), dict(decay=math.nan), dict(status=A + 2)],
     "bkv_evict_weight": [dict(K=layers(A, 0)), dict(V=layers(A + 8, A)), dict(W=layers(A, A + 2)), dict(W=layers(0, A)), dict(lens=0),
                          dict(lens=A + 2), dict(kept=0), dict(kept=A + 1), dict(new=A), dict(new=A + 2), dict(status=A + 2)],
 }
@@ -105,6 +109,7 @@ def test_attend_workspace(bkv):
 
 
 def test_unsupported(bkv):
+    assert call(bkv, "bkv_weigh_prompt", cfg_for(bkv, heads=97, kv_heads=1), {**GOOD["bkv_weigh_prompt"], "qs": 97 * 128}.values()) == 7
     big = cfg_for(bkv, budget=(1 << 19) + 1, max_cache=1 << 20, flags=2)
     assert call(bkv, "bkv_evict_weight", big, GOOD["bkv_evict_weight"].values()) == 7
 
@@ -153,6 +158,8 @@ def test_the_binding_refuses_what_does_not_match(bkv, monkeypatch):
         bkv.bkv_attend_paged_bytes(c, b, table)
     with pytest.raises(ValueError, match="q:"):
         bkv.bkv_attend_paged(c, t(3, 8, 128), K, K, b, t(3, 8, 128), ws)
+    with pytest.raises(ValueError, match="q:"):
+        bkv.bkv_weigh_prompt(c, t(8, 128), None, K, b, b, None)
     with pytest.raises(ValueError, match="q_pre:"):
         bkv.bkv_store_paged(c, bkv.make_rope(), None, None, None, b, b, b, None, K, K)
     with pytest.raises(ValueError, match="K:"):
