@@ -41,6 +41,8 @@ constexpr int kStages = 3;                  // tiles under way per warp
 constexpr int kTileBytes16 = 2 * kTileSlots * kD * 2;  // K and V of a tile: 8 KB
 constexpr int kAttendSmem = kAttendWarps * kStages * kTileBytes16;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 5;                // per SM
+constexpr int kJoinTiles = 16;              // tiles of a block's weights, at least
 constexpr float kMinusInf = -__builtin_huge_valf();
 constexpr float kLag = 8.f;
 
@@ -54,8 +56,11 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Copies 16 bytes, or writes 16 zero bytes.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -70,7 +75,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -79,34 +84,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ int len_of(const AttendPagedParams& P, int b) { return min(max(P.lens[b], 0), P.pg.cap); }
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + kTileSlots - 1) / kTileSlots); }
 
-// Tiles of the whole call per (KV head, chunk): one warp, all lanes get it. `bad`: a length was clamped.
-__device__ __forceinline__ int64_t all_tiles(const AttendPagedParams& P, int lane, bool& bad) {
-  int64_t n = 0;
+// Tiles of the whole call per (KV head, chunk), fewer than 2^31 / units: one warp, all lanes
+// get it. `bad`: a length was clamped.
+__device__ __forceinline__ int all_tiles(const AttendPagedParams& P, int lane, bool& bad) {
+  int n = 0;
   bad = false;
+#pragma unroll 4
   for (int b = lane; b < P.batch; b += 32) {
-    const int len = len_of(P, b);
-    bad |= len != P.lens[b];
+    const int given = P.lens[b], len = min(max(given, 0), P.pg.cap);
+    bad |= len != given;
     n += tiles_of(len);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(kAll, n, off);
   bad = __any_sync(kAll, bad);
-  return n;
+  return __reduce_add_sync(kAll, n);
 }
 // Tiles per share. One tile per warp at least; more when there are not warps enough.
-__device__ __forceinline__ int64_t share_of(int64_t tiles) {
-  return max((tiles + kAttendShares - 1) / kAttendShares, (int64_t)1);
-}
+__device__ __forceinline__ int share_of(int tiles) { return max((tiles + kAttendShares - 1) / kAttendShares, 1); }
 // The sequence that tile t (of `per` tiles for each of a sequence's own) lies in, and the
 // sum of the tiles in front of it; b = batch behind the last. One warp.
-__device__ __forceinline__ void find_sequence(const AttendPagedParams& P, int64_t t, int per, int lane, int& b, int64_t& before) {
-  int64_t base = 0;
+__device__ __forceinline__ void find_sequence(const AttendPagedParams& P, int t, int per, int lane, int& b, int& before) {
+  int base = 0;
   for (int b0 = 0; b0 < P.batch; b0 += 32) {
-    const int64_t n = b0 + lane < P.batch ? tiles_of(len_of(P, b0 + lane)) : 0;
-    int64_t upto = n;
+    const int n = b0 + lane < P.batch ? tiles_of(len_of(P, b0 + lane)) : 0;
+    int upto = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, upto, off);
+      const int y = __shfl_up_sync(kAll, upto, off);
       if (lane >= off) upto += y;
     }
     const unsigned hit = __ballot_sync(kAll, t < (base + upto) * per);
@@ -128,7 +131,7 @@ struct Place {
   int i, n;        // tile of the unit, its tiles
   int len;
   int page;        // pool page of the tile, or -1
-  int64_t before;  // tiles (per unit) of the sequences in front
+  int before;      // tiles (per unit) of the sequences in front
 };
 __device__ __forceinline__ void look_up(const AttendPagedParams& P, Place& p) {
   p.page = pool_page(P.pg, p.b, page_of(P.pg, p.i * kTileSlots));
@@ -160,21 +163,21 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   depend_go();
 
   bool bad;
-  const int64_t total = all_tiles(P, lane, bad) * units;
+  const int total = all_tiles(P, lane, bad) * units;
   if (w == 0 && lane == 0 && bad) latch(P.status, BKV_ERR_INVALID_ARG);
-  const int64_t share = share_of(total);
-  const int64_t t0 = w * share;
-  if (t0 >= total) return;
-  const int count = (int)(min(t0 + share, total) - t0);
+  const int share = share_of(total);
+  const int64_t begin = (int64_t)w * share;
+  if (begin >= total) return;
+  const int t0 = (int)begin, count = min(share, total - t0);
 
   Place c;
   find_sequence(P, t0, units, lane, c.b, c.before);
   c.len = len_of(P, c.b);
   c.n = tiles_of(c.len);
   {
-    const int64_t in = t0 - c.before * units;
-    c.u = (int)(in / c.n);
-    c.i = (int)(in - (int64_t)c.u * c.n);
+    const int in = t0 - c.before * units;
+    c.u = in / c.n;
+    c.i = in - c.u * c.n;
   }
   look_up(P, c);
   Place a = c;  // the next tile to copy; its page is looked up one tile ahead
@@ -194,21 +197,31 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
     if (!BKV_IN_RANGE(base >= 0 && base + rows <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) rows = 0, base = 0;
     if (lane == 0) rows_in[warp][stage] = rows;
     const uint32_t dst = ring + stage * kTileBytes16;
-    const uint4* k = P.K + base * 16 + quad;
-    const uint4* v = P.V + base * 16 + row;
+    const uint4* k = P.K + base * 16 + (row * 16 + quad);
+    const uint4* v = P.V + base * 16 + (quad * 32 + row);
+    if (rows == kTileSlots) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r = row + 8 * t;
-      const bool in = r < rows;
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) copy16(dst + (t * 4 + j) * 512, k + (in ? r * 16 : 0) + 4 * j, in);
-    }
+        for (int j = 0; j < 4; ++j) copy16(dst + (t * 4 + j) * 512, k + t * 128 + 4 * j);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int r = 2 * quad + (s & 1) + 8 * (s >> 1);
-      const bool in = r < rows;
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) copy16(dst + (8 + s * 2 + j) * 512, v + (in ? r * 16 : 0) + 8 * j, in);
+        for (int j = 0; j < 2; ++j) copy16(dst + (8 + s * 2 + j) * 512, v + (s & 1) * 16 + (s >> 1) * 128 + 8 * j);
+    } else {  // zeros for the slots behind the last: what lies there may be NaN
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const bool in = row + 8 * t < rows;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy16_if(dst + (t * 4 + j) * 512, in ? k + t * 128 + 4 * j : P.K, in);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bool in = 2 * quad + (s & 1) + 8 * (s >> 1) < rows;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          copy16_if(dst + (8 + s * 2 + j) * 512, in ? v + (s & 1) * 16 + (s >> 1) * 128 + 8 * j : P.V, in);
+      }
     }
   };
   int ahead = 0;  // tiles copied or under way
@@ -276,30 +289,39 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
     copies_commit();
     stage = stage == kStages - 1 ? 0 : stage + 1;
 
-    float s[2][4];
+    // all of the tile's pieces are asked for at once; two sums per eight slots halve the
+    // chain of products
+    uint4 kf[8], vf[8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    for (int i = 0; i < 8; ++i) kf[i] = lds16(at + i * 512);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 k = lds16(at + (t * 4 + j) * 512);
+    for (int i = 0; i < 8; ++i) vf[i] = lds16(at + (8 + i) * 512);
+    float s[2][4], s1[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = s1[t][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint4 k = kf[t * 4 + j];
         mma16816(s[t], qlo[2 * j][0], NT == 2 ? qhi[NT == 2 ? 2 * j : 0][0] : 0u, qlo[2 * j][1],
                  NT == 2 ? qhi[NT == 2 ? 2 * j : 0][1] : 0u, k.x, k.y);
-        mma16816(s[t], qlo[2 * j + 1][0], NT == 2 ? qhi[NT == 2 ? 2 * j + 1 : 0][0] : 0u, qlo[2 * j + 1][1],
+        mma16816(s1[t], qlo[2 * j + 1][0], NT == 2 ? qhi[NT == 2 ? 2 * j + 1 : 0][0] : 0u, qlo[2 * j + 1][1],
                  NT == 2 ? qhi[NT == 2 ? 2 * j + 1 : 0][1] : 0u, k.z, k.w);
       }
-    }
     // this thread's logits of head `row` (and row + 8): slots 2 quad, 2 quad + 1, and 8 on
     float x[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[t][e] = s[e >> 1][2 * t + (e & 1)] * P.scale_log2;
+        x[t][e] = (s[e >> 1][2 * t + (e & 1)] + s1[e >> 1][2 * t + (e & 1)]) * P.scale_log2;
         if (rows < kTileSlots && 2 * quad + (e & 1) + 8 * (e >> 1) >= rows) x[t][e] = kMinusInf;
       }
     if (P.logits) {
-      const int64_t tile = c.before * P.kv_heads + (int64_t)h * c.n + c.i;
+      const int64_t tile = (int64_t)c.before * P.kv_heads + h * c.n + c.i;
       if (tile < P.tiles_cap) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -352,8 +374,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint4 v0 = lds16(at + (8 + j) * 512), v1 = lds16(at + (10 + j) * 512);
-      const uint4 v2 = lds16(at + (12 + j) * 512), v3 = lds16(at + (14 + j) * 512);
+      const uint4 v0 = vf[j], v1 = vf[2 + j], v2 = vf[4 + j], v3 = vf[6 + j];
       const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
       const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
@@ -422,76 +443,86 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   }
 }
 
-// The pieces of unit u of sequence b: shares c0 .. c1, share c0's piece is its second.
+// The pieces of unit u of a sequence: shares c0 .. c1, share c0's piece is its second.
 struct Pieces {
-  int64_t c0, c1;
-  __device__ __forceinline__ int64_t at(int64_t c) const { return 2 * c + (c == c0 ? 1 : 0); }
+  int c0, c1;
+  __device__ __forceinline__ int at(int c) const { return 2 * c + (c == c0 ? 1 : 0); }
 };
-__device__ __forceinline__ Pieces pieces_of(int64_t before, int u, int n, int units, int64_t share) {
-  const int64_t from = before * units + (int64_t)u * n;
+__device__ __forceinline__ Pieces pieces_of(int before, int u, int n, int units, int share) {
+  const int from = before * units + u * n;
   return Pieces{from / share, (from + n - 1) / share};
 }
 // A head's largest reference over the unit's pieces and the sum relative to it. One warp,
 // all lanes get it.
 __device__ __forceinline__ float2 join_sum(const AttendPagedParams& P, const Pieces& pc, int in_chunk, int lane) {
-  float m = kMinusInf;
-  for (int64_t c = pc.c0 + lane; c <= pc.c1; c += 32) {
-    const float x = P.part_ml[pc.at(c) * 16 + in_chunk].x;
-    m = fmaxf(m, x);
-  }
+  // eight pieces a lane at once, more in rounds: a running maximum and sum
+  float m = kMinusInf, l = 0.f;
+  for (int c0 = pc.c0; c0 <= pc.c1; c0 += 256) {
+    float2 x[8];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
-  float l = 0.f;
-  for (int64_t c = pc.c0 + lane; c <= pc.c1; c += 32) {
-    const float2 x = P.part_ml[pc.at(c) * 16 + in_chunk];
+    for (int k = 0; k < 8; ++k) {
+      const int c = c0 + k * 32 + lane;
+      x[k] = c <= pc.c1 ? P.part_ml[pc.at(c) * 16 + in_chunk] : make_float2(kMinusInf, 0.f);
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+    if (m != kMinusInf) l *= exp2_approx(m - top);
     // a piece without a finite logit has no part (its sum is 0, or NaN, which stays)
-    l += x.x == kMinusInf ? x.y : x.y * exp2_approx(x.x - m);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) l += x[k].x == kMinusInf ? x[k].y : x[k].y * exp2_approx(x[k].x - top);
+    m = top;
   }
+  float top = m;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+  if (m != kMinusInf) l *= exp2_approx(m - top);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kAll, l, off);
-  return make_float2(m, l);
+  return make_float2(top, l);
 }
 
-__global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(const __grid_constant__ AttendPagedParams P) {
-  __shared__ float4 sums[kJoinThreads / 32][32];
+// Outputs of units that lie in several shares, and weights.
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(const __grid_constant__ AttendPagedParams P) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float4 sums[kWarps][32];
+  __shared__ float lse2[kMaxGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = P.kv_heads * P.chunks;
   depend_wait();
   depend_go();
   bool bad;
-  const int64_t tiles = all_tiles(P, lane, bad);
-  const int64_t share = share_of(tiles * units);
+  const int tiles = all_tiles(P, lane, bad);
+  const int share = share_of(tiles * units);
 
-  // outputs whose unit lies in several shares, and those of sequences without a slot.
-  // Few rows: a block each, its warps take the pieces in turn; many: a warp each.
-  const int64_t rows = (int64_t)P.batch * P.heads;
-  const bool wide = rows <= 4 * (int64_t)gridDim.x;
-  const int warps = wide ? kJoinThreads / 32 : 1;
-  const int64_t step_rows = wide ? gridDim.x : (int64_t)gridDim.x * (kJoinThreads / 32);
-  for (int64_t r = wide ? blockIdx.x : (int64_t)blockIdx.x * (kJoinThreads / 32) + warp; r < rows; r += step_rows) {
-    const int b = (int)(r / P.heads), head = (int)(r - (int64_t)b * P.heads);
+  // Outputs, also those of sequences without a slot. Few rows: a block each (the last blocks,
+  // the first have weights to do), its warps take the pieces in turn; many: a warp each.
+  const int rows = P.batch * P.heads;
+  const bool wide = rows <= (int)gridDim.x;
+  const int block = gridDim.x - 1 - blockIdx.x;
+  for (int r = wide ? block : block * kWarps + warp; r < rows; r += gridDim.x * (wide ? 1 : kWarps)) {
+    const int b = r / P.heads, head = r - b * P.heads;
     const int len = len_of(P, b);
     if (len == 0) {
       if (wide && warp != 0) continue;
-      reinterpret_cast<uint2*>(P.out)[r * 32 + lane] = make_uint2(0, 0);
+      reinterpret_cast<uint2*>(P.out)[(int64_t)r * 32 + lane] = make_uint2(0, 0);
       if (lane == 0 && P.lse) P.lse[r] = kMinusInf;
       continue;
     }
     const int h = head / P.group, g = head - h * P.group, u = h * P.chunks + g / P.chunk, in = g % P.chunk;
-    int64_t before = 0;
+    int before = 0;
     for (int x = lane; x < b; x += 32) before += tiles_of(len_of(P, x));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(kAll, before, off);
+    before = __reduce_add_sync(kAll, before);
     const Pieces pc = pieces_of(before, u, tiles_of(len), units, share);
-    if (pc.c0 == pc.c1) continue;  // block-uniform where the block shares a row
+    if (pc.c0 == pc.c1) continue;  // one answer for the whole block where it shares a row
     const float2 ml = join_sum(P, pc, in, lane);
     const float inv = 1.f / ml.y;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t from = pc.c0 + (wide ? warp : 0);
+    const int by = wide ? kWarps : 1;
 #pragma unroll 8
-    for (int64_t c = from; c <= pc.c1; c += warps) {
+    for (int c = pc.c0 + (wide ? warp : 0); c <= pc.c1; c += by) {
       const float m = P.part_ml[pc.at(c) * 16 + in].x;
-      const float4 x = P.part_o[(pc.at(c) * P.chunk + in) * 32 + lane];
+      const float4 x = P.part_o[(int64_t)(pc.at(c) * P.chunk + in) * 32 + lane];
       const float f = m == kMinusInf ? 1.f : exp2_approx(m - ml.x) * inv;  // without a finite logit: o is 0, or NaN
       y.x = fmaf(f, x.x, y.x);
       y.y = fmaf(f, x.y, y.y);
@@ -503,7 +534,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(const __grid_c
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
-        for (int k = 1; k < kJoinThreads / 32; ++k) {
+        for (int k = 1; k < kWarps; ++k) {
           const float4 x = sums[k][lane];
           y.x += x.x;
           y.y += x.y;
@@ -515,7 +546,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(const __grid_c
       if (warp != 0) continue;
     }
     if (ml.y == 0.f) y.x = y.y = y.z = y.w = __builtin_nanf("");  // every logit is -inf
-    reinterpret_cast<uint2*>(P.out)[r * 32 + lane] = make_uint2(pack2_bf16(y.x, y.y), pack2_bf16(y.z, y.w));
+    reinterpret_cast<uint2*>(P.out)[(int64_t)r * 32 + lane] = make_uint2(pack2_bf16(y.x, y.y), pack2_bf16(y.z, y.w));
     const float check = (y.x * 0.f + y.y * 0.f) + (y.z * 0.f + y.w * 0.f);
     if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
     if (lane == 0) {
@@ -526,67 +557,73 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(const __grid_c
   }
 
   if (!P.weights) return;
-  // weights: a warp takes an equal share of the (sequence, KV head, tile) row, a thread a slot
-  const int64_t all = tiles * P.kv_heads;
-  if (all > P.tiles_cap) {  // a page in two tables: more tiles than the pool has slots for
+  // Weights: a block takes an equal share of the (sequence, KV head, tile) row, unit by unit:
+  // its warps find the heads' sums, then a thread takes four slots of a tile.
+  const int64_t room = P.tiles_cap;
+  const int64_t all = (int64_t)tiles * P.kv_heads;
+  if (all > room) {  // a page in two tables: more tiles than the pool has slots for
     if (blockIdx.x == 0 && tid == 0) latch(P.status, BKV_ERR_INVALID_ARG);
     return;
   }
-  const int64_t nw = (int64_t)gridDim.x * (kJoinThreads / 32), w = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp;
-  const int64_t each = (all + nw - 1) / nw;
-  int64_t t = w * each;
-  const int64_t end = min(t + each, all);
-  if (t >= end) return;
-  int b;
-  int64_t before;
+  const int each = max((int)((all + gridDim.x - 1) / gridDim.x), kJoinTiles);
+  const int64_t begin = (int64_t)blockIdx.x * each;
+  if (begin >= all) return;
+  int t = (int)begin;
+  const int end = (int)min(begin + each, all);
+  int b, before;
   find_sequence(P, t, P.kv_heads, lane, b, before);
-  while (t < end) {
-    const int len = len_of(P, b), n = tiles_of(len);
-    if (n == 0) {
-      ++b;
-      continue;
-    }
-    const int64_t in = t - before * P.kv_heads;
-    const int h = (int)(in / n), i0 = (int)(in - (int64_t)h * n);
-    if (h >= P.kv_heads) {
-      before += n;
-      ++b;
-      continue;
-    }
-    const int cnt = (int)min((int64_t)(n - i0), end - t);
-    for (int g0 = 0; g0 < P.group; g0 += 32) {  // 32 heads' sums at a time, a lane each
-      float mine = 0.f;
-      const int gn = min(32, P.group - g0);
-      for (int g = 0; g < gn; ++g) {
-        const int u = h * P.chunks + (g0 + g) / P.chunk;
-        const Pieces pc = pieces_of(before, u, n, units, share);
-        float x;
-        if (pc.c0 == pc.c1) {
-          x = P.lse2[(int64_t)b * P.heads + h * P.group + g0 + g];
-        } else {
-          const float2 ml = join_sum(P, pc, (g0 + g) % P.chunk, lane);
-          x = ml.x + log2f(ml.y);
-        }
-        if (lane == g) mine = x;
+  int len = len_of(P, b), n = tiles_of(len), h = (t - before * P.kv_heads) / n, i0 = t - before * P.kv_heads - h * n;
+  while (true) {
+    const int cnt = min(n - i0, end - t);
+    for (int g = warp; g < P.group; g += kWarps) {
+      const Pieces pc = pieces_of(before, h * P.chunks + g / P.chunk, n, units, share);
+      float x;
+      if (pc.c0 == pc.c1) {
+        x = P.lse2[(int64_t)b * P.heads + h * P.group + g];
+      } else {
+        const float2 ml = join_sum(P, pc, g % P.chunk, lane);
+        x = ml.x + log2f(ml.y);
       }
-      for (int s0 = 0; s0 < cnt * kTileSlots; s0 += 32) {
-        const int s = s0 + lane, i = i0 + s / kTileSlots, slot = i * kTileSlots + s % kTileSlots;
-        const bool in_len = s < cnt * kTileSlots && slot < len;
-        const int64_t row = in_len ? pool_row(P.pg, P.kv_heads, b, h, slot) : -1;
-        const float* x = P.logits + ((t + s / kTileSlots) * P.group + g0) * kTileSlots + s % kTileSlots;
-        float sum = 0.f;
-        for (int g = 0; g < gn; ++g) {
-          const float lse2 = __shfl_sync(kAll, mine, g);
-          if (row >= 0) sum += exp2_approx(x[g * kTileSlots] - lse2);
-        }
-        if (row < 0 || !BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) continue;
-        float old = 0.f;
-        if (g0 > 0) old = P.weights[row];
-        else if (slot != len - 1 && P.decay != 0.f) old = P.decay * P.weights[row];
-        P.weights[row] = old + sum;
+      if (lane == 0) lse2[g] = x;
+    }
+    __syncthreads();
+    for (int q = tid; q < cnt * 4; q += kJoinThreads) {
+      const int slot = (i0 + q / 4) * kTileSlots + q % 4 * 4, in = min(4, len - slot);
+      if (in <= 0) continue;
+      const int64_t row = pool_row(P.pg, P.kv_heads, b, h, slot);
+      if (row < 0 || !BKV_IN_RANGE(row + in <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) continue;
+      float* w = P.weights + row;
+      float old[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = e < in && P.decay != 0.f && slot + e != len - 1 ? w[e] : 0.f;
+      const float4* x = reinterpret_cast<const float4*>(P.logits + (int64_t)(t + q / 4) * P.group * kTileSlots) + q % 4;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int g = 0; g < P.group; ++g) {
+        const float4 v = x[g * 4];
+        const float z = lse2[g];
+        sum[0] += exp2_approx(v.x - z);
+        sum[1] += exp2_approx(v.y - z);
+        sum[2] += exp2_approx(v.z - z);
+        sum[3] += exp2_approx(v.w - z);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < in) w[e] = fmaf(P.decay, old[e], sum[e]);
     }
     t += cnt;
+    if (t >= end) return;
+    __syncthreads();
+    i0 = 0;
+    if (++h == P.kv_heads) {
+      h = 0;
+      before += n;
+      do {  // there are tiles left, so a sequence has them
+        if (++b >= P.batch) return;
+        len = len_of(P, b);
+      } while (len == 0);
+      n = tiles_of(len);
+    }
   }
 }
 
@@ -604,7 +641,7 @@ cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attend_paged_kernel<NT>, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * kSms);
+  cfg.gridDim = dim3(kJoinCtas * kSms);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_paged_kernel, p);

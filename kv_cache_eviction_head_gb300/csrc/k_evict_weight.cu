@@ -5,13 +5,15 @@
 //   K[i] = K_old[kept[i]], V and weights likewise.
 //
 // Two launches. The first finds the keep set: a radix select over the weights' order-
-// preserving bits (four passes of eight bits, one histogram each) gives the smallest kept
-// weight, a pass over the slots in order writes the kept list. The second moves the rows.
+// preserving bits (three passes of eleven bits, one histogram each: the first tells the
+// exponents and two bits more apart, so that few threads meet in a bin) gives the smallest
+// kept weight, a pass over the slots in order writes the kept list. The keys of the first
+// 8192 slots stay in shared memory. The second launch moves the rows.
 // In slot order kept[i] >= i ascends, so a block that walks up the list and loads a chunk
 // of rows before it writes them never overwrites a row that is still to be read. Order-
 // free, dropped slots below the budget take kept ones from behind it, which are disjoint.
 //
-// Bound: HBM; moved rows are read and written once, weights read by each pass (from L2).
+// Bound: HBM; moved rows are read and written once, weights read once.
 #include "paged/paged.cuh"
 
 namespace bkv {
@@ -20,9 +22,12 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kSelectThreads = 256;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;                                    // eleven bits of a key
+constexpr int kMostCached = 8192;                              // slots whose keys stay in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 32;                                  // rows of K and of V per step
 constexpr int kMoveLoads = kMoveRows * 32 / kMoveThreads;      // 16-byte pieces per thread and step
+constexpr int kMoveWarps = kMoveThreads / 32;
 
 struct Unit {
   int layer, b, h;
@@ -55,8 +60,10 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 }
 
 __global__ void __launch_bounds__(kSelectThreads) select_weight_kernel(const __grid_constant__ EvictWeightParams P) {
-  extern __shared__ uint32_t mask_words[];  // order-free: kept slots below the budget as bits, then the kept in front of every word
-  __shared__ int hist[256];
+  // the first P.cached slots' keys; order-free: kept slots below the budget as bits, and the
+  // kept in front of every word
+  extern __shared__ uint32_t dynamic[];
+  __shared__ int hist[kBins];
   __shared__ int chosen, left;
   __shared__ int2 warp_sum[kSelectWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -75,7 +82,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_weight_kernel(const __g
   }
   const float* W = P.W[u.layer];
   const int from = P.prefix, to = u.len - P.recent;  // candidates
-  auto key = [&](int slot) {
+  auto read_key = [&](int slot) {
     const int64_t row = pool_row(P.pg, P.kv_heads, u.b, u.h, slot);
     if (row < 0) {
       latch(P.status, BKV_ERR_INVALID_ARG);
@@ -83,42 +90,53 @@ __global__ void __launch_bounds__(kSelectThreads) select_weight_kernel(const __g
     }
     return BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status) ? key_of(W[row]) : 0u;
   };
+  uint32_t* cache = dynamic;
+#pragma unroll 8
+  for (int s = tid; s < min(to, P.cached); s += kSelectThreads) cache[s] = s >= from ? read_key(s) : 0u;
+  // a thread only reads keys that it wrote itself
+  auto key = [&](int slot) { return slot < P.cached ? cache[slot] : read_key(slot); };
   int need = P.budget - P.prefix - P.recent;  // of the candidates, fewer than there are
   uint32_t least = 0, known = 0;              // the smallest kept key, as far as its bits are known
   if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+#pragma unroll
+      for (int i = 0; i < kBins / kSelectThreads; ++i) hist[i * kSelectThreads + tid] = 0;
       __syncthreads();
-      for (int s = from + tid; s < to; s += kSelectThreads) {
+      for (int s = tid; s < to; s += kSelectThreads) {
+        if (s < from) continue;
         const uint32_t k = key(s);
-        if ((k & known) == least) atomicAdd(&hist[k >> shift & 255], 1);
+        if ((k & known) == least) atomicAdd(&hist[k >> shift & digit], 1);
       }
       __syncthreads();
-      if (warp == 0) {
-        // the bin, from the top, in which the need-th largest lies: eight bins a lane
-        int mine[8], sum = 0;
+      // the bin, from the top, in which the need-th largest lies: eight bins a thread
+      int mine[kBins / kSelectThreads], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mine[i] = hist[255 - (lane * 8 + i)];
-          sum += mine[i];
-        }
-        int upto = sum;
+      for (int i = 0; i < kBins / kSelectThreads; ++i) {
+        mine[i] = hist[kBins - 1 - (tid * (kBins / kSelectThreads) + i)];
+        sum += mine[i];
+      }
+      int upto = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(kAll, upto, off);
-          if (lane >= off) upto += y;
-        }
-        const unsigned hit = __ballot_sync(kAll, upto >= need);
-        if (lane == __ffs(hit) - 1) {
-          int above = upto - sum, i = 0;
-          while (i < 7 && above + mine[i] < need) above += mine[i++];
-          chosen = 255 - (lane * 8 + i);
-          left = need - above;
-        }
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kAll, upto, off);
+        if (lane >= off) upto += y;
+      }
+      if (lane == 31) warp_sum[warp].x = upto;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kSelectWarps; ++k)
+        if (k < warp) upto += warp_sum[k].x;
+      if (upto - sum < need && upto >= need) {
+        int above = upto - sum, i = 0;
+        while (i < kBins / kSelectThreads - 1 && above + mine[i] < need) above += mine[i++];
+        chosen = kBins - 1 - (tid * (kBins / kSelectThreads) + i);
+        left = need - above;
       }
       __syncthreads();
       least |= (uint32_t)chosen << shift;
-      known |= 255u << shift;
+      known |= digit << shift;
       need = left;  // how many of those equal so far are kept
     }
   }
@@ -126,8 +144,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_weight_kernel(const __g
   const bool any = P.budget - P.prefix - P.recent > 0;
   int above = 0, equal = 0;  // kept beyond the ties, and ties, in front of the slots looked at
   const int words = (P.budget + 31) / 32;
-  uint32_t* bits = mask_words;
-  int* in_front = reinterpret_cast<int*>(mask_words + words);
+  uint32_t* bits = dynamic + P.cached;
+  int* in_front = reinterpret_cast<int*>(bits + words);
   int below = 0;  // order-free: kept slots below the budget
   for (int s0 = 0; s0 < u.len; s0 += kSelectThreads) {
     const int s = s0 + tid;
@@ -192,58 +210,80 @@ __global__ void __launch_bounds__(kSelectThreads) select_weight_kernel(const __g
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_weight_kernel(const __grid_constant__ EvictWeightParams P) {
-  __shared__ int64_t src[kMoveRows], dst[kMoveRows];
-  const int tid = threadIdx.x;
+  __shared__ int64_t src[2 * kMoveThreads], dst[2 * kMoveThreads];  // rows that move
+  __shared__ int moved_in[kMoveWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   depend_wait();
   depend_go();
   const Unit u = unit_of(P);
   if (!u.evicts) return;
   const int32_t* kept = P.kept + (int64_t)blockIdx.x * P.budget;
-  uint4* pool[2] = {P.K[u.layer], P.V[u.layer]};
+  uint4* pool = tid & 16 ? P.V[u.layer] : P.K[u.layer];
   float* W = P.W[u.layer];
-  const int part = tid & 15, kv = tid >> 4 & 1, r = tid >> 5;
-  for (int i0 = 0; i0 < P.budget; i0 += kMoveRows) {
-    float w = 0.f;
-    bool moves = false;
-    if (tid < kMoveRows) {
-      const int i = i0 + tid;
-      const int from = i < P.budget ? kept[i] : i;
-      int64_t a = -1, b = -1;
-      if (from != i && from >= 0 && from < u.len) {
-        a = pool_row(P.pg, P.kv_heads, u.b, u.h, from);
-        b = pool_row(P.pg, P.kv_heads, u.b, u.h, i);
-        if (a < 0 || b < 0) {
-          latch(P.status, BKV_ERR_INVALID_ARG);
-        } else if (BKV_IN_RANGE(max(a, b) < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) {
-          moves = true;
-          w = W[a];
-        }
-      }
-      src[tid] = moves ? a : -1;
-      dst[tid] = b;
+  const int part = tid & 15;
+  int count = 0;  // rows in the list
+  for (int i0 = 0; i0 < P.budget; i0 += kMoveThreads) {
+    const int i = i0 + tid;
+    const int from = i < P.budget ? kept[i] : i;
+    int64_t a = -1, b = -1;
+    if (from != i && from >= 0 && from < u.len) {
+      a = pool_row(P.pg, P.kv_heads, u.b, u.h, from);
+      b = pool_row(P.pg, P.kv_heads, u.b, u.h, i);
+      if (a < 0 || b < 0) latch(P.status, BKV_ERR_INVALID_ARG);
+      if (b < 0 || !BKV_IN_RANGE(max(a, b) < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) a = -1;
     }
-    if (!__syncthreads_or(moves)) continue;
-    uint4 x[kMoveLoads];
+    const unsigned moving = __ballot_sync(kAll, a >= 0);
+    if (lane == 0) moved_in[warp] = __popc(moving);
+    __syncthreads();
+    int at = count + __popc(moving & ((1u << lane) - 1));
 #pragma unroll
-    for (int k = 0; k < kMoveLoads; ++k) {
-      const int64_t a = src[k * (kMoveThreads / 32) + r];
-      if (a >= 0) x[k] = pool[kv][a * 16 + part];
+    for (int k = 0; k < kMoveWarps; ++k) {
+      const int n = moved_in[k];
+      if (k < warp) at += n;
+      count += n;
+    }
+    if (a >= 0) {
+      src[at] = a;
+      dst[at] = b;
     }
     __syncthreads();
+    if (count <= kMoveThreads && i0 + kMoveThreads < P.budget) continue;
+    // The next step's rows are loaded before this step's are written: their sources lie
+    // behind all that this step writes.
+    uint4 x[kMoveLoads], y[kMoveLoads];
+    float wx = 0.f, wy = 0.f;
+    auto load = [&](int c, uint4 (&v)[kMoveLoads], float& w) {
 #pragma unroll
-    for (int k = 0; k < kMoveLoads; ++k) {
-      const int at = k * (kMoveThreads / 32) + r;
-      if (src[at] >= 0) pool[kv][dst[at] * 16 + part] = x[k];
+      for (int k = 0; k < kMoveLoads; ++k) {
+        const int r = c + k * kMoveWarps + warp;
+        if (r < count) v[k] = pool[src[r] * 16 + part];
+      }
+      if (tid < kMoveRows && c + tid < count) w = W[src[c + tid]];
+    };
+    load(0, x, wx);
+    for (int c = 0; c < count; c += kMoveRows) {
+      load(c + kMoveRows, y, wy);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kMoveLoads; ++k) {
+        const int r = c + k * kMoveWarps + warp;
+        if (r < count) pool[dst[r] * 16 + part] = x[k];
+        x[k] = y[k];
+      }
+      if (tid < kMoveRows && c + tid < count) W[dst[c + tid]] = wx;
+      wx = wy;
     }
-    if (moves) W[dst[tid]] = w;
+    count = 0;
     __syncthreads();
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict_weight(const EvictWeightParams& p, cudaStream_t s) {
-  const size_t mask = p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0;
+cudaError_t launch_evict_weight(const EvictWeightParams& given, cudaStream_t s) {
+  EvictWeightParams p = given;
+  p.cached = p.pg.cap < kMostCached ? p.pg.cap : kMostCached;
+  const size_t mask = (size_t)p.cached * 4 + (p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0);
   cudaError_t e = cudaFuncSetAttribute(select_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = dependent_launch();

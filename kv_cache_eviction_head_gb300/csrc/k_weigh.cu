@@ -93,10 +93,23 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// A value that tcgen05.ld delivers is there only after the wait: ties the registers to it.
-__device__ __forceinline__ void tie(float (&v)[32]) {
+// 32 TMEM lanes x 48 consecutive columns.
+constexpr int kHalf = kCols / 2;
+__device__ __forceinline__ void load_half(uint32_t taddr, float (&v)[kHalf]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < kHalf; i += 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]),
+          "=r"(r[i + 7]), "=r"(r[i + 8]), "=r"(r[i + 9]), "=r"(r[i + 10]), "=r"(r[i + 11]), "=r"(r[i + 12]),
+          "=r"(r[i + 13]), "=r"(r[i + 14]), "=r"(r[i + 15])
+        : "r"(taddr + i));
+}
+// A value that tcgen05.ld delivers is there only after the wait: ties the registers to it.
+__device__ __forceinline__ void tie(float (&v)[kHalf]) {
+#pragma unroll
+  for (int i = 0; i < kHalf; i += 8)
     asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -116,6 +129,35 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Adds up the exponentials of half a tile's columns; `whole`: all of them count.
+__device__ __forceinline__ void add_half(const float (&v)[kHalf], const float* col, bool whole, int from, int to, uint64_t scale,
+                                         uint64_t (&part)[2]) {
+  const float4* cols = reinterpret_cast<const float4*>(col);
+  if (whole) {
+#pragma unroll
+    for (int q = 0; q < kHalf / 4; ++q) {
+      const float4 c = cols[q];
+      float a0, a1, a2, a3;
+      unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a0, a1);
+      unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a2, a3);
+      part[0] = add_pair(part[0], pair(fast_exp2(a0), fast_exp2(a1)));
+      part[1] = add_pair(part[1], pair(fast_exp2(a2), fast_exp2(a3)));
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kHalf / 4; ++q) {
+      const float4 c = cols[q];
+      float a[4];
+      unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a[0], a[1]);
+      unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a[2], a[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = 4 * q + e >= from && 4 * q + e < to ? fast_exp2(a[e]) : 0.f;
+      part[0] = add_pair(part[0], pair(a[0], a[1]));
+      part[1] = add_pair(part[1], pair(a[2], a[3]));
+    }
+  }
 }
 
 // What a CTA works on: one tile of slots of one (sequence, KV head).
@@ -311,65 +353,63 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
       if (lane == 0) mbar_arrive(&C.keys);
       ++nth;
 
-      // columns: this thread sees query rows from G * (slot - first - token of the tile's first row) on
       const uint64_t scale = pair(P.scale_log2, P.scale_log2);
-      uint64_t sum[2] = {0ull, 0ull};
-      auto column = [&](int k, int part) {
-        const int i = w.i0 + k * P.tpt + ct[part];
-        if (lane + 32 * part >= filled || i >= w.n) return -__builtin_huge_valf();
-        const float x = P.row_lse[((int64_t)w.begin + i) * P.heads + w.h * P.group + cg[part]];
-        return x == -__builtin_huge_valf() ? x : -x * kLog2e;  // a row that sees nothing gives nothing
+      uint64_t sum[2] = {0ull, 0ull};  // of whole tiles of columns: tens of thousands of terms, so a tile's are added up first
+      const float* lse[3];  // of this lane's columns of the next tile
+      int token[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        token[p] = lane + 32 * p < filled ? w.i0 + ct[p] : w.n;
+        lse[p] = P.row_lse + ((int64_t)w.begin + w.i0 + ct[p]) * P.heads + w.h * P.group + cg[p];
+      }
+      float next[3];
+      auto columns = [&] {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          next[p] = token[p] < w.n ? *lse[p] : -__builtin_huge_valf();
+          if (lane + 32 * p < filled) token[p] += P.tpt;
+          lse[p] += (int64_t)P.tpt * P.heads;
+        }
       };
-      float next[3] = {column(0, 0), column(0, 1), column(0, 2)};
-      for (int k = 0; k < w.tiles; ++k, ++it) {
+      columns();
+      float v[2][kHalf];  // the two halves of a tile's columns, one being loaded while the other is added up
+      go = wait(&C.sfull[it & 1], it / 2 & 1, ctl, P.status);
+      tc_fence_after();
+      if (go) load_half(tmem + lanes + (it & 1) * kCols, v[0]);
+      tmem_wait_ld();
+      tie(v[0]);
+      for (int k = 0; go && k < w.tiles; ++k, ++it) {
         const int x = it & 1;
         float* col = C.col[warp][x];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) col[lane + 32 * p] = next[p];
+        for (int p = 0; p < 3; ++p)
+          col[lane + 32 * p] = next[p] == -__builtin_huge_valf() ? next[p] : -next[p] * kLog2e;  // a row that sees nothing gives nothing
         __syncwarp();  // also: the tile before's columns are read
-        if (k + 1 < w.tiles) {
-#pragma unroll
-          for (int p = 0; p < 3; ++p) next[p] = column(k + 1, p);
-        }
-        go = wait(&C.sfull[x], it / 2 & 1, ctl, P.status);
-        if (!go) break;
-        tc_fence_after();
+        if (k + 1 < w.tiles) columns();
+        // this thread sees the columns from G * (slot - first - token of the tile's first row) on
         const int i = w.i0 + k * P.tpt;
         const int from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
         const int to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
         // whole tiles of columns that all slots of the tile see
         const bool whole = finite && w.j0 + 127 <= w.first + i && w.n - i >= P.tpt;
-#pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          float v[32];
-          tmem_ld32(tmem + lanes + x * kCols + c0, v);
-          tmem_wait_ld();
-          tie(v);
-          if (c0 + 32 == kCols) {  // read: the buffer may be filled again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&C.sempty[x]);
-          }
-          const float4* cols = reinterpret_cast<const float4*>(col + c0);
-          if (whole) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 c = cols[q];
-              float a0, a1, a2, a3;
-              unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a0, a1);
-              unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a2, a3);
-              sum[0] = add_pair(sum[0], pair(fast_exp2(a0), fast_exp2(a1)));
-              sum[1] = add_pair(sum[1], pair(fast_exp2(a2), fast_exp2(a3)));
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const float a = fmaf(v[q], P.scale_log2, col[c0 + q]);
-              const float p = c0 + q >= from && c0 + q < to ? fast_exp2(a) : 0.f;
-              sum[q >> 1 & 1] = add_pair(sum[q >> 1 & 1], q & 1 ? pair(0.f, p) : pair(p, 0.f));
-            }
-          }
+        uint64_t part[2] = {0ull, 0ull};
+        load_half(tmem + lanes + x * kCols + kHalf, v[1]);
+        add_half(v[0], col, whole, from, to, scale, part);
+        tmem_wait_ld();
+        tie(v[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.sempty[x]);  // read: the buffer may be filled again
+        if (k + 1 < w.tiles) {
+          go = wait(&C.sfull[x ^ 1], (it + 1) / 2 & 1, ctl, P.status);
+          tc_fence_after();
+          if (go) load_half(tmem + lanes + (x ^ 1) * kCols, v[0]);
         }
+        add_half(v[1], col + kHalf, whole, from - kHalf, to - kHalf, scale, part);
+        sum[0] = add_pair(sum[0], part[0]);
+        sum[1] = add_pair(sum[1], part[1]);
+        tmem_wait_ld();
+        tie(v[0]);
       }
       if (go && in) {
         float a0, a1, a2, a3;

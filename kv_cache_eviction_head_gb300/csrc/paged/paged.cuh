@@ -125,6 +125,7 @@ struct EvictWeightParams {
   uint32_t* status;
   int layers, batch, kv_heads, budget, prefix, recent;
   int order_free;
+  int cached;              // slots whose keys the selection keeps on chip (set by the launch)
 };
 cudaError_t launch_evict_weight(const EvictWeightParams& p, cudaStream_t s);
 

@@ -191,6 +191,10 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
   p.group = c.heads / c.kv_heads;
   p.chunk = p.group > 8 ? 16 : 8;
   p.chunks = (p.group + p.chunk - 1) / p.chunk;
+  // the kernels count tiles of 16 slots, and output rows, in 32 bits
+  if ((int64_t)c.batch * ((p.pg.cap + bkv::kTileSlots - 1) / bkv::kTileSlots) * c.kv_heads * p.chunks > 0x7FFF0000 ||
+      (int64_t)c.batch * c.heads > 0x7FFFFFFF / 32)
+    return BKV_ERR_UNSUPPORTED;
   p.tiles_cap = weights ? most_tiles(c, p.pg) * c.kv_heads : 0;
   char* base = static_cast<char*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
