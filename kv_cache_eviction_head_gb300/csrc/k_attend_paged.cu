@@ -15,14 +15,12 @@
 // launch joins in the order of the shares. The split goes by the lengths alone: the same
 // call gives the same bits.
 //
-// A warp's ring of tiles is private down to the thread: every thread copies (cp.async)
-// the 16-byte pieces that its own matrix fragments are made of and reads back only
-// those, so the ring needs no barrier and its shared-memory accesses no swizzle. This
-// works since the fragments' inner dimensions may be permuted freely: S = Q K^T
-// (m16n8k16, rows: query heads, columns: slots) takes as its k-steps the four 16-byte
-// pieces q + 4j of a key row that thread q of a quad holds, on both sides alike;
-// O^T = V^T P^T (rows: d, columns: heads) takes two neighbouring slots' pieces, whose
-// elements are paired by byte permutes; and P as it leaves S is that product's B operand.
+// A warp's ring of tiles is its own: one lane asks TMA for the four boxes of a tile
+// (64 elements x 16 slots of K and of V, twice; SWIZZLE_128B, so that the fragments' loads
+// meet no bank twice), the warp waits for their barrier. S = Q K^T (m16n8k16, rows: query
+// heads, columns: slots); P as it leaves S is the B operand of O^T = V^T P^T (rows: d,
+// columns: heads). Copied by the threads themselves (cp.async, 16 bytes each, in fragment
+// order) the same tiles came at 4.7 TB/s whatever the number of warps and stages.
 //
 // Rounding: logits, maxima, sums, weights and O are fp32; P is rounded to bf16 for the
 // product with bf16 V (at most 2^-8 relative per term, as the output), the sums and
@@ -31,15 +29,16 @@
 //
 // Weights need the final sum: the first launch leaves its logits (fp32, 4 G bytes a
 // slot) in the workspace, and the second turns them into probabilities.
-#include "paged/paged.cuh"
+#include "paged/device.cuh"
 
 namespace bkv {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kStages = 3;                  // tiles under way per warp
-constexpr int kTileBytes16 = 2 * kTileSlots * kD * 2;  // K and V of a tile: 8 KB
-constexpr int kAttendSmem = kAttendWarps * kStages * kTileBytes16;
+constexpr int kBox = kTileSlots * 128;       // 16 slots x 64 elements
+constexpr int kTileBox = 4 * kBox;           // K and V of a tile: 8 KB
+constexpr int kAttendSmem = kAttendWarps * kStages * kTileBox + 1024;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 5;                // per SM
 constexpr int kJoinTiles = 16;              // tiles of a block's weights, at least
@@ -56,22 +55,15 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Four 8 x 8 tiles of 16-bit elements, plain or transposed; lane i gives the address of
+// row i % 8 of tile i / 8.
+__device__ __forceinline__ void load_tiles(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-// Copies 16 bytes, or writes 16 zero bytes.
-__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void load_tiles_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -152,13 +144,23 @@ __device__ __forceinline__ void step(const AttendPagedParams& P, Place& p, int u
 
 template <int NT>
 __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(const __grid_constant__ AttendPagedParams P) {
-  extern __shared__ __align__(128) unsigned char ring_bytes[];
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t full[kAttendWarps][kStages];
   __shared__ int rows_in[kAttendWarps][kStages];  // visible slots of a tile
+  __shared__ Ctl ctl_of[kAttendWarps];            // a warp's waits end for itself alone
   constexpr int kChunk = 8 * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quad = lane & 3, row = lane >> 2;
   const int w = blockIdx.x * kAttendWarps + warp;
   const int units = P.kv_heads * P.chunks;
+  uint64_t* bar = full[warp];
+  Ctl* ctl = &ctl_of[warp];
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
   depend_wait();
   depend_go();
 
@@ -182,45 +184,30 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   look_up(P, c);
   Place a = c;  // the next tile to copy; its page is looked up one tile ahead
 
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_bytes) + warp * kStages * kTileBytes16 + lane * 16;
+  const uint32_t ring = ((smem_u32(raw) + 1023u) & ~1023u) + warp * kStages * kTileBox;
+  const uint64_t policy = policy_evict_normal();
   auto fetch = [&](int stage) {
     const int slot0 = a.i * kTileSlots;
-    const int h = a.u / P.chunks;
     int rows = min(kTileSlots, a.len - slot0);
-    int64_t base = 0;
-    if (a.page >= 0) {
-      base = ((int64_t)a.page * P.kv_heads + h) * P.pg.page_size + (slot0 - page_of(P.pg, slot0) * P.pg.page_size);
-    } else {
+    const int z = a.page * P.kv_heads + a.u / P.chunks;
+    if (a.page < 0) {
       rows = 0;
       if (lane == 0) latch(P.status, BKV_ERR_INVALID_ARG);
+    } else if (!BKV_IN_RANGE(z < P.pg.pages * P.kv_heads, P.status)) {
+      rows = 0;
     }
-    if (!BKV_IN_RANGE(base >= 0 && base + rows <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) rows = 0, base = 0;
-    if (lane == 0) rows_in[warp][stage] = rows;
-    const uint32_t dst = ring + stage * kTileBytes16;
-    const uint4* k = P.K + base * 16 + (row * 16 + quad);
-    const uint4* v = P.V + base * 16 + (quad * 32 + row);
-    if (rows == kTileSlots) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) copy16(dst + (t * 4 + j) * 512, k + t * 128 + 4 * j);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) copy16(dst + (8 + s * 2 + j) * 512, v + (s & 1) * 16 + (s >> 1) * 128 + 8 * j);
-    } else {  // zeros for the slots behind the last: what lies there may be NaN
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const bool in = row + 8 * t < rows;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) copy16_if(dst + (t * 4 + j) * 512, in ? k + t * 128 + 4 * j : P.K, in);
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bool in = 2 * quad + (s & 1) + 8 * (s >> 1) < rows;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          copy16_if(dst + (8 + s * 2 + j) * 512, in ? v + (s & 1) * 16 + (s >> 1) * 128 + 8 * j : P.V, in);
+    if (lane == 0) {
+      rows_in[warp][stage] = rows;
+      if (rows > 0) {
+        const int y = slot0 - page_of(P.pg, slot0) * P.pg.page_size;
+        const uint32_t dst = ring + stage * kTileBox;
+        mbar_expect_tx(&bar[stage], kTileBox);
+        tma_rows(dst, &P.kmap, 0, y, z, &bar[stage], policy);
+        tma_rows(dst + kBox, &P.kmap, 64, y, z, &bar[stage], policy);
+        tma_rows(dst + 2 * kBox, &P.vmap, 0, y, z, &bar[stage], policy);
+        tma_rows(dst + 3 * kBox, &P.vmap, 64, y, z, &bar[stage], policy);
+      } else {
+        mbar_arrive(&bar[stage]);
       }
     }
   };
@@ -233,8 +220,12 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
       step(P, a, units);
       if (ahead < count) look_up(P, a);
     }
-    copies_commit();
   }
+
+  // a lane's row of the fragments' tiles: (slots 0-7, 16-byte pieces 0 and 1), (slots 8-15,
+  // pieces 0 and 1)
+  const int tile_row = lane & 7, piece0 = lane >> 3 & 1;
+  const uint32_t slot_row = (uint32_t)((lane >> 4) * 8 + tile_row) * 128;
 
   uint32_t qlo[8][2], qhi[NT == 2 ? 8 : 1][2];
   float o[NT][8][4];
@@ -242,12 +233,14 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   int first = 0;  // tile of the unit that this piece begins with
   bool fresh = true;
   int stage = 0;
-  for (int it = 0; it < count; ++it) {
+  uint32_t phase = 0;
+  int it = 0;
+  for (; it < count; ++it) {
     const int h = c.u / P.chunks, head0 = (c.u - h * P.chunks) * kChunk;  // first query head of the chunk, in its group
     if (fresh) {
       fresh = false;
       first = c.i;
-      const uint4* q = P.q + (int64_t)c.b * P.q_stride + ((int64_t)h * P.group + head0) * 16 + quad;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(P.q + (int64_t)c.b * P.q_stride + ((int64_t)h * P.group + head0) * 16) + quad;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         m[t] = kMinusInf;
@@ -258,27 +251,18 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
           for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
         const bool in = head0 + row + 8 * t < P.group;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (in) x = q[(row + 8 * t) * 16 + 4 * j];
-          if (t == 0) {
-            qlo[2 * j][0] = x.x;
-            qlo[2 * j][1] = x.y;
-            qlo[2 * j + 1][0] = x.z;
-            qlo[2 * j + 1][1] = x.w;
-          } else if constexpr (NT == 2) {
-            qhi[2 * j][0] = x.x;
-            qhi[2 * j][1] = x.y;
-            qhi[2 * j + 1][0] = x.z;
-            qhi[2 * j + 1][1] = x.w;
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = in ? q[(row + 8 * t) * 64 + k * 8 + e * 4] : 0u;
+            if (t == 0) qlo[k][e] = x;
+            else if constexpr (NT == 2) qhi[k][e] = x;
           }
-        }
       }
     }
-    copies_wait<kStages - 2>();
-    __syncwarp();
+    if (!__all_sync(kAll, mbar_wait(&bar[stage], phase, ctl, P.status))) break;
     const int rows = rows_in[warp][stage];
-    const uint32_t at = ring + stage * kTileBytes16;
+    const uint32_t at = ring + stage * kTileBox;
     // the stage that the tile before has left
     if (ahead < count) {
       fetch(stage == 0 ? kStages - 1 : stage - 1);
@@ -286,31 +270,35 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
       step(P, a, units);
       if (ahead < count) look_up(P, a);
     }
-    copies_commit();
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (rows < kTileSlots) {  // what lies behind the last slot may be NaN: a weight of 0 does not undo it
+      for (int i = lane; i < (kTileSlots - rows) * 16; i += 32)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + (2 + (i >> 3 & 1)) * kBox + (rows + (i >> 4)) * 128 + (i & 7) * 16), "r"(0) : "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+      __syncwarp();
+    }
 
-    // all of the tile's pieces are asked for at once; two sums per eight slots halve the
-    // chain of products
-    uint4 kf[8], vf[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) kf[i] = lds16(at + i * 512);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) vf[i] = lds16(at + (8 + i) * 512);
-    float s[2][4], s1[2][4];
+    float s[2][4], s1[2][4];  // two sums per eight slots halve the chain of products
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = s1[t][e] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint4 k = kf[t * 4 + j];
-        mma16816(s[t], qlo[2 * j][0], NT == 2 ? qhi[NT == 2 ? 2 * j : 0][0] : 0u, qlo[2 * j][1],
-                 NT == 2 ? qhi[NT == 2 ? 2 * j : 0][1] : 0u, k.x, k.y);
-        mma16816(s1[t], qlo[2 * j + 1][0], NT == 2 ? qhi[NT == 2 ? 2 * j + 1 : 0][0] : 0u, qlo[2 * j + 1][1],
-                 NT == 2 ? qhi[NT == 2 ? 2 * j + 1 : 0][1] : 0u, k.z, k.w);
+    for (int k = 0; k < 8; ++k) {
+      uint32_t f[4];
+      load_tiles(f, at + (k >> 2) * kBox + slot_row + (uint32_t)((((k & 3) * 2 + piece0) ^ tile_row) << 4));
+      const uint32_t h0 = NT == 2 ? qhi[NT == 2 ? k : 0][0] : 0u, h1 = NT == 2 ? qhi[NT == 2 ? k : 0][1] : 0u;
+      if (k & 1) {
+        mma16816(s1[0], qlo[k][0], h0, qlo[k][1], h1, f[0], f[1]);
+        mma16816(s1[1], qlo[k][0], h0, qlo[k][1], h1, f[2], f[3]);
+      } else {
+        mma16816(s[0], qlo[k][0], h0, qlo[k][1], h1, f[0], f[1]);
+        mma16816(s[1], qlo[k][0], h0, qlo[k][1], h1, f[2], f[3]);
       }
+    }
     // this thread's logits of head `row` (and row + 8): slots 2 quad, 2 quad + 1, and 8 on
     float x[NT][4];
 #pragma unroll
@@ -373,17 +361,11 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
       pb[t][1] = pack2_bf16(p[2], p[3]);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 v0 = vf[j], v1 = vf[2 + j], v2 = vf[4 + j], v3 = vf[6 + j];
-      const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-      const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+    for (int k = 0; k < 8; ++k) {
+      uint32_t f[4];  // (d 0-7, slots 0-7), (d 8-15, slots 0-7), (d 0-7, slots 8-15), (d 8-15, slots 8-15)
+      load_tiles_t(f, at + (2 + (k >> 2)) * kBox + slot_row + (uint32_t)((((k & 3) * 2 + piece0) ^ tile_row) << 4));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a0 = __byte_perm(w0[e], w1[e], 0x5410), a1 = __byte_perm(w0[e], w1[e], 0x7632);
-        const uint32_t a2 = __byte_perm(w2[e], w3[e], 0x5410), a3 = __byte_perm(w2[e], w3[e], 0x7632);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(o[t][j * 4 + e], a0, a1, a2, a3, pb[t][0], pb[t][1]);
-      }
+      for (int t = 0; t < NT; ++t) mma16816(o[t][k], f[0], f[1], f[2], f[3], pb[t][0], pb[t][1]);
     }
 
     if (c.i + 1 == c.n || it + 1 == count) {  // the unit ends here, or this share of it
@@ -408,38 +390,40 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
         }
         const float d0 = 1.f / __shfl_sync(kAll, l[t], 8 * quad), d1 = 1.f / __shfl_sync(kAll, l[t], 8 * quad + 4);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {  // head 2 quad + e of this eight
+        for (int e = 0; e < 2; ++e) {  // head 2 quad + e of this eight: elements 16 k + row and 16 k + 8 + row
           if (head0 + 8 * t + 2 * quad + e >= P.group) continue;
           const float d = e ? d1 : d0;
+          if (whole) {
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + (out_row + 2 * quad + e) * kD + row;
+            float check = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[2 * k] = o[t][j * 4 + k][e];
-              y[2 * k + 1] = o[t][j * 4 + k][2 + e];
+            for (int k = 0; k < 8; ++k) {
+              const float y0 = o[t][k][e] * d, y1 = o[t][k][2 + e] * d;
+              check += y0 * 0.f + y1 * 0.f;
+              to[16 * k] = __float2bfloat16_rn(y0);
+              to[16 * k + 8] = __float2bfloat16_rn(y1);
             }
-            if (whole) {
-              float check = 0.f;
+            if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
+          } else {
+            // a piece's elements in the order of the fragments
+            float4* to = P.part_o + (piece * kChunk + 8 * t + 2 * quad + e) * 32 + row * 4;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                y[k] *= d;
-                check += y[k] * 0.f;
-              }
-              if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
-              P.out[(out_row + 2 * quad + e) * 16 + row + 8 * j] =
-                  make_uint4(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
-            } else {
-              float4* to = P.part_o + (piece * kChunk + 8 * t + 2 * quad + e) * 32 + (row + 8 * j) * 2;
-              to[0] = make_float4(y[0], y[1], y[2], y[3]);
-              to[1] = make_float4(y[4], y[5], y[6], y[7]);
-            }
+            for (int k = 0; k < 4; ++k)
+              to[k] = make_float4(o[t][2 * k][e], o[t][2 * k][2 + e], o[t][2 * k + 1][e], o[t][2 * k + 1][2 + e]);
           }
         }
       }
       fresh = true;
     }
     step(P, c, units);
+  }
+  // a wait ran out: copies under way land before the shared memory goes
+  for (; it < ahead; ++it) {
+    wait_done(&bar[stage], phase);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
   }
 }
 
@@ -546,7 +530,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
       if (warp != 0) continue;
     }
     if (ml.y == 0.f) y.x = y.y = y.z = y.w = __builtin_nanf("");  // every logit is -inf
-    reinterpret_cast<uint2*>(P.out)[(int64_t)r * 32 + lane] = make_uint2(pack2_bf16(y.x, y.y), pack2_bf16(y.z, y.w));
+    // elements (lane / 4) + 8 i, i = 4 (lane % 4) .. + 3: the order of the fragments
+    __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + (int64_t)r * kD + (lane >> 2) + (lane & 3) * 32;
+    to[0] = __float2bfloat16_rn(y.x);
+    to[8] = __float2bfloat16_rn(y.y);
+    to[16] = __float2bfloat16_rn(y.z);
+    to[24] = __float2bfloat16_rn(y.w);
     const float check = (y.x * 0.f + y.y * 0.f) + (y.z * 0.f + y.w * 0.f);
     if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
     if (lane == 0) {
@@ -648,6 +637,13 @@ cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool encode_attend_paged_maps(AttendPagedParams& p) {
+  const cuuint64_t row = (cuuint64_t)kD * 2, plane = (cuuint64_t)p.pg.page_size * row;
+  const cuuint64_t planes = (cuuint64_t)p.pg.pages * p.kv_heads;
+  return encode_rows(&p.kmap, p.K, (cuuint64_t)p.pg.page_size, row, planes, plane, kTileSlots, 1) &&
+         encode_rows(&p.vmap, p.V, (cuuint64_t)p.pg.page_size, row, planes, plane, kTileSlots, 1);
+}
 
 cudaError_t launch_attend_paged(const AttendPagedParams& p, cudaStream_t s) {
   return p.chunk == 8 ? launch<1>(p, s) : launch<2>(p, s);

@@ -20,8 +20,7 @@
 // Rounding: products and sums are fp32, nothing is rounded to fewer bits.
 #include <cstddef>
 
-#include "paged/paged.cuh"
-#include "score_common.cuh"
+#include "paged/device.cuh"
 
 namespace bkv {
 namespace {
@@ -54,12 +53,6 @@ __device__ __forceinline__ uint32_t lane_elected() {
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, Ctl* ctl, uint32_t* status) {
   return __all_sync(kFull, mbar_wait(b, parity, ctl, status));
 }
-// Waits for work handed to the hardware, whatever has become of the call.
-__device__ __forceinline__ void wait_done(uint64_t* b, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_test(b, parity))
-    if (clock64() - t0 > kWaitCycles) return;
-}
 // A (128 slots x 16 bf16) from TMEM, B (96 query rows) from shared memory.
 template <uint32_t kAStep, uint32_t kBStep>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t elected) {
@@ -76,13 +69,6 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t elected) {
       "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
       "r"(elected)
-      : "memory");
-}
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -432,23 +418,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
 }  // namespace
 
 bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride) {
-  // the driver's encoder, looked up once per process (thread-safe static initialisation)
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    cudaDriverEntryPointQueryResult qres;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qres) != cudaSuccess ||
-        qres != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  if (!encode) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.heads, (cuuint64_t)p.total};
-  const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)q_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.tpt};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode(&p.qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_rows(&p.qmap, q, (cuuint64_t)p.heads, (cuuint64_t)kD * 2, (cuuint64_t)p.total, (cuuint64_t)q_stride * 2,
+                     (cuuint32_t)p.group, (cuuint32_t)p.tpt);
 }
 
 cudaError_t launch_weigh(const WeighParams& p, int grid, cudaStream_t s) {

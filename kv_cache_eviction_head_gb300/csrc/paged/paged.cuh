@@ -71,6 +71,7 @@ constexpr int kAttendCtas = 2 * kSms;                         // two per SM
 constexpr int kAttendShares = kAttendCtas * kAttendWarps;     // warps of a launch, at most
 constexpr int kTileSlots = 16;
 struct AttendPagedParams {
+  CUtensorMap kmap, vmap;  // pools [pages * kv_heads][page_size][d], box (64, 16, 1)
   Pages pg;
   const uint4* q;          // sequence b, head h at q + b * q_stride + h * 16 (uint4 units)
   int64_t q_stride;
@@ -94,6 +95,8 @@ struct AttendPagedParams {
   float* logits;           // [tile][group][16], log2 units; with weights only
 };
 cudaError_t launch_attend_paged(const AttendPagedParams& p, cudaStream_t s);
+// Fills p's tensor maps (host only). False on failure.
+bool encode_attend_paged_maps(AttendPagedParams& p);
 
 constexpr int kWeighRows = 96;  // query rows per tile: query heads per KV head, at most
 struct WeighParams {

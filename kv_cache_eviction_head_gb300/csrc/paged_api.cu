@@ -191,8 +191,9 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
   p.group = c.heads / c.kv_heads;
   p.chunk = p.group > 8 ? 16 : 8;
   p.chunks = (p.group + p.chunk - 1) / p.chunk;
-  // the kernels count tiles of 16 slots, and output rows, in 32 bits
-  if ((int64_t)c.batch * ((p.pg.cap + bkv::kTileSlots - 1) / bkv::kTileSlots) * c.kv_heads * p.chunks > 0x7FFF0000 ||
+  // the kernels count tiles of 16 slots, output rows and (page, KV head) planes in 32 bits
+  if ((int64_t)p.pg.pages * c.kv_heads > 0x7FFFFFFF ||
+      (int64_t)c.batch * ((p.pg.cap + bkv::kTileSlots - 1) / bkv::kTileSlots) * c.kv_heads * p.chunks > 0x7FFF0000 ||
       (int64_t)c.batch * c.heads > 0x7FFFFFFF / 32)
     return BKV_ERR_UNSUPPORTED;
   p.tiles_cap = weights ? most_tiles(c, p.pg) * c.kv_heads : 0;
@@ -202,6 +203,7 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
   p.lse2 = reinterpret_cast<float*>(base + w.lse2);
   p.logits = weights ? reinterpret_cast<float*>(base + w.logits) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (!bkv::encode_attend_paged_maps(p)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
   return bkv::launch_attend_paged(p, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
