@@ -14,7 +14,9 @@
 // A tile of columns is tpt = 96 / G tokens with the G query heads of the KV head. Two
 // buffers of 96 columns and the keys' 64 take 256 columns of TMEM, so that two CTAs
 // share an SM and one's set-up, ends and hand-overs lie under the other's products.
-// CTA: 4 warps that exponentiate and add, a TMA producer, an MMA issuer. Blocks of the
+// CTA: 8 warps that exponentiate and add (two for each 32 slots, half the columns each: with
+// one, whose chain of load, exponential and sum nothing covered, the long prompts took 588
+// us), a TMA producer, an MMA issuer. Blocks of the
 // grid take the slots' tiles in order, those that most queries see first.
 //
 // Rounding: products and sums are fp32, nothing is rounded to fewer bits.
@@ -25,12 +27,13 @@
 namespace bkv {
 namespace {
 
-constexpr int kCols = kWeighRows;
+constexpr int kCols = kWeighRows, kHalf = kCols / 2;
 constexpr int kQSlab = kCols * 128;              // 96 rows x 64 bf16
 constexpr int kQTile = 2 * kQSlab;               // 24 KB
 constexpr int kQStages = 4;
-constexpr int kWeighThreads = 192;
-constexpr int kProducer = 4, kIssuer = 5;        // warps; 0 - 3 add up
+constexpr int kAdders = 8;                       // warps 0 - 7: warp w adds up columns 48 (w / 4) .. of slots 32 (w % 4) ..
+constexpr int kProducer = kAdders, kIssuer = kAdders + 1;
+constexpr int kWeighThreads = 32 * (kAdders + 2);
 constexpr uint32_t kTmemCols = 256, kTmemKeys = 192;  // two buffers of 96 columns, the keys behind them
 constexpr int kWeighSmem = kQStages * kQTile + 1024;
 
@@ -38,11 +41,16 @@ struct WeighControl {
   uint64_t full[kQStages], empty[kQStages];
   uint64_t keys, keys_free;       // the keys are in TMEM; its products are done
   uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM; they have been read
+  uint64_t halves;                // the second half of the columns is added up
   Ctl ctl;
-  // -lse log2(e) of a tile's columns, a copy per adding warp: no barrier among them
-  alignas(16) float col[4][2][kCols];
+  // -lse log2(e) of a half tile's columns, a copy per adding warp: no barrier among them
+  alignas(16) float col[kAdders][2][kHalf];
+  float other[128];               // the second half's sums
+  // per item (in turn) and warp: a key holds an infinity or NaN, which would make NaN of the
+  // products with rows that no token fills
+  int odd[2][kAdders];
 };
-static_assert(offsetof(WeighControl, col) % 16 == 0 && (kCols * sizeof(float)) % 16 == 0, "read as float4");
+static_assert(offsetof(WeighControl, col) % 16 == 0 && (kHalf * sizeof(float)) % 16 == 0, "read as float4");
 
 __device__ __forceinline__ uint32_t lane_elected() {
   uint32_t e;
@@ -80,7 +88,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // 32 TMEM lanes x 48 consecutive columns.
-constexpr int kHalf = kCols / 2;
 __device__ __forceinline__ void load_half(uint32_t taddr, float (&v)[kHalf]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
@@ -117,32 +124,33 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Adds up the exponentials of half a tile's columns; `whole`: all of them count.
-__device__ __forceinline__ void add_half(const float (&v)[kHalf], const float* col, bool whole, int from, int to, uint64_t scale,
-                                         uint64_t (&part)[2]) {
+// Adds up the exponentials of half a tile's columns.
+__device__ __forceinline__ void add_half(const float (&v)[kHalf], const float* col, uint64_t scale, uint64_t (&part)[2]) {
   const float4* cols = reinterpret_cast<const float4*>(col);
-  if (whole) {
 #pragma unroll
-    for (int q = 0; q < kHalf / 4; ++q) {
-      const float4 c = cols[q];
-      float a0, a1, a2, a3;
-      unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a0, a1);
-      unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a2, a3);
-      part[0] = add_pair(part[0], pair(fast_exp2(a0), fast_exp2(a1)));
-      part[1] = add_pair(part[1], pair(fast_exp2(a2), fast_exp2(a3)));
-    }
-  } else {
+  for (int q = 0; q < kHalf / 4; ++q) {
+    const float4 c = cols[q];
+    float a0, a1, a2, a3;
+    unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a0, a1);
+    unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a2, a3);
+    part[0] = add_pair(part[0], pair(fast_exp2(a0), fast_exp2(a1)));
+    part[1] = add_pair(part[1], pair(fast_exp2(a2), fast_exp2(a3)));
+  }
+}
+// The same of columns from .. to - 1 only.
+__device__ __forceinline__ void add_half_of(const float (&v)[kHalf], const float* col, int from, int to, uint64_t scale,
+                                            uint64_t (&part)[2]) {
+  const float4* cols = reinterpret_cast<const float4*>(col);
 #pragma unroll
-    for (int q = 0; q < kHalf / 4; ++q) {
-      const float4 c = cols[q];
-      float a[4];
-      unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a[0], a[1]);
-      unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a[2], a[3]);
+  for (int q = 0; q < kHalf / 4; ++q) {
+    const float4 c = cols[q];
+    float a[4];
+    unpair(fma_pair(pair(v[4 * q], v[4 * q + 1]), scale, pair(c.x, c.y)), a[0], a[1]);
+    unpair(fma_pair(pair(v[4 * q + 2], v[4 * q + 3]), scale, pair(c.z, c.w)), a[2], a[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] = 4 * q + e >= from && 4 * q + e < to ? fast_exp2(a[e]) : 0.f;
-      part[0] = add_pair(part[0], pair(a[0], a[1]));
-      part[1] = add_pair(part[1], pair(a[2], a[3]));
-    }
+    for (int e = 0; e < 4; ++e) a[e] = 4 * q + e >= from && 4 * q + e < to ? fast_exp2(a[e]) : 0.f;
+    part[0] = add_pair(part[0], pair(a[0], a[1]));
+    part[1] = add_pair(part[1], pair(a[2], a[3]));
   }
 }
 
@@ -200,10 +208,11 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.sfull[i], 1);
-      mbar_init(&C.sempty[i], 4);
+      mbar_init(&C.sempty[i], kAdders);
     }
-    mbar_init(&C.keys, 4);
+    mbar_init(&C.keys, kAdders);
     mbar_init(&C.keys_free, 1);
+    mbar_init(&C.halves, 4);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -296,33 +305,36 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     // products under way are done before TMEM goes
     if (nth > 0) wait_done(&C.keys_free, (nth - 1) & 1);
   } else {
-    uint32_t it = 0, nth = 0;
+    uint32_t nth = 0, turn = 0, phase = 0;  // items so far; buffer of the tile to come and its parity
     bool go = true;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    int ct[3], cg[3];  // this lane's columns of a tile: token and head
+    const int half = warp >> 2, mine = tid & 127;  // columns, slot of the tile
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const int c0 = half * kHalf;
+    const uint32_t t_half = tmem + lanes + c0;
+    int ct[2], cg[2];  // this lane's columns of a tile: token and head
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      ct[p] = (lane + 32 * p) / P.group;
-      cg[p] = lane + 32 * p - ct[p] * P.group;
+    for (int p = 0; p < 2; ++p) {
+      ct[p] = (c0 + lane + 32 * p) / P.group;
+      cg[p] = c0 + lane + 32 * p - ct[p] * P.group;
     }
     for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
       const WeighItem w = item_of(P, item);
       if (w.tiles == 0) continue;
-      // this thread's key, into its lane of TMEM
-      const int slot = w.j0 + tid;
+      // this thread's key, one half of it, into its lane of TMEM
+      const int slot = w.j0 + mine;
       const int64_t row = slot < w.slots ? pool_row(P.pg, P.kv_heads, w.b, w.h, slot) : -1;
       if (slot < w.slots && row < 0) latch(P.status, BKV_ERR_INVALID_ARG);
       const bool in = row >= 0 && BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status);
       if (nth > 0) go = wait(&C.keys_free, (nth - 1) & 1, ctl, P.status);
       if (!go) break;
       tc_fence_after();
-      uint32_t odd = 0;  // the key holds an infinity or NaN: rows that no token fills would make NaN of it
+      uint32_t odd = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < 2; ++x) {
         uint32_t r[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 v = in ? P.K[row * 16 + x * 4 + k] : make_uint4(0, 0, 0, 0);
+          const uint4 v = in ? P.K[row * 16 + half * 8 + x * 4 + k] : make_uint4(0, 0, 0, 0);
           r[4 * k] = v.x;
           r[4 * k + 1] = v.y;
           r[4 * k + 2] = v.z;
@@ -330,9 +342,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) odd |= ((r[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-        tmem_store16(tmem + lanes + kTmemKeys + x * 16, r);
+        tmem_store16(tmem + lanes + kTmemKeys + half * 32 + x * 16, r);
       }
-      const bool finite = !__any_sync(kFull, odd != 0);
+      odd = __any_sync(kFull, odd != 0);
+      if (lane == 0) C.odd[nth & 1][warp] = (int)odd;  // the other half's warp reads it after a product with these keys
       tmem_stored();
       tc_fence_before();
       __syncwarp();
@@ -341,71 +354,83 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
 
       const uint64_t scale = pair(P.scale_log2, P.scale_log2);
       uint64_t sum[2] = {0ull, 0ull};  // of whole tiles of columns: tens of thousands of terms, so a tile's are added up first
-      const float* lse[3];  // of this lane's columns of the next tile
-      int token[3];
+      // this lane's columns of the tile to come: their log-sum-exps, and the first tokens they
+      // would belong to
+      const float* lse[2];
+      int token[2];
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        token[p] = lane + 32 * p < filled ? w.i0 + ct[p] : w.n;
+      for (int p = 0; p < 2; ++p) {
+        token[p] = c0 + lane + 32 * p < filled && lane + 32 * p < kHalf ? w.i0 + ct[p] : 0x7FFFFFFF;
         lse[p] = P.row_lse + ((int64_t)w.begin + w.i0 + ct[p]) * P.heads + w.h * P.group + cg[p];
       }
-      float next[3];
-      auto columns = [&] {
+      const int64_t lse_step = (int64_t)P.tpt * P.heads;
+      float next[2];
+      auto columns = [&](int k) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          next[p] = token[p] < w.n ? *lse[p] : -__builtin_huge_valf();
-          if (lane + 32 * p < filled) token[p] += P.tpt;
-          lse[p] += (int64_t)P.tpt * P.heads;
+        for (int p = 0; p < 2; ++p) {
+          next[p] = token[p] < w.n - k * P.tpt ? *lse[p] : -__builtin_huge_valf();
+          lse[p] += lse_step;
         }
       };
-      columns();
-      float v[2][kHalf];  // the two halves of a tile's columns, one being loaded while the other is added up
-      go = wait(&C.sfull[it & 1], it / 2 & 1, ctl, P.status);
-      tc_fence_after();
-      if (go) load_half(tmem + lanes + (it & 1) * kCols, v[0]);
-      tmem_wait_ld();
-      tie(v[0]);
-      for (int k = 0; go && k < w.tiles; ++k, ++it) {
-        const int x = it & 1;
-        float* col = C.col[warp][x];
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-          col[lane + 32 * p] = next[p] == -__builtin_huge_valf() ? next[p] : -next[p] * kLog2e;  // a row that sees nothing gives nothing
-        __syncwarp();  // also: the tile before's columns are read
-        if (k + 1 < w.tiles) columns();
-        // this thread sees the columns from G * (slot - first - token of the tile's first row) on
-        const int i = w.i0 + k * P.tpt;
-        const int from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
-        const int to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
-        // whole tiles of columns that all slots of the tile see
-        const bool whole = finite && w.j0 + 127 <= w.first + i && w.n - i >= P.tpt;
-        uint64_t part[2] = {0ull, 0ull};
-        load_half(tmem + lanes + x * kCols + kHalf, v[1]);
-        add_half(v[0], col, whole, from, to, scale, part);
+      columns(0);
+      // tiles of columns in front of `seen` hold rows that do not see all slots, those from `full`
+      // on rows of other sequences
+      const int full = (w.n - w.i0) / P.tpt;
+      int seen = (int)min(max((int64_t)w.j0 + 127 - w.first - w.i0 + P.tpt - 1, (int64_t)0) / P.tpt, (int64_t)full);
+#pragma unroll 1
+      for (int k = 0; k < w.tiles; ++k) {
+        float* col = C.col[warp][turn];
+        // a row that sees nothing gives nothing
+        col[lane] = next[0] == -__builtin_huge_valf() ? next[0] : -next[0] * kLog2e;
+        if (lane < kHalf - 32) col[lane + 32] = next[1] == -__builtin_huge_valf() ? next[1] : -next[1] * kLog2e;
+        __syncwarp();  // also: the columns of the tile before are read
+        if (k + 1 < w.tiles) columns(k + 1);
+        go = wait(&C.sfull[turn], phase, ctl, P.status);
+        if (!go) break;
+        tc_fence_after();
+        // the other half's keys have been looked at: a product with them is done
+        if (k == 0 && (odd | C.odd[(nth - 1) & 1][warp ^ 4])) seen = full;
+        float v[kHalf];
+        load_half(t_half + turn * kCols, v);
         tmem_wait_ld();
-        tie(v[1]);
+        tie(v);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&C.sempty[x]);  // read: the buffer may be filled again
-        if (k + 1 < w.tiles) {
-          go = wait(&C.sfull[x ^ 1], (it + 1) / 2 & 1, ctl, P.status);
-          tc_fence_after();
-          if (go) load_half(tmem + lanes + (x ^ 1) * kCols, v[0]);
+        if (lane == 0) mbar_arrive(&C.sempty[turn]);  // read: the buffer may be filled again
+        uint64_t part[2] = {0ull, 0ull};
+        if (k >= seen && k < full) {
+          add_half(v, col, scale, part);
+        } else {
+          // this thread sees the columns from G * (slot - first - token of the tile's first row) on
+          const int i = w.i0 + k * P.tpt;
+          const int from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
+          const int to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
+          add_half_of(v, col, from - c0, to - c0, scale, part);
         }
-        add_half(v[1], col + kHalf, whole, from - kHalf, to - kHalf, scale, part);
         sum[0] = add_pair(sum[0], part[0]);
         sum[1] = add_pair(sum[1], part[1]);
-        tmem_wait_ld();
-        tie(v[0]);
+        phase ^= turn;
+        turn ^= 1;
       }
-      if (go && in) {
-        float a0, a1, a2, a3;
-        unpair(sum[0], a0, a1);
-        unpair(sum[1], a2, a3);
-        const float s = (a0 + a1) + (a2 + a3);
-        float old = 0.f;
-        if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
-        P.weights[row] = old + s;
-        if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+      if (!go) break;
+      float a0, a1, a2, a3;
+      unpair(sum[0], a0, a1);
+      unpair(sum[1], a2, a3);
+      float s = (a0 + a1) + (a2 + a3);
+      if (half == 1) {
+        C.other[mine] = s;  // read before the next item's keys are, which this item's products wait for
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.halves);
+      } else {
+        go = wait(&C.halves, (nth - 1) & 1, ctl, P.status);
+        if (!go) break;
+        s += C.other[mine];
+        if (in) {
+          float old = 0.f;
+          if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
+          P.weights[row] = old + s;
+          if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+        }
       }
     }
   }
