@@ -14,10 +14,9 @@
 // A tile of columns is tpt = 96 / G tokens with the G query heads of the KV head. Two
 // buffers of 96 columns and the keys' 64 take 256 columns of TMEM, so that two CTAs
 // share an SM and one's set-up, ends and hand-overs lie under the other's products.
-// CTA: 8 warps that exponentiate and add (two for each 32 slots, half the columns each: with
-// one, whose chain of load, exponential and sum nothing covered, the long prompts took 588
-// us), a TMA producer, an MMA issuer. Blocks of the
-// grid take the slots' tiles in order, those that most queries see first.
+// CTA: 8 warps that exponentiate and add, four for each buffer (so for every other tile), a
+// TMA producer, an MMA issuer. Blocks of the grid take the slots' tiles in order, those that
+// most queries see first.
 //
 // Rounding: products and sums are fp32, nothing is rounded to fewer bits.
 #include <cstddef>
@@ -31,7 +30,7 @@ constexpr int kCols = kWeighRows, kHalf = kCols / 2;
 constexpr int kQSlab = kCols * 128;              // 96 rows x 64 bf16
 constexpr int kQTile = 2 * kQSlab;               // 24 KB
 constexpr int kQStages = 4;
-constexpr int kAdders = 8;                       // warps 0 - 7: warp w adds up columns 48 (w / 4) .. of slots 32 (w % 4) ..
+constexpr int kAdders = 8;                       // warps 0 - 7: warp w adds up every other tile (w / 4) for slots 32 (w % 4) ..
 constexpr int kProducer = kAdders, kIssuer = kAdders + 1;
 constexpr int kWeighThreads = 32 * (kAdders + 2);
 constexpr uint32_t kTmemCols = 256, kTmemKeys = 192;  // two buffers of 96 columns, the keys behind them
@@ -41,16 +40,16 @@ struct WeighControl {
   uint64_t full[kQStages], empty[kQStages];
   uint64_t keys, keys_free;       // the keys are in TMEM; its products are done
   uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM; they have been read
-  uint64_t halves;                // the second half of the columns is added up
+  uint64_t others;                // the odd tiles are added up
   Ctl ctl;
-  // -lse log2(e) of a half tile's columns, a copy per adding warp: no barrier among them
-  alignas(16) float col[kAdders][2][kHalf];
-  float other[128];               // the second half's sums
+  // -lse log2(e) of a tile's columns, a copy per adding warp: no barrier among them
+  alignas(16) float col[kAdders][kCols];
+  float other[128];               // the odd tiles' sums
   // per item (in turn) and warp: a key holds an infinity or NaN, which would make NaN of the
   // products with rows that no token fills
   int odd[2][kAdders];
 };
-static_assert(offsetof(WeighControl, col) % 16 == 0 && (kHalf * sizeof(float)) % 16 == 0, "read as float4");
+static_assert(offsetof(WeighControl, col) % 16 == 0 && (kCols * sizeof(float)) % 16 == 0, "read as float4");
 
 __device__ __forceinline__ uint32_t lane_elected() {
   uint32_t e;
@@ -208,11 +207,11 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.sfull[i], 1);
-      mbar_init(&C.sempty[i], kAdders);
+      mbar_init(&C.sempty[i], kAdders / 2);
     }
     mbar_init(&C.keys, kAdders);
     mbar_init(&C.keys_free, 1);
-    mbar_init(&C.halves, 4);
+    mbar_init(&C.others, kAdders / 2);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -305,17 +304,18 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     // products under way are done before TMEM goes
     if (nth > 0) wait_done(&C.keys_free, (nth - 1) & 1);
   } else {
-    uint32_t nth = 0, turn = 0, phase = 0;  // items so far; buffer of the tile to come and its parity
+    uint32_t nth = 0, done = 0, phase = 0;  // items and tiles so far, parity of this group's buffer
     bool go = true;
-    const int half = warp >> 2, mine = tid & 127;  // columns, slot of the tile
+    const int group = warp >> 2, mine = tid & 127;  // buffer, slot of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const int c0 = half * kHalf;
-    const uint32_t t_half = tmem + lanes + c0;
-    int ct[2], cg[2];  // this lane's columns of a tile: token and head
+    const uint32_t t_mine = tmem + lanes + group * kCols;
+    float* col = C.col[warp];
+    int ct[3], at[3];  // this lane's columns of a tile: token (none: never in the sequence), place in the log-sum-exps
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      ct[p] = (c0 + lane + 32 * p) / P.group;
-      cg[p] = c0 + lane + 32 * p - ct[p] * P.group;
+    for (int p = 0; p < 3; ++p) {
+      const int c = lane + 32 * p, t = c / P.group;
+      ct[p] = c < filled ? t : 0x7FFFFFFF;
+      at[p] = c < filled ? t * P.heads + c - t * P.group : 0;
     }
     for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
       const WeighItem w = item_of(P, item);
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         uint32_t r[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 v = in ? P.K[row * 16 + half * 8 + x * 4 + k] : make_uint4(0, 0, 0, 0);
+          const uint4 v = in ? P.K[row * 16 + group * 8 + x * 4 + k] : make_uint4(0, 0, 0, 0);
           r[4 * k] = v.x;
           r[4 * k + 1] = v.y;
           r[4 * k + 2] = v.z;
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) odd |= ((r[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-        tmem_store16(tmem + lanes + kTmemKeys + half * 32 + x * 16, r);
+        tmem_store16(tmem + lanes + kTmemKeys + group * 32 + x * 16, r);
       }
       odd = __any_sync(kFull, odd != 0);
-      if (lane == 0) C.odd[nth & 1][warp] = (int)odd;  // the other half's warp reads it after a product with these keys
+      if (lane == 0) C.odd[nth & 1][warp] = (int)odd;  // the other group's warp reads it after a product with these keys
       tmem_stored();
       tc_fence_before();
       __syncwarp();
@@ -354,75 +354,76 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
 
       const uint64_t scale = pair(P.scale_log2, P.scale_log2);
       uint64_t sum[2] = {0ull, 0ull};  // of whole tiles of columns: tens of thousands of terms, so a tile's are added up first
-      // this lane's columns of the tile to come: their log-sum-exps, and the first tokens they
-      // would belong to
-      const float* lse[2];
-      int token[2];
+      const int begin = (done & 1) ^ group;  // this group's first tile of the item
+      done += w.tiles;
+      const float* lse = P.row_lse + ((int64_t)w.begin + w.i0 + begin * P.tpt) * P.heads + w.h * P.group;
+      int left = w.n - w.i0 - begin * P.tpt;  // tokens from the first of the tile to come on
+      float next[3];
+      auto columns = [&] {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        token[p] = c0 + lane + 32 * p < filled && lane + 32 * p < kHalf ? w.i0 + ct[p] : 0x7FFFFFFF;
-        lse[p] = P.row_lse + ((int64_t)w.begin + w.i0 + ct[p]) * P.heads + w.h * P.group + cg[p];
-      }
-      const int64_t lse_step = (int64_t)P.tpt * P.heads;
-      float next[2];
-      auto columns = [&](int k) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          next[p] = token[p] < w.n - k * P.tpt ? *lse[p] : -__builtin_huge_valf();
-          lse[p] += lse_step;
+        for (int p = 0; p < 3; ++p) {
+          next[p] = -__builtin_huge_valf();
+          if (ct[p] < left) next[p] = lse[at[p]];
         }
+        lse += 2 * (int64_t)P.tpt * P.heads;
+        left -= 2 * P.tpt;
       };
-      columns(0);
+      columns();
       // tiles of columns in front of `seen` hold rows that do not see all slots, those from `full`
       // on rows of other sequences
       const int full = (w.n - w.i0) / P.tpt;
       int seen = (int)min(max((int64_t)w.j0 + 127 - w.first - w.i0 + P.tpt - 1, (int64_t)0) / P.tpt, (int64_t)full);
 #pragma unroll 1
-      for (int k = 0; k < w.tiles; ++k) {
-        float* col = C.col[warp][turn];
+      for (int k = begin; k < w.tiles; k += 2) {
         // a row that sees nothing gives nothing
-        col[lane] = next[0] == -__builtin_huge_valf() ? next[0] : -next[0] * kLog2e;
-        if (lane < kHalf - 32) col[lane + 32] = next[1] == -__builtin_huge_valf() ? next[1] : -next[1] * kLog2e;
-        __syncwarp();  // also: the columns of the tile before are read
-        if (k + 1 < w.tiles) columns(k + 1);
-        go = wait(&C.sfull[turn], phase, ctl, P.status);
-        if (!go) break;
-        tc_fence_after();
-        // the other half's keys have been looked at: a product with them is done
-        if (k == 0 && (odd | C.odd[(nth - 1) & 1][warp ^ 4])) seen = full;
-        float v[kHalf];
-        load_half(t_half + turn * kCols, v);
-        tmem_wait_ld();
-        tie(v);
-        tc_fence_before();
+#pragma unroll
+        for (int p = 0; p < 3; ++p) col[lane + 32 * p] = next[p] == -__builtin_huge_valf() ? next[p] : -next[p] * kLog2e;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&C.sempty[turn]);  // read: the buffer may be filled again
-        uint64_t part[2] = {0ull, 0ull};
-        if (k >= seen && k < full) {
-          add_half(v, col, scale, part);
-        } else {
-          // this thread sees the columns from G * (slot - first - token of the tile's first row) on
+        columns();
+        go = wait(&C.sfull[group], phase, ctl, P.status);
+        if (!go) break;
+        phase ^= 1;
+        tc_fence_after();
+        // the other group's keys have been looked at: a product with them is done
+        if (k == begin && (odd | C.odd[(nth - 1) & 1][warp ^ 4])) seen = full;
+        const bool whole = k >= seen && k < full;
+        // this thread sees the columns from G * (slot - first - token of the tile's first row) on
+        int from = 0, to = 0;
+        if (!whole) {
           const int i = w.i0 + k * P.tpt;
-          const int from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
-          const int to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
-          add_half_of(v, col, from - c0, to - c0, scale, part);
+          from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
+          to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
+        }
+        uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += kHalf) {
+          float v[kHalf];
+          load_half(t_mine + c0, v);
+          tmem_wait_ld();
+          tie(v);
+          if (c0 > 0) {  // read: the buffer may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&C.sempty[group]);
+          }
+          if (whole) add_half(v, col + c0, scale, part);
+          else add_half_of(v, col + c0, from - c0, to - c0, scale, part);
         }
         sum[0] = add_pair(sum[0], part[0]);
         sum[1] = add_pair(sum[1], part[1]);
-        phase ^= turn;
-        turn ^= 1;
+        __syncwarp();  // the columns are read
       }
       if (!go) break;
       float a0, a1, a2, a3;
       unpair(sum[0], a0, a1);
       unpair(sum[1], a2, a3);
       float s = (a0 + a1) + (a2 + a3);
-      if (half == 1) {
-        C.other[mine] = s;  // read before the next item's keys are, which this item's products wait for
+      if (group == 1) {
+        C.other[mine] = s;  // read before the next item's keys are, which that item's products wait for
         __syncwarp();
-        if (lane == 0) mbar_arrive(&C.halves);
+        if (lane == 0) mbar_arrive(&C.others);
       } else {
-        go = wait(&C.halves, (nth - 1) & 1, ctl, P.status);
+        go = wait(&C.others, (nth - 1) & 1, ctl, P.status);
         if (!go) break;
         s += C.other[mine];
         if (in) {
