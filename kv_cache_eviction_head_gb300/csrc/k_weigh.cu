@@ -15,8 +15,10 @@
 // buffers of 96 columns and the keys' 64 take 256 columns of TMEM, so that two CTAs
 // share an SM and one's set-up, ends and hand-overs lie under the other's products.
 // CTA: 8 warps that exponentiate and add, four for each buffer (so for every other tile), a
-// TMA producer, an MMA issuer. Blocks of the grid take the slots' tiles in order, those that
-// most queries see first.
+// TMA producer that also looks up the columns' log-sum-exps, an MMA issuer. Blocks of the
+// grid take the slots' tiles in order, those that most queries see first. Where there are
+// few such tiles, the CTAs of a cluster share one's queries and join their sums, in rank
+// order, through distributed shared memory.
 //
 // Rounding: products and sums are fp32, nothing is rounded to fewer bits.
 #include <cstddef>
@@ -31,23 +33,28 @@ constexpr int kQSlab = kCols * 128;              // 96 rows x 64 bf16
 constexpr int kQTile = 2 * kQSlab;               // 24 KB
 constexpr int kQStages = 4;
 constexpr int kAdders = 8;                       // warps 0 - 7: warp w adds up every other tile (w / 4) for slots 32 (w % 4) ..
+constexpr int kMostSplits = 8;
 constexpr int kProducer = kAdders, kIssuer = kAdders + 1;
 constexpr int kWeighThreads = 32 * (kAdders + 2);
+constexpr int kColStages = 4;
 constexpr uint32_t kTmemCols = 256, kTmemKeys = 192;  // two buffers of 96 columns, the keys behind them
 constexpr int kWeighSmem = kQStages * kQTile + 1024;
 
 struct WeighControl {
   uint64_t full[kQStages], empty[kQStages];
   uint64_t keys, keys_free;       // the keys are in TMEM; its products are done
-  uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM; they have been read
+  uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM and its columns written; the logits have been read
   uint64_t others;                // the odd tiles are added up
   Ctl ctl;
-  // -lse log2(e) of a tile's columns, a copy per adding warp: no barrier among them
-  alignas(16) float col[kAdders][kCols];
+  // -lse log2(e) of a tile's columns. Tile i's place is written when buffer i % 2 is free for
+  // it, so after tile i - 2 has been read, and by the same warps tile i - 4 added up
+  alignas(16) float col[kColStages][kCols];
   float other[128];               // the odd tiles' sums
   // per item (in turn) and warp: a key holds an infinity or NaN, which would make NaN of the
   // products with rows that no token fills
   int odd[2][kAdders];
+  uint64_t ranks;                 // rank 0: the other ranks' sums are here
+  float rank_sum[kMostSplits - 1][128];
 };
 static_assert(offsetof(WeighControl, col) % 16 == 0 && (kCols * sizeof(float)) % 16 == 0, "read as float4");
 
@@ -153,6 +160,45 @@ __device__ __forceinline__ void add_half_of(const float (&v)[kHalf], const float
   }
 }
 
+// Clusters: the CTAs of one share an item's tiles of columns.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_rank0(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A bounded wait for what other CTAs of the cluster have written.
+__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, Ctl* ctl, uint32_t* status) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    if (__all_sync(kFull, ok)) return true;
+    if (__any_sync(kFull, ctl->abort || clock64() - t0 > kWaitCycles)) {
+      latch(status, BKV_ERR_TIMEOUT);
+      ctl->abort = 1;
+      return false;
+    }
+  }
+}
+
 // What a CTA works on: one tile of slots of one (sequence, KV head).
 struct WeighItem {
   int b, h;
@@ -162,6 +208,7 @@ struct WeighItem {
   int first;      // slots before the first token
   int slots;      // slots of the sequence: first + n, at most what its table holds
   int tiles;      // tiles of query rows; 0: nothing to do
+  int own;        // those of this CTA: rank, rank + splits, ...
 };
 // A sequence as the call may read it; `bad`: something had to be clamped.
 __device__ __forceinline__ void read_sequence(const WeighParams& P, int b, int& begin, int& n, int& first, int& slots, bool& bad) {
@@ -174,7 +221,7 @@ __device__ __forceinline__ void read_sequence(const WeighParams& P, int b, int& 
   slots = n == 0 ? 0 : (int)min(most, (int64_t)P.pg.cap);
   bad = begin != x || end != y || (n > 0 && (first != f || most > P.pg.cap));
 }
-__device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item) {
+__device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item, int rank) {
   WeighItem w;
   const int per = P.batch * P.kv_heads;
   const int64_t tile = item / per;
@@ -190,6 +237,7 @@ __device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item)
     w.i0 = max(0, w.j0 - w.first);
     w.tiles = (w.n - w.i0 + P.tpt - 1) / P.tpt;
   }
+  w.own = (w.tiles - rank + P.splits - 1) / P.splits;
   return w;
 }
 
@@ -200,17 +248,20 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   unsigned char* qring = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Ctl* ctl = &C.ctl;
+  const int rank = P.splits > 1 ? (int)cluster_rank() : 0;
+  const int64_t item0 = blockIdx.x / P.splits, item_step = gridDim.x / P.splits;
   if (tid == 0) {
     for (int i = 0; i < kQStages; ++i) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&C.sfull[i], 1);
+      mbar_init(&C.sfull[i], 2);
       mbar_init(&C.sempty[i], kAdders / 2);
     }
     mbar_init(&C.keys, kAdders);
     mbar_init(&C.keys_free, 1);
+    mbar_init(&C.ranks, max((P.splits - 1) * kAdders / 2, 1));
     mbar_init(&C.others, kAdders / 2);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -242,28 +293,66 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
+  if (P.splits > 1) cluster_sync();  // the ranks' barriers are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const int64_t total = items;
 
   if (warp == kProducer) {
+    // Copies run two tiles ahead of the columns, which need a free buffer of logits.
     const uint64_t keep = policy_evict_last();  // queries are read once per tile of slots
-    uint32_t it = 0;
-    bool go = true;
-    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
-      const WeighItem w = item_of(P, item);
-      for (int k = 0; k < w.tiles; ++k, ++it) {
-        const int s = it % kQStages;
-        go = wait(&C.empty[s], (it / kQStages & 1) ^ 1, ctl, P.status);
-        if (!go) break;
-        if (lane == 0) {
-          mbar_expect_tx(&C.full[s], (uint32_t)(2 * filled * 128));
-          const int t = w.begin + w.i0 + k * P.tpt;
+    int ct[3], at[3];  // this lane's columns of a tile: token (none: never in the sequence), place in the log-sum-exps
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            tma_rows(smem_u32(qring + s * kQTile + x * kQSlab), &P.qmap, x * 64, w.h * P.group, t, &C.full[s], keep);
+    for (int p = 0; p < 3; ++p) {
+      const int c = lane + 32 * p, t = c / P.group;
+      ct[p] = c < filled ? t : 0x7FFFFFFF;
+      at[p] = c < filled ? t * P.heads + c - t * P.group : 0;
+    }
+    uint32_t it = 0, ci = 0;  // tiles copied, columns written
+    bool go = true;
+    for (int64_t item = item0; go && item < total; item += item_step) {
+      const WeighItem w = item_of(P, item, rank);
+      if (w.own <= 0) continue;
+      const float* lse = P.row_lse + ((int64_t)w.begin + w.i0 + (int64_t)rank * P.tpt) * P.heads + w.h * P.group;
+      int left = w.n - w.i0 - rank * P.tpt;  // tokens from the first of the tile on
+      float next[3];
+      auto columns = [&] {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          next[p] = -__builtin_huge_valf();
+          if (ct[p] < left) next[p] = lse[at[p]];
         }
-        __syncwarp();
+        lse += (int64_t)P.splits * P.tpt * P.heads;
+        left -= P.splits * P.tpt;
+      };
+      columns();
+      for (int k = 0; go && k < w.own + 2; ++k) {
+        if (k < w.own) {
+          const int s = it % kQStages;
+          go = wait(&C.empty[s], (it / kQStages & 1) ^ 1, ctl, P.status);
+          if (!go) break;
+          if (lane == 0) {
+            mbar_expect_tx(&C.full[s], (uint32_t)(2 * filled * 128));
+            const int t = w.begin + w.i0 + (k * P.splits + rank) * P.tpt;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              tma_rows(smem_u32(qring + s * kQTile + x * kQSlab), &P.qmap, x * 64, w.h * P.group, t, &C.full[s], keep);
+          }
+          __syncwarp();
+          ++it;
+        }
+        if (k >= 2) {
+          go = wait(&C.sempty[ci & 1], (ci / 2 & 1) ^ 1, ctl, P.status);
+          if (!go) break;
+          float* col = C.col[ci % kColStages];
+          // a row that sees nothing gives nothing
+#pragma unroll
+          for (int p = 0; p < 3; ++p) col[lane + 32 * p] = next[p] == -__builtin_huge_valf() ? next[p] : -next[p] * kLog2e;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C.sfull[ci & 1]);
+          ++ci;
+          columns();
+        }
       }
     }
     // copies under way land before the CTA's shared memory goes
@@ -274,12 +363,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     const uint32_t idesc = idesc_bf16(128, kCols);
     uint32_t it = 0, nth = 0;
     bool go = true;
-    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
-      const WeighItem w = item_of(P, item);
-      if (w.tiles == 0) continue;
+    for (int64_t item = item0; go && item < total; item += item_step) {
+      const WeighItem w = item_of(P, item, rank);
+      if (w.own <= 0) continue;
       go = wait(&C.keys, nth & 1, ctl, P.status);
       tc_fence_after();
-      for (int k = 0; go && k < w.tiles; ++k, ++it) {
+      for (int k = 0; go && k < w.own; ++k, ++it) {
         const int s = it % kQStages, x = it & 1;
         go = wait(&C.full[s], it / kQStages & 1, ctl, P.status) && wait(&C.sempty[x], (it / 2 & 1) ^ 1, ctl, P.status);
         if (!go) break;
@@ -309,129 +398,121 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     const int group = warp >> 2, mine = tid & 127;  // buffer, slot of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_mine = tmem + lanes + group * kCols;
-    float* col = C.col[warp];
-    int ct[3], at[3];  // this lane's columns of a tile: token (none: never in the sequence), place in the log-sum-exps
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const int c = lane + 32 * p, t = c / P.group;
-      ct[p] = c < filled ? t : 0x7FFFFFFF;
-      at[p] = c < filled ? t * P.heads + c - t * P.group : 0;
-    }
-    for (int64_t item = blockIdx.x; go && item < total; item += gridDim.x) {
-      const WeighItem w = item_of(P, item);
+    for (int64_t item = item0; go && item < total; item += item_step) {
+      const WeighItem w = item_of(P, item, rank);
       if (w.tiles == 0) continue;
       // this thread's key, one half of it, into its lane of TMEM
       const int slot = w.j0 + mine;
       const int64_t row = slot < w.slots ? pool_row(P.pg, P.kv_heads, w.b, w.h, slot) : -1;
       if (slot < w.slots && row < 0) latch(P.status, BKV_ERR_INVALID_ARG);
       const bool in = row >= 0 && BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status);
-      if (nth > 0) go = wait(&C.keys_free, (nth - 1) & 1, ctl, P.status);
-      if (!go) break;
-      tc_fence_after();
-      uint32_t odd = 0;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t r[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 v = in ? P.K[row * 16 + group * 8 + x * 4 + k] : make_uint4(0, 0, 0, 0);
-          r[4 * k] = v.x;
-          r[4 * k + 1] = v.y;
-          r[4 * k + 2] = v.z;
-          r[4 * k + 3] = v.w;
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) odd |= ((r[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-        tmem_store16(tmem + lanes + kTmemKeys + group * 32 + x * 16, r);
-      }
-      odd = __any_sync(kFull, odd != 0);
-      if (lane == 0) C.odd[nth & 1][warp] = (int)odd;  // the other group's warp reads it after a product with these keys
-      tmem_stored();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C.keys);
-      ++nth;
-
-      const uint64_t scale = pair(P.scale_log2, P.scale_log2);
-      uint64_t sum[2] = {0ull, 0ull};  // of whole tiles of columns: tens of thousands of terms, so a tile's are added up first
-      const int begin = (done & 1) ^ group;  // this group's first tile of the item
-      done += w.tiles;
-      const float* lse = P.row_lse + ((int64_t)w.begin + w.i0 + begin * P.tpt) * P.heads + w.h * P.group;
-      int left = w.n - w.i0 - begin * P.tpt;  // tokens from the first of the tile to come on
-      float next[3];
-      auto columns = [&] {
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          next[p] = -__builtin_huge_valf();
-          if (ct[p] < left) next[p] = lse[at[p]];
-        }
-        lse += 2 * (int64_t)P.tpt * P.heads;
-        left -= 2 * P.tpt;
-      };
-      columns();
-      // tiles of columns in front of `seen` hold rows that do not see all slots, those from `full`
-      // on rows of other sequences
-      const int full = (w.n - w.i0) / P.tpt;
-      int seen = (int)min(max((int64_t)w.j0 + 127 - w.first - w.i0 + P.tpt - 1, (int64_t)0) / P.tpt, (int64_t)full);
-#pragma unroll 1
-      for (int k = begin; k < w.tiles; k += 2) {
-        // a row that sees nothing gives nothing
-#pragma unroll
-        for (int p = 0; p < 3; ++p) col[lane + 32 * p] = next[p] == -__builtin_huge_valf() ? next[p] : -next[p] * kLog2e;
-        __syncwarp();
-        columns();
-        go = wait(&C.sfull[group], phase, ctl, P.status);
+      float s = 0.f;
+      if (w.own > 0) {
+        if (nth > 0) go = wait(&C.keys_free, (nth - 1) & 1, ctl, P.status);
         if (!go) break;
-        phase ^= 1;
         tc_fence_after();
-        // the other group's keys have been looked at: a product with them is done
-        if (k == begin && (odd | C.odd[(nth - 1) & 1][warp ^ 4])) seen = full;
-        const bool whole = k >= seen && k < full;
-        // this thread sees the columns from G * (slot - first - token of the tile's first row) on
-        int from = 0, to = 0;
-        if (!whole) {
-          const int i = w.i0 + k * P.tpt;
-          from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
-          to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
-        }
-        uint64_t part[2] = {0ull, 0ull};
+        uint32_t odd = 0;
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += kHalf) {
-          float v[kHalf];
-          load_half(t_mine + c0, v);
-          tmem_wait_ld();
-          tie(v);
-          if (c0 > 0) {  // read: the buffer may be filled again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&C.sempty[group]);
+        for (int x = 0; x < 2; ++x) {
+          uint32_t r[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = in ? P.K[row * 16 + group * 8 + x * 4 + k] : make_uint4(0, 0, 0, 0);
+            r[4 * k] = v.x;
+            r[4 * k + 1] = v.y;
+            r[4 * k + 2] = v.z;
+            r[4 * k + 3] = v.w;
           }
-          if (whole) add_half(v, col + c0, scale, part);
-          else add_half_of(v, col + c0, from - c0, to - c0, scale, part);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) odd |= ((r[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+          tmem_store16(tmem + lanes + kTmemKeys + group * 32 + x * 16, r);
         }
-        sum[0] = add_pair(sum[0], part[0]);
-        sum[1] = add_pair(sum[1], part[1]);
-        __syncwarp();  // the columns are read
-      }
-      if (!go) break;
-      float a0, a1, a2, a3;
-      unpair(sum[0], a0, a1);
-      unpair(sum[1], a2, a3);
-      float s = (a0 + a1) + (a2 + a3);
-      if (group == 1) {
-        C.other[mine] = s;  // read before the next item's keys are, which that item's products wait for
+        odd = __any_sync(kFull, odd != 0);
+        if (lane == 0) C.odd[nth & 1][warp] = (int)odd;  // the other group's warp reads it after a product with these keys
+        tmem_stored();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&C.others);
-      } else {
-        go = wait(&C.others, (nth - 1) & 1, ctl, P.status);
-        if (!go) break;
-        s += C.other[mine];
-        if (in) {
-          float old = 0.f;
-          if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
-          P.weights[row] = old + s;
-          if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+        if (lane == 0) mbar_arrive(&C.keys);
+        ++nth;
+
+        const uint64_t scale = pair(P.scale_log2, P.scale_log2);
+        uint64_t sum[2] = {0ull, 0ull};  // of whole tiles of columns: tens of thousands of terms, so a tile's are added up first
+        // this group's tiles of the item: every other one of the CTA's
+        const int begin = ((done & 1) ^ group) * P.splits + rank, by = 2 * P.splits;
+        uint32_t tile = done + ((done & 1) ^ group);  // counted over the CTA's items
+        done += w.own;
+        // tiles of columns in front of `seen` hold rows that do not see all slots, those from `full`
+        // on rows of other sequences
+        const int full = (w.n - w.i0) / P.tpt;
+        int seen = (int)min(max((int64_t)w.j0 + 127 - w.first - w.i0 + P.tpt - 1, (int64_t)0) / P.tpt, (int64_t)full);
+#pragma unroll 1
+        for (int k = begin; k < w.tiles; k += by) {
+          go = wait(&C.sfull[group], phase, ctl, P.status);
+          if (!go) break;
+          phase ^= 1;
+          tc_fence_after();
+          // the other group's keys have been looked at: a product with them is done
+          if (k == begin && (odd | C.odd[(nth - 1) & 1][warp ^ 4])) seen = full;
+          const bool whole = k >= seen && k < full;
+          // this thread sees the columns from G * (slot - first - token of the tile's first row) on
+          int from = 0, to = 0;
+          if (!whole) {
+            const int i = w.i0 + k * P.tpt;
+            from = (int)min(max((int64_t)P.group * ((int64_t)slot - w.first - i), (int64_t)0), (int64_t)kCols);
+            to = (int)min((int64_t)filled, (int64_t)(w.n - i) * P.group);
+          }
+          const float* col = C.col[tile % kColStages];
+          tile += 2;
+          uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c0 = 0; c0 < kCols; c0 += kHalf) {
+            float v[kHalf];
+            load_half(t_mine + c0, v);
+            tmem_wait_ld();
+            tie(v);
+            if (c0 > 0) {  // read: the buffer may be filled again
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&C.sempty[group]);
+            }
+            if (whole) add_half(v, col + c0, scale, part);
+            else add_half_of(v, col + c0, from - c0, to - c0, scale, part);
+          }
+          sum[0] = add_pair(sum[0], part[0]);
+          sum[1] = add_pair(sum[1], part[1]);
         }
+        if (!go) break;
+        float a0, a1, a2, a3;
+        unpair(sum[0], a0, a1);
+        unpair(sum[1], a2, a3);
+        s = (a0 + a1) + (a2 + a3);
+        if (group == 1) {
+          C.other[mine] = s;  // read before the next item's keys are, which that item's products wait for
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C.others);
+        } else {
+          go = wait(&C.others, (nth - 1) & 1, ctl, P.status);
+          if (!go) break;
+          s += C.other[mine];
+        }
+      }
+      if (group == 1) continue;
+      if (rank > 0) {
+        store_cluster(in_rank0(&C.rank_sum[rank - 1][mine]), s);
+        __syncwarp();
+        if (lane == 0) arrive_cluster(in_rank0(&C.ranks));
+        continue;
+      }
+      if (P.splits > 1) {  // in the order of the ranks; such a cluster has one item
+        go = wait_cluster(&C.ranks, 0, ctl, P.status);
+        if (!go) break;
+        for (int r = 1; r < P.splits; ++r) s += C.rank_sum[r - 1][mine];
+      }
+      if (in) {
+        float old = 0.f;
+        if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
+        P.weights[row] = old + s;
+        if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
       }
     }
   }
@@ -439,6 +520,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
+  if (P.splits > 1) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
 }  // namespace
@@ -448,18 +530,32 @@ bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride) {
                      (cuuint32_t)p.group, (cuuint32_t)p.tpt);
 }
 
-cudaError_t launch_weigh(const WeighParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeighSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at = dependent_launch();
+  WeighParams q = p;
+  // Shares are halved while that keeps all CTAs in three or so rounds of 2 x 152 and leaves
+  // eight tiles of queries to each, for prompts of the average length
+  const int64_t tiles = p.total / p.batch / p.tpt;
+  q.splits = 1;
+  while (q.splits < kMostSplits && items * q.splits < 4 * kSms && 16 * q.splits <= tiles) q.splits *= 2;
+  cudaLaunchAttribute at[2];
+  at[0] = dependent_launch();
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  // blocks walk on from there; a cluster has one item
+  cfg.gridDim = dim3((unsigned)(items * q.splits < 8 * 2 * kSms || q.splits > 1 ? items * q.splits : 8 * 2 * kSms));
   cfg.blockDim = dim3(kWeighThreads);
   cfg.dynamicSmemBytes = kWeighSmem;
   cfg.stream = s;
-  cfg.attrs = &at;
+  cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weigh_kernel, p);
+  if (q.splits > 1) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)q.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, weigh_kernel, q);
 }
 
 }  // namespace bkv

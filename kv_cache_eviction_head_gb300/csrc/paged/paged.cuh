@@ -112,8 +112,10 @@ struct WeighParams {
   float scale_log2;
   int batch, heads, kv_heads, group, total;
   int tpt;                 // tokens per tile of query rows
+  int splits;              // CTAs that share a tile of slots (set by the launch)
 };
-cudaError_t launch_weigh(const WeighParams& p, int grid, cudaStream_t s);
+// items: (sequence, KV head, tile of 128 slots) triples there can be
+cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s);
 // Fills p's tensor map (host only). False on failure.
 bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride);
 

@@ -241,11 +241,9 @@ bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const
   if (total > 0 && !bkv::encode_weigh_map(p, q, q_stride)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
   if (total == 0) return BKV_OK;
-  // a block for every tile of 128 slots there can be, up to eight rounds of two per SM;
-  // blocks walk on from there
+  // tiles of 128 slots there can be
   const int64_t items = (int64_t)c.batch * c.kv_heads * ((p.pg.cap + 127) / 128);
-  const int grid = (int)std::min<int64_t>(items, 8 * 2 * bkv::kSms);
-  return bkv::launch_weigh(p, grid, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+  return bkv::launch_weigh(p, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 
 bkv_status bkv_evict_weight(const bkv_config* cfg, const bkv_pages* pages, void* const* K, void* const* V,
