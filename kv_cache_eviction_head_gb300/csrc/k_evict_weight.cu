@@ -22,15 +22,9 @@ namespace bkv {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kEvictThreads = 256;
-constexpr int kEvictCtas = 4;                               // per SM
-constexpr int kWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;                                 // eleven bits of a key
-constexpr int kPerThread = kBins / kEvictThreads;
 constexpr int kMostCached = 8192;                           // slots whose keys stay in shared memory
-constexpr int kFew = kEvictThreads;                         // keys of a bin that are ranked directly
-constexpr int kMoveRows = 32;                               // rows of K and of V per step
-constexpr int kMoveLoads = kMoveRows * 32 / kEvictThreads;  // 16-byte pieces per thread and step
+constexpr int kMoveLoads = 4;                               // 16-byte pieces per thread and step
 
 struct Unit {
   int layer, b, h;
@@ -62,23 +56,27 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (x & 0x80000000u) ? ~x : x | 0x80000000u;
 }
 
+template <int kThreads>
 struct Shared {
   union {
     int hist[kBins];         // in descending order of the digits
-    uint32_t few[kFew];      // keys of the bin in question
+    uint32_t few[kThreads];  // keys of a bin that are ranked directly
     struct {
-      int64_t src[kEvictThreads * 2], dst[kEvictThreads * 2];  // rows that move
+      int64_t src[kThreads * 2], dst[kThreads * 2];  // rows that move
     } list;
   };
   int chosen, left, found;
-  int2 warp_sum[kWarps];
+  int2 warp_sum[kThreads / 32];
 };
 
-__global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel(const __grid_constant__ EvictWeightParams P) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel(const __grid_constant__ EvictWeightParams P) {
+  constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads, kFew = kThreads;
+  constexpr int kMoveRows = kMoveLoads * kThreads / 32;  // rows of K and of V per step
   // the first P.cached slots' keys; order-free: kept slots below the budget as bits, and the
   // kept in front of every word
   extern __shared__ uint32_t dynamic[];
-  __shared__ __align__(16) Shared S;
+  __shared__ __align__(16) Shared<kThreads> S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   depend_wait();
   depend_go();
@@ -90,7 +88,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
   }
   if (!u.evicts) {
     // within the budget everything stays; a refused sequence has no keep set
-    for (int i = tid; i < P.budget; i += kEvictThreads) kept[i] = i < u.len && u.len <= P.budget ? i : -1;
+    for (int i = tid; i < P.budget; i += kThreads) kept[i] = i < u.len && u.len <= P.budget ? i : -1;
     return;
   }
   float* W = P.W[u.layer];
@@ -105,7 +103,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
   };
   uint32_t* cache = dynamic;
 #pragma unroll 8
-  for (int s = tid; s < min(to, P.cached); s += kEvictThreads) cache[s] = s >= from ? read_key(s) : 0u;
+  for (int s = tid; s < min(to, P.cached); s += kThreads) cache[s] = s >= from ? read_key(s) : 0u;
   auto key = [&](int slot) { return slot < P.cached ? cache[slot] : read_key(slot); };
 
   // The smallest kept key, as far as its bits are known, and how many of those equal in these
@@ -116,19 +114,21 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
   for (int shift = 21; any && shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
     const uint32_t digit = shift == 0 ? 1023u : 2047u;
     int4* clear = reinterpret_cast<int4*>(S.hist);
-    clear[tid] = clear[tid + kEvictThreads] = make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; ++i) clear[tid + i * kThreads] = make_int4(0, 0, 0, 0);
     if (tid == 0) S.found = 0;
     __syncthreads();
-    for (int s = tid; s < to; s += kEvictThreads) {
+    for (int s = tid; s < to; s += kThreads) {
       if (s < from) continue;
       const uint32_t k = key(s);
       if ((k & known) == least) atomicAdd(&S.hist[kBins - 1 - (k >> shift & digit)], 1);
     }
     __syncthreads();
-    // the bin, from the top, in which the need-th largest lies: eight bins a thread
+    // the bin, from the top, in which the need-th largest lies: neighbouring bins a thread
     int mine[kPerThread], sum = 0;
-    *reinterpret_cast<int4*>(&mine[0]) = reinterpret_cast<const int4*>(S.hist)[2 * tid];
-    *reinterpret_cast<int4*>(&mine[4]) = reinterpret_cast<const int4*>(S.hist)[2 * tid + 1];
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; ++i)
+      *reinterpret_cast<int4*>(&mine[4 * i]) = reinterpret_cast<const int4*>(S.hist)[tid * (kPerThread / 4) + i];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) sum += mine[i];
     int upto = sum;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
     if (in_bin <= kFew) {
       // few: each counts those above it
       __syncthreads();
-      for (int s = tid; s < to; s += kEvictThreads) {
+      for (int s = tid; s < to; s += kThreads) {
         if (s < from) continue;
         const uint32_t k = key(s);
         if ((k & known) == least) {
@@ -195,31 +195,46 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
     __syncthreads();
   }
 
-  // The kept list. A warp takes neighbouring slots, counts what it keeps, and lists it behind
-  // what the warps in front of it keep.
+  // The kept list. A warp takes neighbouring slots: words of 32, as many as lanes at a time,
+  // lane i keeping what is known of word i. It counts what it keeps, and lists it behind what
+  // the warps in front of it keep.
   const int ties = any ? need : 0;
   const int span = ((u.len + kWarps - 1) / kWarps + 31) / 32 * 32;
   const int begin = min(warp * span, u.len), end = min(begin + span, u.len);
-  auto look = [&](int s, bool& gt, bool& eq) {
-    gt = eq = false;
-    if (s >= end) return;
-    if (s < from || s >= to) {
-      gt = true;
-    } else if (any) {
-      const uint32_t k = key(s) & known;
-      gt = k > least;
-      eq = k == least;
+  uint32_t greater = 0, equal = 0;  // word `lane` of the 32 looked at: slots kept in any case, slots equal to the least
+  auto look = [&](int s0) {
+    greater = equal = 0;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+      const int s = s0 + i * 32 + lane;
+      if (s0 + i * 32 >= end) break;
+      bool gt = false, eq = false;
+      if (s < end) {
+        if (s < from || s >= to) {
+          gt = true;
+        } else if (any) {
+          const uint32_t k = key(s) & known;
+          gt = k > least;
+          eq = k == least;
+        }
+      }
+      const unsigned bg = __ballot_sync(kAll, gt), be = __ballot_sync(kAll, eq);
+      if (lane == i) {
+        greater = bg;
+        equal = be;
+      }
     }
   };
   __syncthreads();  // the keys are all there; S.warp_sum is free
   {
     int g = 0, e = 0;
-    for (int s0 = begin; s0 < end; s0 += 32) {
-      bool gt, eq;
-      look(s0 + lane, gt, eq);
-      g += __popc(__ballot_sync(kAll, gt));
-      e += __popc(__ballot_sync(kAll, eq));
+    for (int s0 = begin; s0 < end; s0 += 1024) {
+      look(s0);
+      g += __popc(greater);
+      e += __popc(equal);
     }
+    g = __reduce_add_sync(kAll, g);
+    e = __reduce_add_sync(kAll, e);
     if (lane == 0) S.warp_sum[warp] = make_int2(g, e);
   }
   __syncthreads();
@@ -232,43 +247,74 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
   const int words = (P.budget + 31) / 32;
   uint32_t* bits = dynamic + P.cached;
   int* in_front = reinterpret_cast<int*>(bits + words);
-  {
-    int g = g0, e = e0;
-    for (int s0 = begin; s0 < end; s0 += 32) {
-      const int s = s0 + lane;
-      bool gt, eq;
-      look(s, gt, eq);
-      const unsigned bg = __ballot_sync(kAll, gt), be = __ballot_sync(kAll, eq);
-      const int rank = e + __popc(be & lower);
-      const bool keep = gt || (eq && rank < ties);
-      const int at = g + __popc(bg & lower) + min(rank, ties);  // kept slots in front of s
-      if (!P.order_free) {
-        if (keep && at < P.budget) kept[at] = s;
-      } else {
-        const unsigned bk = __ballot_sync(kAll, keep && s < P.budget);
-        if (lane == 0 && s < P.budget) {
-          bits[s >> 5] = bk;
-          in_front[s >> 5] = at;
-        }
-        if (keep && s < P.budget) kept[s] = s;
+  uint32_t keep = 0;  // of word `lane`: its kept slots, and those in front of it
+  int at = 0;
+  auto keep_words = [&](int s0) {
+    if (span > 1024) look(s0);  // otherwise it was the only look
+    int g = __popc(greater), e = __popc(equal);
+    const int own_g = g, own_e = e;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(kAll, g, off), y = __shfl_up_sync(kAll, e, off);
+      if (lane >= off) {
+        g += x;
+        e += y;
       }
-      g += __popc(bg);
-      e += __popc(be);
     }
+    const int g_all = __shfl_sync(kAll, g, 31), e_all = __shfl_sync(kAll, e, 31);
+    g += g0 - own_g;
+    e += e0 - own_e;
+    at = g + min(e, ties);
+    uint32_t low = equal;  // the lowest of the equal ones, up to `ties` in all
+    for (int drop = own_e - max(ties - e, 0); drop > 0 && low; --drop) low &= ~(0x80000000u >> __clz(low));
+    keep = greater | low;
+    g0 += g_all;
+    e0 += e_all;
+  };
+  const int g_begin = g0, e_begin = e0;
+  for (int s0 = begin; s0 < end; s0 += 1024) {
+    keep_words(s0);
     if (P.order_free) {
+      const int w0 = s0 + lane * 32;
+      if (w0 < min(end, P.budget)) {
+        bits[w0 >> 5] = P.budget - w0 < 32 ? keep & ((1u << (P.budget - w0)) - 1) : keep;
+        in_front[w0 >> 5] = at;
+      }
+    }
+    for (int i = 0; i < 32 && s0 + i * 32 < end; ++i) {
+      const uint32_t k = __shfl_sync(kAll, keep, i);
+      const int to_slot = P.order_free ? s0 + i * 32 + lane : __shfl_sync(kAll, at, i) + __popc(k & lower);
+      if ((k >> lane & 1) && to_slot < P.budget) kept[to_slot] = s0 + i * 32 + lane;
+    }
+  }
+  __syncthreads();
+
+  int count = 0;  // rows in the list
+  auto rows_of = [&](int source, int i, int64_t& a, int64_t& b) {
+    a = pool_row(P.pg, P.kv_heads, u.b, u.h, source);
+    b = pool_row(P.pg, P.kv_heads, u.b, u.h, i);
+    if (a < 0 || b < 0) latch(P.status, BKV_ERR_INVALID_ARG);
+    if (b < 0 || !BKV_IN_RANGE(max(a, b) < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) a = -1;
+  };
+  bool listed = false;
+  if (P.order_free) {
+    // the t-th dropped slot below the budget takes the t-th kept one from there on
+    const int below = in_front[words - 1] + __popc(bits[words - 1]);
+    const int moved = P.budget - below;
+    listed = moved <= 2 * kThreads;
+    if (listed) {
+      for (int t = tid; t < moved; t += kThreads) S.list.src[t] = -1;
       __syncthreads();
-      // the t-th dropped slot below the budget takes the t-th kept one from there on
-      const int below = in_front[words - 1] + __popc(bits[words - 1]);
-      g = g0;
-      e = e0;
-      for (int s0 = begin; s0 < end; s0 += 32) {
-        const int s = s0 + lane;
-        bool gt, eq;
-        look(s, gt, eq);
-        const unsigned bg = __ballot_sync(kAll, gt), be = __ballot_sync(kAll, eq);
-        const int rank = e + __popc(be & lower);
-        const int t = g + __popc(bg & lower) + min(rank, ties) - below;
-        if (s >= P.budget && (gt || (eq && rank < ties))) {
+    }
+    if (end > P.budget) {
+      g0 = g_begin;
+      e0 = e_begin;
+      for (int s0 = begin; s0 < end; s0 += 1024) {
+        keep_words(s0);
+        for (int i = 0; i < 32 && s0 + i * 32 < end; ++i) {
+          const uint32_t k = __shfl_sync(kAll, keep, i);
+          const int t = __shfl_sync(kAll, at, i) + __popc(k & lower) - below, source = s0 + i * 32 + lane;
+          if (source < P.budget || !(k >> lane & 1)) continue;
           int lo = 0, hi = words - 1;  // the last word with at most t dropped slots in front
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -278,45 +324,47 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
           uint32_t holes = ~bits[lo];
           for (int skip = t - (lo * 32 - in_front[lo]); skip > 0; --skip) holes &= holes - 1;
           const int hole = lo * 32 + __ffs(holes) - 1;
-          if (holes != 0 && hole < P.budget) kept[hole] = s;
+          if (holes == 0 || hole >= P.budget) continue;
+          kept[hole] = source;
+          if (listed && t >= 0 && t < 2 * kThreads) {
+            int64_t a, b;
+            rows_of(source, hole, a, b);
+            S.list.src[t] = a;
+            S.list.dst[t] = b;
+          }
         }
-        g += __popc(bg);
-        e += __popc(be);
       }
     }
+    if (listed) count = moved;
+    __syncthreads();
   }
-  __syncthreads();
 
   // The rows.
   uint4* pool = tid & 16 ? P.V[u.layer] : P.K[u.layer];
   const int part = tid & 15;
-  int count = 0;  // rows in the list
-  for (int i0 = 0; i0 < P.budget; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    const int source = i < P.budget ? kept[i] : i;
-    int64_t a = -1, b = -1;
-    if (source != i && source >= 0 && source < u.len) {
-      a = pool_row(P.pg, P.kv_heads, u.b, u.h, source);
-      b = pool_row(P.pg, P.kv_heads, u.b, u.h, i);
-      if (a < 0 || b < 0) latch(P.status, BKV_ERR_INVALID_ARG);
-      if (b < 0 || !BKV_IN_RANGE(max(a, b) < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) a = -1;
-    }
-    const unsigned moving = __ballot_sync(kAll, a >= 0);
-    if (lane == 0) S.warp_sum[warp].x = __popc(moving);
-    __syncthreads();
-    int at = count + __popc(moving & lower);
+  for (int i0 = listed ? P.budget - 1 : 0; i0 < P.budget; i0 += kThreads) {
+    if (!listed) {
+      const int i = i0 + tid;
+      const int source = i < P.budget ? kept[i] : i;
+      int64_t a = -1, b = -1;
+      if (source != i && source >= 0 && source < u.len) rows_of(source, i, a, b);
+      const unsigned moving = __ballot_sync(kAll, a >= 0);
+      if (lane == 0) S.warp_sum[warp].x = __popc(moving);
+      __syncthreads();
+      int place = count + __popc(moving & lower);
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const int n = S.warp_sum[k].x;
-      if (k < warp) at += n;
-      count += n;
+      for (int k = 0; k < kWarps; ++k) {
+        const int n = S.warp_sum[k].x;
+        if (k < warp) place += n;
+        count += n;
+      }
+      if (a >= 0) {
+        S.list.src[place] = a;
+        S.list.dst[place] = b;
+      }
+      __syncthreads();
+      if (count <= kThreads && i0 + kThreads < P.budget) continue;
     }
-    if (a >= 0) {
-      S.list.src[at] = a;
-      S.list.dst[at] = b;
-    }
-    __syncthreads();
-    if (count <= kEvictThreads && i0 + kEvictThreads < P.budget) continue;
     // The next step's rows are loaded before this step's are written: their sources lie
     // behind all that this step writes.
     uint4 x[kMoveLoads], y[kMoveLoads];
@@ -325,9 +373,9 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
 #pragma unroll
       for (int k = 0; k < kMoveLoads; ++k) {
         const int r = c + k * kWarps + warp;
-        if (r < count) v[k] = pool[S.list.src[r] * 16 + part];
+        if (r < count && S.list.src[r] >= 0) v[k] = pool[S.list.src[r] * 16 + part];
       }
-      if (tid < kMoveRows && c + tid < count) w = W[S.list.src[c + tid]];
+      if (tid < kMoveRows && c + tid < count && S.list.src[c + tid] >= 0) w = W[S.list.src[c + tid]];
     };
     load(0, x, wx);
     for (int c = 0; c < count; c += kMoveRows) {
@@ -336,10 +384,10 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
 #pragma unroll
       for (int k = 0; k < kMoveLoads; ++k) {
         const int r = c + k * kWarps + warp;
-        if (r < count) pool[S.list.dst[r] * 16 + part] = x[k];
+        if (r < count && S.list.src[r] >= 0) pool[S.list.dst[r] * 16 + part] = x[k];
         x[k] = y[k];
       }
-      if (tid < kMoveRows && c + tid < count) W[S.list.dst[c + tid]] = wx;
+      if (tid < kMoveRows && c + tid < count && S.list.src[c + tid] >= 0) W[S.list.dst[c + tid]] = wx;
       wx = wy;
     }
     count = 0;
@@ -347,22 +395,33 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictCtas) evict_weight_kernel
   }
 }
 
+template <int kThreads>
+cudaError_t launch(const EvictWeightParams& p, cudaStream_t s) {
+  const auto fn = evict_weight_kernel<kThreads>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.layers * p.batch * p.kv_heads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)p.cached * 4 + (p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
 }  // namespace
 
 cudaError_t launch_evict_weight(const EvictWeightParams& given, cudaStream_t s) {
   EvictWeightParams p = given;
   p.cached = p.pg.cap < kMostCached ? p.pg.cap : kMostCached;
-  cudaError_t e = cudaFuncSetAttribute(evict_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at = dependent_launch();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.layers * p.batch * p.kv_heads));
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.dynamicSmemBytes = (size_t)p.cached * 4 + (p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0);
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_weight_kernel, p);
+  // Few units: 512 threads each (288 units of 2,064 slots: 27 us, with 256 threads 31, with 128
+  // 44). Many: 256 (6,144 units of 2,048 slots: 1,699 us, with 512 1,692, with 128 1,758), or
+  // order-free, where a unit is a chain of latencies and little else, 128 and so twice the
+  // units at once (4,096 units of 1,040 slots: 81 us, with 256 93, with 512 138).
+  const int64_t units = (int64_t)p.layers * p.batch * p.kv_heads;
+  return units <= 2 * kSms ? launch<512>(p, s) : p.order_free ? launch<128>(p, s) : launch<256>(p, s);
 }
 
 }  // namespace bkv
