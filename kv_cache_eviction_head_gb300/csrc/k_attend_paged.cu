@@ -35,12 +35,11 @@ namespace bkv {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kStages = 3;                  // tiles under way per warp
 constexpr int kBox = kTileSlots * 128;       // 16 slots x 64 elements
 constexpr int kTileBox = 4 * kBox;           // K and V of a tile: 8 KB
-constexpr int kAttendSmem = kAttendWarps * kStages * kTileBox + 1024;
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCtas = 5;                // per SM
+constexpr int kJoinCtas = 3;                // per SM
+constexpr int kAhead = 4;                   // heads whose logits are asked for ahead
 constexpr int kJoinTiles = 16;              // tiles of a block's weights, at least
 constexpr float kMinusInf = -__builtin_huge_valf();
 constexpr float kLag = 8.f;
@@ -91,7 +90,7 @@ __device__ __forceinline__ int all_tiles(const AttendPagedParams& P, int lane, b
   return __reduce_add_sync(kAll, n);
 }
 // Tiles per share. One tile per warp at least; more when there are not warps enough.
-__device__ __forceinline__ int share_of(int tiles) { return max((tiles + kAttendShares - 1) / kAttendShares, 1); }
+__device__ __forceinline__ int share_of(int tiles, int shares) { return max((tiles + shares - 1) / shares, 1); }
 // The sequence that tile t (of `per` tiles for each of a sequence's own) lies in, and the
 // sum of the tiles in front of it; b = batch behind the last. One warp.
 __device__ __forceinline__ void find_sequence(const AttendPagedParams& P, int t, int per, int lane, int& b, int& before) {
@@ -142,7 +141,7 @@ __device__ __forceinline__ void step(const AttendPagedParams& P, Place& p, int u
   } while (p.n == 0);
 }
 
-template <int NT>
+template <int NT, int kAttendWarps, int kStages>
 __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(const __grid_constant__ AttendPagedParams P) {
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t full[kAttendWarps][kStages];
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   bool bad;
   const int total = all_tiles(P, lane, bad) * units;
   if (w == 0 && lane == 0 && bad) latch(P.status, BKV_ERR_INVALID_ARG);
-  const int share = share_of(total);
+  const int share = share_of(total, P.shares);
   const int64_t begin = (int64_t)w * share;
   if (begin >= total) return;
   const int t0 = (int)begin, count = min(share, total - t0);
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
   Place a = c;  // the next tile to copy; its page is looked up one tile ahead
 
   const uint32_t ring = ((smem_u32(raw) + 1023u) & ~1023u) + warp * kStages * kTileBox;
-  const uint64_t policy = policy_evict_normal();
+  const uint64_t policy = policy_evict_first();  // read once, unlike the workspace and the weights (ragged lengths: 67 -> 60 us)
   auto fetch = [&](int stage) {
     const int slot0 = a.i * kTileSlots;
     int rows = min(kTileSlots, a.len - slot0);
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   depend_go();
   bool bad;
   const int tiles = all_tiles(P, lane, bad);
-  const int share = share_of(tiles * units);
+  const int share = share_of(tiles * units, P.shares);
 
   // Outputs, also those of sequences without a slot. Few rows: a block each (the last blocks,
   // the first have weights to do), its warps take the pieces in turn; many: a warp each.
@@ -564,6 +563,32 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   int len = len_of(P, b), n = tiles_of(len), h = (t - before * P.kv_heads) / n, i0 = t - before * P.kv_heads - h * n;
   while (true) {
     const int cnt = min(n - i0, end - t);
+    // four slots of a tile: their pool row, old weights and the first heads' logits, asked for
+    // before the sums are looked for
+    struct Slots {
+      int64_t row;
+      int in;
+      float old[4];
+      float4 x[kAhead];
+    };
+    auto fetch = [&](int q, Slots& v) {
+      v.row = -1;
+      if (q >= cnt * 4) return;
+      const int slot = (i0 + q / 4) * kTileSlots + q % 4 * 4;
+      v.in = min(4, len - slot);
+      if (v.in <= 0) return;
+      v.row = pool_row(P.pg, P.kv_heads, b, h, slot);
+      if (!BKV_IN_RANGE(v.row + v.in <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) v.row = -1;
+      if (v.row < 0) return;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.old[e] = e < v.in && P.decay != 0.f && slot + e != len - 1 ? P.weights[v.row + e] : 0.f;
+      const float4* x = reinterpret_cast<const float4*>(P.logits + (int64_t)(t + q / 4) * P.group * kTileSlots) + q % 4;
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g)
+        if (g < P.group) v.x[g] = x[g * 4];
+    };
+    Slots now, next;
+    fetch(tid, now);
     for (int g = warp; g < P.group; g += kWarps) {
       const Pieces pc = pieces_of(before, h * P.chunks + g / P.chunk, n, units, share);
       float x;
@@ -577,28 +602,26 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
     }
     __syncthreads();
     for (int q = tid; q < cnt * 4; q += kJoinThreads) {
-      const int slot = (i0 + q / 4) * kTileSlots + q % 4 * 4, in = min(4, len - slot);
-      if (in <= 0) continue;
-      const int64_t row = pool_row(P.pg, P.kv_heads, b, h, slot);
-      if (row < 0 || !BKV_IN_RANGE(row + in <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) continue;
-      float* w = P.weights + row;
-      float old[4];
+      fetch(q + kJoinThreads, next);
+      if (now.row >= 0) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](const float4& v, float z) {
+          sum[0] += exp2_approx(v.x - z);
+          sum[1] += exp2_approx(v.y - z);
+          sum[2] += exp2_approx(v.z - z);
+          sum[3] += exp2_approx(v.w - z);
+        };
 #pragma unroll
-      for (int e = 0; e < 4; ++e) old[e] = e < in && P.decay != 0.f && slot + e != len - 1 ? w[e] : 0.f;
-      const float4* x = reinterpret_cast<const float4*>(P.logits + (int64_t)(t + q / 4) * P.group * kTileSlots) + q % 4;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < kAhead; ++g)
+          if (g < P.group) add(now.x[g], lse2[g]);
+        const float4* x = reinterpret_cast<const float4*>(P.logits + (int64_t)(t + q / 4) * P.group * kTileSlots) + q % 4;
 #pragma unroll 4
-      for (int g = 0; g < P.group; ++g) {
-        const float4 v = x[g * 4];
-        const float z = lse2[g];
-        sum[0] += exp2_approx(v.x - z);
-        sum[1] += exp2_approx(v.y - z);
-        sum[2] += exp2_approx(v.z - z);
-        sum[3] += exp2_approx(v.w - z);
-      }
+        for (int g = kAhead; g < P.group; ++g) add(x[g * 4], lse2[g]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < in) w[e] = fmaf(P.decay, old[e], sum[e]);
+        for (int e = 0; e < 4; ++e)
+          if (e < now.in) P.weights[now.row + e] = fmaf(P.decay, now.old[e], sum[e]);
+      }
+      now = next;
     }
     t += cnt;
     if (t >= end) return;
@@ -616,19 +639,24 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   }
 }
 
-template <int NT>
-cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(attend_paged_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
+template <int NT, int kWarps, int kStages>
+cudaError_t launch(const AttendPagedParams& given, cudaStream_t s) {
+  constexpr int kSmem = kWarps * kStages * kTileBox + 1024;
+  static_assert(kWarps <= kAttendWarps, "the workspace holds the pieces of kAttendWarps warps per CTA");
+  AttendPagedParams p = given;
+  p.shares = kAttendCtas * kWarps;
+  const auto fn = attend_paged_kernel<NT, kWarps, kStages>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = dependent_launch();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kAttendCtas);
-  cfg.blockDim = dim3(kAttendWarps * 32);
-  cfg.dynamicSmemBytes = kAttendSmem;
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attend_paged_kernel<NT>, p);
+  e = cudaLaunchKernelEx(&cfg, fn, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(kJoinCtas * kSms);
   cfg.blockDim = dim3(kJoinThreads);
@@ -646,7 +674,9 @@ bool encode_attend_paged_maps(AttendPagedParams& p) {
 }
 
 cudaError_t launch_attend_paged(const AttendPagedParams& p, cudaStream_t s) {
-  return p.chunk == 8 ? launch<1>(p, s) : launch<2>(p, s);
+  // five warps with two tiles under way each: 192 sequences 269 us; four with three 280, three
+  // with four 280, two with six 341. Sixteen rows leave registers for four.
+  return p.chunk == 8 ? launch<1, 5, 2>(p, s) : launch<2, 4, 3>(p, s);
 }
 
 }  // namespace bkv

@@ -66,7 +66,7 @@ cudaError_t launch_store_paged(const StorePagedParams& p, cudaStream_t s);
 
 // Attention of one token: the visible tiles of all (sequence, KV head, chunk of query
 // heads) units stand in a row and are dealt out evenly to the warps of one launch.
-constexpr int kAttendWarps = 4;                               // per CTA
+constexpr int kAttendWarps = 5;                               // per CTA, at most
 constexpr int kAttendCtas = 2 * kSms;                         // two per SM
 constexpr int kAttendShares = kAttendCtas * kAttendWarps;     // warps of a launch, at most
 constexpr int kTileSlots = 16;
@@ -87,6 +87,7 @@ struct AttendPagedParams {
   int batch, heads, kv_heads, group;
   int chunk;               // query heads per unit: 8 or 16
   int chunks;              // units per KV head
+  int shares;              // warps of the launch (set by the launch)
   int64_t tiles_cap;       // tiles the logits have room for
   // workspace
   float2* part_ml;         // [2 * shares][16] reference maximum (log2) and sum of a piece
