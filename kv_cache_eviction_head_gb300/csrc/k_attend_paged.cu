@@ -41,6 +41,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 3;                // per SM
 constexpr int kAhead = 4;                   // heads whose logits are asked for ahead
 constexpr int kJoinTiles = 16;              // tiles of a block's weights, at least
+constexpr int kJoinHeads = 512;             // heads whose sums a block holds at a time
 constexpr float kMinusInf = -__builtin_huge_valf();
 constexpr float kLag = 8.f;
 
@@ -116,6 +117,23 @@ __device__ __forceinline__ void find_sequence(const AttendPagedParams& P, int t,
   before = base;
 }
 
+// For the second launch: the tiles in front of every sequence and its length. One warp.
+__device__ __forceinline__ void list_sequences(const AttendPagedParams& P, int lane) {
+  int base = 0;
+  for (int b0 = 0; b0 < P.batch; b0 += 32) {
+    const int len = b0 + lane < P.batch ? len_of(P, b0 + lane) : 0, n = tiles_of(len);
+    int upto = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kAll, upto, off);
+      if (lane >= off) upto += y;
+    }
+    if (b0 + lane < P.batch) P.seq[b0 + lane] = make_int2(base + upto - n, len);
+    base += __shfl_sync(kAll, upto, 31);
+  }
+  if (lane == 0) P.seq[P.batch] = make_int2(base, 0);
+}
+
 // A place in the row of tiles.
 struct Place {
   int b, u;        // sequence, unit within it (KV head * chunks + chunk)
@@ -165,7 +183,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 2) attend_paged_kernel(cons
 
   bool bad;
   const int total = all_tiles(P, lane, bad) * units;
-  if (w == 0 && lane == 0 && bad) latch(P.status, BKV_ERR_INVALID_ARG);
+  if (w == 0) {
+    if (lane == 0 && bad) latch(P.status, BKV_ERR_INVALID_ARG);
+    list_sequences(P, lane);
+  }
   const int share = share_of(total, P.shares);
   const int64_t begin = (int64_t)w * share;
   if (begin >= total) return;
@@ -438,22 +459,22 @@ __device__ __forceinline__ Pieces pieces_of(int before, int u, int n, int units,
 // A head's largest reference over the unit's pieces and the sum relative to it. One warp,
 // all lanes get it.
 __device__ __forceinline__ float2 join_sum(const AttendPagedParams& P, const Pieces& pc, int in_chunk, int lane) {
-  // eight pieces a lane at once, more in rounds: a running maximum and sum
+  // four pieces a lane at once, more in rounds: a running maximum and sum
   float m = kMinusInf, l = 0.f;
-  for (int c0 = pc.c0; c0 <= pc.c1; c0 += 256) {
-    float2 x[8];
+  for (int c0 = pc.c0; c0 <= pc.c1; c0 += 128) {
+    float2 x[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const int c = c0 + k * 32 + lane;
       x[k] = c <= pc.c1 ? P.part_ml[pc.at(c) * 16 + in_chunk] : make_float2(kMinusInf, 0.f);
     }
     float top = m;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, x[k].x);
     if (m != kMinusInf) l *= exp2_approx(m - top);
     // a piece without a finite logit has no part (its sum is 0, or NaN, which stays)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) l += x[k].x == kMinusInf ? x[k].y : x[k].y * exp2_approx(x[k].x - top);
+    for (int k = 0; k < 4; ++k) l += x[k].x == kMinusInf ? x[k].y : x[k].y * exp2_approx(x[k].x - top);
     m = top;
   }
   float top = m;
@@ -465,17 +486,54 @@ __device__ __forceinline__ float2 join_sum(const AttendPagedParams& P, const Pie
   return make_float2(top, l);
 }
 
+// A row's running state over some of its pieces: reference, sum, and this lane's four elements.
+struct Joined {
+  float m, l;
+  float4 y;
+};
+__device__ __forceinline__ void join_in(Joined& j, float m, float l, const float4& y) {
+  const float top = fmaxf(j.m, m);
+  const float f = j.m == kMinusInf ? 1.f : exp2_approx(j.m - top);  // without a finite logit so far: 0, or NaN, as it is
+  const float g = m == kMinusInf ? 1.f : exp2_approx(m - top);
+  j.m = top;
+  j.l = j.l * f + l * g;
+  j.y.x = j.y.x * f + y.x * g;
+  j.y.y = j.y.y * f + y.y * g;
+  j.y.z = j.y.z * f + y.z * g;
+  j.y.w = j.y.w * f + y.w * g;
+}
+__device__ __forceinline__ Joined join_pieces(const AttendPagedParams& P, const Pieces& pc, int in_chunk, int from, int by, int lane) {
+  Joined j{kMinusInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int c0 = from; c0 <= pc.c1; c0 += 4 * by) {
+    float2 ml[4];
+    float4 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k * by;
+      ml[k] = make_float2(kMinusInf, 0.f);
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c <= pc.c1) {
+        ml[k] = P.part_ml[pc.at(c) * 16 + in_chunk];
+        y[k] = P.part_o[(int64_t)(pc.at(c) * P.chunk + in_chunk) * 32 + lane];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) join_in(j, ml[k].x, ml[k].y, y[k]);
+  }
+  return j;
+}
+
 // Outputs of units that lie in several shares, and weights.
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(const __grid_constant__ AttendPagedParams P) {
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ float4 sums[kWarps][32];
-  __shared__ float lse2[kMaxGroup];
+  __shared__ float2 sums_ml[kWarps];
+  __shared__ float lse2[kJoinHeads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = P.kv_heads * P.chunks;
   depend_wait();
   depend_go();
-  bool bad;
-  const int tiles = all_tiles(P, lane, bad);
+  const int tiles = P.seq[P.batch].x;
   const int share = share_of(tiles * units, P.shares);
 
   // Outputs, also those of sequences without a slot. Few rows: a block each (the last blocks,
@@ -485,50 +543,31 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   const int block = gridDim.x - 1 - blockIdx.x;
   for (int r = wide ? block : block * kWarps + warp; r < rows; r += gridDim.x * (wide ? 1 : kWarps)) {
     const int b = r / P.heads, head = r - b * P.heads;
-    const int len = len_of(P, b);
-    if (len == 0) {
+    const int2 q = P.seq[b];
+    if (q.y == 0) {
       if (wide && warp != 0) continue;
       reinterpret_cast<uint2*>(P.out)[(int64_t)r * 32 + lane] = make_uint2(0, 0);
       if (lane == 0 && P.lse) P.lse[r] = kMinusInf;
       continue;
     }
     const int h = head / P.group, g = head - h * P.group, u = h * P.chunks + g / P.chunk, in = g % P.chunk;
-    int before = 0;
-    for (int x = lane; x < b; x += 32) before += tiles_of(len_of(P, x));
-    before = __reduce_add_sync(kAll, before);
-    const Pieces pc = pieces_of(before, u, tiles_of(len), units, share);
+    const Pieces pc = pieces_of(q.x, u, tiles_of(q.y), units, share);
     if (pc.c0 == pc.c1) continue;  // one answer for the whole block where it shares a row
-    const float2 ml = join_sum(P, pc, in, lane);
-    const float inv = 1.f / ml.y;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int by = wide ? kWarps : 1;
-#pragma unroll 8
-    for (int c = pc.c0 + (wide ? warp : 0); c <= pc.c1; c += by) {
-      const float m = P.part_ml[pc.at(c) * 16 + in].x;
-      const float4 x = P.part_o[(int64_t)(pc.at(c) * P.chunk + in) * 32 + lane];
-      const float f = m == kMinusInf ? 1.f : exp2_approx(m - ml.x) * inv;  // without a finite logit: o is 0, or NaN
-      y.x = fmaf(f, x.x, y.x);
-      y.y = fmaf(f, x.y, y.y);
-      y.z = fmaf(f, x.z, y.z);
-      y.w = fmaf(f, x.w, y.w);
-    }
+    Joined j = join_pieces(P, pc, in, pc.c0 + (wide ? warp : 0), wide ? kWarps : 1, lane);
     if (wide) {
-      sums[warp][lane] = y;
+      sums[warp][lane] = j.y;
+      if (lane == 0) sums_ml[warp] = make_float2(j.m, j.l);
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
-        for (int k = 1; k < kWarps; ++k) {
-          const float4 x = sums[k][lane];
-          y.x += x.x;
-          y.y += x.y;
-          y.z += x.z;
-          y.w += x.w;
-        }
+        for (int k = 1; k < kWarps; ++k) join_in(j, sums_ml[k].x, sums_ml[k].y, sums[k][lane]);
       }
       __syncthreads();
       if (warp != 0) continue;
     }
-    if (ml.y == 0.f) y.x = y.y = y.z = y.w = __builtin_nanf("");  // every logit is -inf
+    const float inv = 1.f / j.l;
+    float4 y = make_float4(j.y.x * inv, j.y.y * inv, j.y.z * inv, j.y.w * inv);
+    if (j.l == 0.f) y.x = y.y = y.z = y.w = __builtin_nanf("");  // every logit is -inf
     // elements (lane / 4) + 8 i, i = 4 (lane % 4) .. + 3: the order of the fragments
     __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + (int64_t)r * kD + (lane >> 2) + (lane & 3) * 32;
     to[0] = __float2bfloat16_rn(y.x);
@@ -538,18 +577,17 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
     const float check = (y.x * 0.f + y.y * 0.f) + (y.z * 0.f + y.w * 0.f);
     if (check != 0.f) latch(P.status, BKV_ERR_NONFINITE);
     if (lane == 0) {
-      const float lse = (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+      const float lse = (j.m + log2f(j.l)) * 0.6931471805599453f;
       if (P.lse) P.lse[r] = lse;
       if (!(fabsf(lse) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
     }
   }
 
   if (!P.weights) return;
-  // Weights: a block takes an equal share of the (sequence, KV head, tile) row, unit by unit:
-  // its warps find the heads' sums, then a thread takes four slots of a tile.
-  const int64_t room = P.tiles_cap;
+  // Weights: a block takes an equal share of the (sequence, KV head, tile) row, sequence by
+  // sequence: its warps find the heads' sums, then a thread takes four slots of a tile.
   const int64_t all = (int64_t)tiles * P.kv_heads;
-  if (all > room) {  // a page in two tables: more tiles than the pool has slots for
+  if (all > P.tiles_cap) {  // a page in two tables: more tiles than the pool has slots for
     if (blockIdx.x == 0 && tid == 0) latch(P.status, BKV_ERR_INVALID_ARG);
     return;
   }
@@ -558,26 +596,42 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   if (begin >= all) return;
   int t = (int)begin;
   const int end = (int)min(begin + each, all);
-  int b, before;
-  find_sequence(P, t, P.kv_heads, lane, b, before);
-  int len = len_of(P, b), n = tiles_of(len), h = (t - before * P.kv_heads) / n, i0 = t - before * P.kv_heads - h * n;
+  // the sequence of tile t: the last with at most t tiles in front of it that has any itself
+  int b = 0;
+  for (int b0 = 0; b0 < P.batch; b0 += 32) {
+    const bool in_front = b0 + lane < P.batch && P.seq[b0 + lane].x * P.kv_heads <= t;
+    const int n = __popc(__ballot_sync(kAll, in_front));
+    b = n ? b0 + n - 1 : b;
+    if (n < 32) break;
+  }
+  const int most_heads = kJoinHeads / P.group;  // KV heads whose sums fit
   while (true) {
-    const int cnt = min(n - i0, end - t);
+    const int2 seq = P.seq[b];
+    const int len = seq.y, n = tiles_of(len), before = seq.x;
+    if (len == 0) {  // none of its own; there are tiles left, so a later sequence has them
+      if (++b >= P.batch) return;
+      continue;
+    }
+    const int i0 = t - before * P.kv_heads, h0 = i0 / n;  // place in the sequence's tiles
+    const int cnt = min(min(n * P.kv_heads, n * (h0 + most_heads)) - i0, end - t);
+    const int heads = ((i0 + cnt - 1) / n - h0 + 1) * P.group;
     // four slots of a tile: their pool row, old weights and the first heads' logits, asked for
     // before the sums are looked for
     struct Slots {
       int64_t row;
-      int in;
+      int in, h;
       float old[4];
       float4 x[kAhead];
     };
     auto fetch = [&](int q, Slots& v) {
       v.row = -1;
       if (q >= cnt * 4) return;
-      const int slot = (i0 + q / 4) * kTileSlots + q % 4 * 4;
+      const int i = i0 + q / 4;
+      v.h = i / n;
+      const int slot = (i - v.h * n) * kTileSlots + q % 4 * 4;
       v.in = min(4, len - slot);
       if (v.in <= 0) return;
-      v.row = pool_row(P.pg, P.kv_heads, b, h, slot);
+      v.row = pool_row(P.pg, P.kv_heads, b, v.h, slot);
       if (!BKV_IN_RANGE(v.row + v.in <= (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) v.row = -1;
       if (v.row < 0) return;
 #pragma unroll
@@ -589,34 +643,36 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
     };
     Slots now, next;
     fetch(tid, now);
-    for (int g = warp; g < P.group; g += kWarps) {
+    for (int k = warp; k < heads; k += kWarps) {
+      const int h = h0 + k / P.group, g = k % P.group;
       const Pieces pc = pieces_of(before, h * P.chunks + g / P.chunk, n, units, share);
       float x;
       if (pc.c0 == pc.c1) {
-        x = P.lse2[(int64_t)b * P.heads + h * P.group + g];
+        x = P.lse2[(int64_t)b * P.heads + h0 * P.group + k];
       } else {
         const float2 ml = join_sum(P, pc, g % P.chunk, lane);
         x = ml.x + log2f(ml.y);
       }
-      if (lane == 0) lse2[g] = x;
+      if (lane == 0) lse2[k] = x;
     }
     __syncthreads();
     for (int q = tid; q < cnt * 4; q += kJoinThreads) {
       fetch(q + kJoinThreads, next);
       if (now.row >= 0) {
+        const float* z = lse2 + (now.h - h0) * P.group;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](const float4& v, float z) {
-          sum[0] += exp2_approx(v.x - z);
-          sum[1] += exp2_approx(v.y - z);
-          sum[2] += exp2_approx(v.z - z);
-          sum[3] += exp2_approx(v.w - z);
+        auto add = [&](const float4& v, float l) {
+          sum[0] += exp2_approx(v.x - l);
+          sum[1] += exp2_approx(v.y - l);
+          sum[2] += exp2_approx(v.z - l);
+          sum[3] += exp2_approx(v.w - l);
         };
 #pragma unroll
         for (int g = 0; g < kAhead; ++g)
-          if (g < P.group) add(now.x[g], lse2[g]);
+          if (g < P.group) add(now.x[g], z[g]);
         const float4* x = reinterpret_cast<const float4*>(P.logits + (int64_t)(t + q / 4) * P.group * kTileSlots) + q % 4;
 #pragma unroll 4
-        for (int g = kAhead; g < P.group; ++g) add(x[g * 4], lse2[g]);
+        for (int g = kAhead; g < P.group; ++g) add(x[g * 4], z[g]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (e < now.in) P.weights[now.row + e] = fmaf(P.decay, now.old[e], sum[e]);
@@ -625,17 +681,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
     }
     t += cnt;
     if (t >= end) return;
+    if (i0 + cnt == n * P.kv_heads && ++b >= P.batch) return;
     __syncthreads();
-    i0 = 0;
-    if (++h == P.kv_heads) {
-      h = 0;
-      before += n;
-      do {  // there are tiles left, so a sequence has them
-        if (++b >= P.batch) return;
-        len = len_of(P, b);
-      } while (len == 0);
-      n = tiles_of(len);
-    }
   }
 }
 
@@ -646,7 +693,8 @@ cudaError_t launch(const AttendPagedParams& given, cudaStream_t s) {
   AttendPagedParams p = given;
   p.shares = kAttendCtas * kWarps;
   const auto fn = attend_paged_kernel<NT, kWarps, kStages>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = allow_shared(fn, kSmem, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = dependent_launch();
   cudaLaunchConfig_t cfg{};

@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
 template <int kThreads>
 cudaError_t launch(const EvictWeightParams& p, cudaStream_t s) {
   const auto fn = evict_weight_kernel<kThreads>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_shared(fn, 200 * 1024, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = dependent_launch();
   cudaLaunchConfig_t cfg{};

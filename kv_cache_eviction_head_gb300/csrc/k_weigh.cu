@@ -531,7 +531,8 @@ bool encode_weigh_map(WeighParams& p, const void* q, int64_t q_stride) {
 }
 
 cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeighSmem);
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_shared(weigh_kernel, kWeighSmem, configured);
   if (e != cudaSuccess) return e;
   WeighParams q = p;
   // Shares are halved while that keeps all CTAs in three or so rounds of 2 x 152 and leaves

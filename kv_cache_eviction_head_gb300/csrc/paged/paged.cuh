@@ -4,6 +4,8 @@
 // paged_api.cu.
 #pragma once
 
+#include <atomic>
+
 #include "attend/attend.cuh"
 
 namespace bkv {
@@ -40,6 +42,20 @@ __device__ __forceinline__ int64_t pool_row(const Pages& p, int kv_heads, int b,
   const int k = page_of(p, slot);
   const int page = pool_page(p, b, k);
   return page < 0 ? -1 : ((int64_t)page * kv_heads + h) * p.page_size + (slot - k * p.page_size);
+}
+
+// Allows a kernel its dynamic shared memory, once per device (a bit each; devices beyond
+// the 64th every time).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel fn, int bytes, std::atomic<unsigned long long>& configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (configured.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured.fetch_or(bit);
+  return e;
 }
 
 struct StorePagedParams {
@@ -93,6 +109,7 @@ struct AttendPagedParams {
   float2* part_ml;         // [2 * shares][16] reference maximum (log2) and sum of a piece
   float4* part_o;          // [2 * shares][chunk][d / 4]
   float* lse2;             // [batch][heads] log2 of the sum, of units done by one warp
+  int2* seq;               // [batch + 1] tiles in front of a sequence (all of them), its length
   float* logits;           // [tile][group][16], log2 units; with weights only
 };
 cudaError_t launch_attend_paged(const AttendPagedParams& p, cudaStream_t s);

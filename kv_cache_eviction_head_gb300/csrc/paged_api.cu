@@ -45,7 +45,7 @@ int64_t most_tiles(const bkv_config& c, const bkv::Pages& p) {
 }
 
 struct Workspace {
-  size_t part_ml, part_o, lse2, logits, bytes;
+  size_t part_ml, part_o, lse2, seq, logits, bytes;
 };
 Workspace lay_out(const bkv_config& c, const bkv::Pages& p, bool weighed) {
   const size_t g = (size_t)(c.heads / c.kv_heads), pieces = 2 * (size_t)bkv::kAttendShares;
@@ -54,7 +54,8 @@ Workspace lay_out(const bkv_config& c, const bkv::Pages& p, bool weighed) {
   w.part_ml = 0;
   w.part_o = up(pieces * 16 * sizeof(float2));
   w.lse2 = w.part_o + up(pieces * (g > 8 ? 16 : 8) * bkv::kD * sizeof(float));
-  w.logits = w.lse2 + up((size_t)c.batch * c.heads * sizeof(float));
+  w.seq = w.lse2 + up((size_t)c.batch * c.heads * sizeof(float));
+  w.logits = w.seq + up(((size_t)c.batch + 1) * sizeof(int2));
   w.bytes = w.logits + (weighed ? up((size_t)most_tiles(c, p) * c.heads * bkv::kTileSlots * sizeof(float)) : 0);
   return w;
 }
@@ -201,6 +202,7 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
   p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
   p.part_o = reinterpret_cast<float4*>(base + w.part_o);
   p.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  p.seq = reinterpret_cast<int2*>(base + w.seq);
   p.logits = weights ? reinterpret_cast<float*>(base + w.logits) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (!bkv::encode_attend_paged_maps(p)) return BKV_ERR_CUDA;
