@@ -173,6 +173,14 @@ def test_weigh_few_and_many_sequences(bkv, lens, first, decay):
     assert weigh_case(bkv, 32, 8, lens, first, 16, 3, decay=decay) <= 0
 
 
+@pytest.mark.parametrize("heads,kv", [(4, 1), (8, 8), (28, 4), (48, 1)])
+@pytest.mark.parametrize("lens", [[1900], [900, 0, 1500, 40]])
+def test_weigh_shared_by_clusters(bkv, heads, kv, lens):
+    """Few tiles of slots: CTAs share a tile's queries, in numbers that do not divide them."""
+    assert weigh_case(bkv, heads, kv, lens, [0] * len(lens), None, 31, decay=0.5) <= 0
+    assert weigh_case(bkv, heads, kv, lens, [300] * len(lens), 64, 32, decay=0.5) <= 0
+
+
 def test_weigh_large_logits(bkv):
     assert weigh_case(bkv, 8, 2, [400, 90], [0, 200], 64, 8, scale=40.0) <= 0
 
@@ -249,9 +257,18 @@ def test_evict_many_layers_and_sequences(bkv):
     evict_case(bkv, 4, 1, [60, 50, 40] * 20, 16, 13, budget=45, prefix=1, recent=2, layers=7)
 
 
+@pytest.mark.parametrize("over", [7, 700])
+def test_evict_many_units_order_free(bkv, over):
+    """More than 304 units, with few dropped slots below the budget and with more than a list holds."""
+    lens = [800 + over, 800 + over + 3, 800] * 20
+    evict_case(bkv, 8, 2, lens, None, 15, budget=800, prefix=1, recent=4, layers=3, order_free=True)
+
+
 def test_evict_long(bkv):
     evict_case(bkv, 4, 2, [9000], 64, 14, budget=4096, prefix=4, recent=16, layers=1)
     evict_case(bkv, 4, 2, [9000], None, 14, budget=5000, prefix=4, recent=16, layers=1, order_free=True)
+    evict_case(bkv, 4, 1, [20000, 17000], 16, 14, budget=12345, prefix=4, recent=16, layers=1, values=[0.0, 1.0, 2.0, 3.0])
+    evict_case(bkv, 4, 1, [20000], 16, 14, budget=12345, prefix=4, recent=16, layers=1, order_free=True, values=[0.0, 1.0])
 
 
 # ---------------------------------------------------------------- rotary store
