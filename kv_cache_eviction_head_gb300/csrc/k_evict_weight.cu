@@ -34,10 +34,10 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_of(const EvictWeightParams& P) {
   Unit u;
-  const int64_t i = blockIdx.x;
-  u.h = (int)(i % P.kv_heads);
-  u.b = (int)(i / P.kv_heads % P.batch);
-  u.layer = (int)(i / ((int64_t)P.kv_heads * P.batch));
+  const unsigned i = blockIdx.x / (unsigned)P.kv_heads;  // fewer than 2^31 units
+  u.h = (int)(blockIdx.x - i * P.kv_heads);
+  u.layer = (int)(i / (unsigned)P.batch);
+  u.b = (int)(i - u.layer * P.batch);
   const int given = P.lens[u.b];
   u.len = min(max(given, 0), P.pg.cap);
   u.bad = u.len != given;
@@ -72,6 +72,7 @@ struct Shared {
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel(const __grid_constant__ EvictWeightParams P) {
   constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads, kFew = kThreads;
+  static_assert(kBins % (4 * kThreads) == 0, "a thread clears and reads its bins four at a time");
   constexpr int kMoveRows = kMoveLoads * kThreads / 32;  // rows of K and of V per step
   // the first P.cached slots' keys; order-free: kept slots below the budget as bits, and the
   // kept in front of every word
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
     for (int i = 0; i < 32 && s0 + i * 32 < end; ++i) {
       const uint32_t k = __shfl_sync(kAll, keep, i);
       const int to_slot = P.order_free ? s0 + i * 32 + lane : __shfl_sync(kAll, at, i) + __popc(k & lower);
-      if ((k >> lane & 1) && to_slot < P.budget) kept[to_slot] = s0 + i * 32 + lane;
+      if ((k >> lane & 1) && (unsigned)to_slot < (unsigned)P.budget) kept[to_slot] = s0 + i * 32 + lane;
     }
   }
   __syncthreads();
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
             else hi = mid - 1;
           }
           uint32_t holes = ~bits[lo];
-          for (int skip = t - (lo * 32 - in_front[lo]); skip > 0; --skip) holes &= holes - 1;
+          for (int skip = t - (lo * 32 - in_front[lo]); skip > 0 && holes; --skip) holes &= holes - 1;
           const int hole = lo * 32 + __ffs(holes) - 1;
           if (holes == 0 || hole >= P.budget) continue;
           kept[hole] = source;
