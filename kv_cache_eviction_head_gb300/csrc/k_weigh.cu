@@ -276,8 +276,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   depend_wait();
   depend_go();
-  if (warp == 0) {
-    // tiles of slots of the longest sequence: the order of items is tile by tile
+  // tiles of slots of the longest sequence: the order of items is tile by tile. A block or
+  // cluster that has one item only needs no answer but that its item is there.
+  const bool one = item_step >= P.items;
+  if (warp == 0 && (!one || blockIdx.x == 0)) {
     int most = 0;
     bool bad = false;
     for (int b = lane; b < P.batch; b += 32) {
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   if (P.splits > 1) cluster_sync();  // the ranks' barriers are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int64_t total = items;
+  const int64_t total = one ? P.items : items;
 
   if (warp == kProducer) {
     // Copies run two tiles ahead of the columns, which need a free buffer of logits.
@@ -535,6 +537,7 @@ cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s) {
   const cudaError_t e = allow_shared(weigh_kernel, kWeighSmem, configured);
   if (e != cudaSuccess) return e;
   WeighParams q = p;
+  q.items = items;
   // Shares are halved while that keeps all CTAs in three or so rounds of 2 x 152 and leaves
   // eight tiles of queries to each, for prompts of the average length
   const int64_t tiles = p.total / p.batch / p.tpt;
