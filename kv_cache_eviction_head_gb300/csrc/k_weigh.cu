@@ -221,16 +221,14 @@ __device__ __forceinline__ void read_sequence(const WeighParams& P, int b, int& 
   slots = n == 0 ? 0 : (int)min(most, (int64_t)P.pg.cap);
   bad = begin != x || end != y || (n > 0 && (first != f || most > P.pg.cap));
 }
-__device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item, int rank) {
+__device__ __forceinline__ WeighItem item_of(const WeighParams& P, int item, int rank) {
   WeighItem w;
-  const int per = P.batch * P.kv_heads;
-  const int64_t tile = item / per;
-  const int u = (int)(item - tile * per);
-  w.b = u / P.kv_heads;
-  w.h = u - w.b * P.kv_heads;
+  const unsigned v = (unsigned)item / (unsigned)P.kv_heads, tile = v / (unsigned)P.batch;
+  w.h = item - (int)v * P.kv_heads;
+  w.b = (int)(v - tile * P.batch);
   bool bad;
   read_sequence(P, w.b, w.begin, w.n, w.first, w.slots, bad);
-  w.j0 = (int)min(tile * 128, (int64_t)0x7FFFFF00);
+  w.j0 = (int)(tile * 128);  // a table holds fewer than 2^31 - 4096 slots, and the items come from it
   w.tiles = 0;
   w.i0 = 0;
   if (w.j0 < w.slots) {
@@ -244,12 +242,12 @@ __device__ __forceinline__ WeighItem item_of(const WeighParams& P, int64_t item,
 __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_constant__ WeighParams P) {
   extern __shared__ unsigned char raw[];
   __shared__ WeighControl C;
-  __shared__ int64_t items;
+  __shared__ int items;
   unsigned char* qring = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Ctl* ctl = &C.ctl;
   const int rank = P.splits > 1 ? (int)cluster_rank() : 0;
-  const int64_t item0 = blockIdx.x / P.splits, item_step = gridDim.x / P.splits;
+  const int item0 = blockIdx.x / P.splits, item_step = gridDim.x / P.splits;
   if (tid == 0) {
     for (int i = 0; i < kQStages; ++i) {
       mbar_init(&C.full[i], 1);
@@ -291,14 +289,14 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     }
     most = __reduce_max_sync(kFull, most);
     if (__any_sync(kFull, bad) && lane == 0 && blockIdx.x == 0) latch(P.status, BKV_ERR_INVALID_ARG);
-    if (lane == 0) items = ((int64_t)most + 127) / 128 * P.batch * P.kv_heads;
+    if (lane == 0) items = (int)(((unsigned)most + 127) / 128) * P.batch * P.kv_heads;
   }
   tc_fence_before();
   __syncthreads();
   if (P.splits > 1) cluster_sync();  // the ranks' barriers are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int64_t total = one ? P.items : items;
+  const int total = one ? P.items : items;
 
   if (warp == kProducer) {
     // Copies run two tiles ahead of the columns, which need a free buffer of logits.
@@ -312,7 +310,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     }
     uint32_t it = 0, ci = 0;  // tiles copied, columns written
     bool go = true;
-    for (int64_t item = item0; go && item < total; item += item_step) {
+    for (int item = item0; go && item < total; item += item_step) {
       const WeighItem w = item_of(P, item, rank);
       if (w.own <= 0) continue;
       const float* lse = P.row_lse + ((int64_t)w.begin + w.i0 + (int64_t)rank * P.tpt) * P.heads + w.h * P.group;
@@ -365,7 +363,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     const uint32_t idesc = idesc_bf16(128, kCols);
     uint32_t it = 0, nth = 0;
     bool go = true;
-    for (int64_t item = item0; go && item < total; item += item_step) {
+    for (int item = item0; go && item < total; item += item_step) {
       const WeighItem w = item_of(P, item, rank);
       if (w.own <= 0) continue;
       go = wait(&C.keys, nth & 1, ctl, P.status);
@@ -400,7 +398,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     const int group = warp >> 2, mine = tid & 127;  // buffer, slot of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_mine = tmem + lanes + group * kCols;
-    for (int64_t item = item0; go && item < total; item += item_step) {
+    for (int item = item0; go && item < total; item += item_step) {
       const WeighItem w = item_of(P, item, rank);
       if (w.tiles == 0) continue;
       // this thread's key, one half of it, into its lane of TMEM
@@ -537,7 +535,7 @@ cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s) {
   const cudaError_t e = allow_shared(weigh_kernel, kWeighSmem, configured);
   if (e != cudaSuccess) return e;
   WeighParams q = p;
-  q.items = items;
+  q.items = (int)items;
   // Shares are halved while that keeps all CTAs in three or so rounds of 2 x 152 and leaves
   // eight tiles of queries to each, for prompts of the average length
   const int64_t tiles = p.total / p.batch / p.tpt;

@@ -131,7 +131,7 @@ struct WeighParams {
   int batch, heads, kv_heads, group, total;
   int tpt;                 // tokens per tile of query rows
   int splits;              // CTAs that share a tile of slots (set by the launch)
-  int64_t items;           // as given to the launch
+  int items;               // as given to the launch, fewer than 2^31 - 4096
 };
 // items: (sequence, KV head, tile of 128 slots) triples there can be
 cudaError_t launch_weigh(const WeighParams& p, int64_t items, cudaStream_t s);

@@ -239,12 +239,13 @@ bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const
   p.kv_heads = c.kv_heads;
   p.total = total;
   p.tpt = bkv::kWeighRows / p.group;
+  // tiles of 128 slots there can be; the kernel counts them in 32 bits
+  const int64_t items = (int64_t)c.batch * c.kv_heads * ((p.pg.cap + 127) / 128);
+  if (items > 0x7FFFFFFF - 4096) return BKV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (total > 0 && !bkv::encode_weigh_map(p, q, q_stride)) return BKV_ERR_CUDA;
   if (zero_status(status, s) != BKV_OK) return BKV_ERR_CUDA;
   if (total == 0) return BKV_OK;
-  // tiles of 128 slots there can be
-  const int64_t items = (int64_t)c.batch * c.kv_heads * ((p.pg.cap + 127) / 128);
   return bkv::launch_weigh(p, items, s) == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 
