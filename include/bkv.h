@@ -477,7 +477,10 @@ bkv_status bkv_attend_paged_bytes(const bkv_config* cfg, const bkv_pages* pages,
  * Slots behind lens[b] may hold anything. The keys of one (sequence, KV head)
  * are split over warps by the lengths of the whole batch: a row's last bits may
  * depend on the other sequences' lengths, but not on their contents, and equal
- * calls give equal bits. */
+ * calls give equal bits. BKV_ERR_UNSUPPORTED if the tables could hold 2^31 tiles
+ * of 16 slots over all sequences and KV heads (and, with more than 16 query heads
+ * each, for every 16 of them). With weights, tables that name more tiles than the
+ * pool has are refused on the device (BKV_ERR_INVALID_ARG, no weight changes). */
 bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const void* q, int64_t q_stride, const void* K,
                             const void* V, const int32_t* lens, void* out, float* lse, float* weights, float decay,
                             void* workspace, size_t workspace_bytes, uint32_t* status, void* cuda_stream);
@@ -493,8 +496,9 @@ bkv_status bkv_attend_paged(const bkv_config* cfg, const bkv_pages* pages, const
  *   lse:     device fp32 [total][heads], as it left it (a row of -inf gives nothing).
  *   weights, decay: as bkv_attend_paged; sequences without tokens and slots
  *            behind the last token stay.
- * BKV_ERR_UNSUPPORTED if heads / kv_heads > 96. A weight that is not finite is
- * latched as BKV_ERR_NONFINITE. */
+ * BKV_ERR_UNSUPPORTED if heads / kv_heads > 96, or if the tables could hold 2^31
+ * tiles of 128 slots over all sequences and KV heads. A weight that is not finite
+ * is latched as BKV_ERR_NONFINITE. */
 bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const void* q, int64_t q_stride, const float* lse,
                             const void* K, const int32_t* cu_seqlens, const int32_t* first_slot, int32_t total,
                             float* weights, float decay, uint32_t* status, void* cuda_stream);

@@ -11,7 +11,9 @@
 //
 // A thread takes two 16-byte pieces of a row, the ones its eight pairs lie in: pieces
 // p and p + r/16 of a half layout, 2p and 2p + 1 of an interleaved one; in both its
-// pairs are 8p .. 8p + 7. Bound: HBM, every row read and written once.
+// pairs are 8p .. 8p + 7. Bound: HBM, every row read and written once (27,380 tokens of 56
+// rows, interleaved, half of the head: 117 us, 6.7 TB/s, 0.99 of a copy; 192 decode tokens 6.7 us,
+// the chain of offsets, slot, page and row).
 #include "paged/paged.cuh"
 
 namespace bkv {
