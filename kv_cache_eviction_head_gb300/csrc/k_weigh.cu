@@ -52,12 +52,15 @@ struct WeighControl {
   uint64_t full[kQStages], empty[kQStages];
   uint64_t keys, keys_free;       // the keys are in TMEM; its products are done
   uint64_t sfull[2], sempty[2];   // a tile's logits are in TMEM and its columns written; the logits have been read
-  uint64_t others;                // the odd tiles are added up
+  uint64_t others[2];             // the odd tiles are added up; items in turn
   Ctl ctl;
   // -lse log2(e) of a tile's columns. Tile i's place is written when buffer i % 2 is free for
   // it, so after tile i - 2 has been read, and by the same warps tile i - 4 added up
   alignas(16) float col[kColStages][kCols];
-  float other[128];               // the odd tiles' sums
+  // per item (in turn): the odd tiles' sums. A group without a tile of an item is done with it
+  // before the other group may have read those of the item in front, but no earlier than that
+  // one's keys are all there, and so those of the item before it read
+  float other[2][128];
   // per item (in turn) and warp: a key holds an infinity or NaN, which would make NaN of the
   // products with rows that no token fills
   int odd[2][kAdders];
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     mbar_init(&C.keys, kAdders);
     mbar_init(&C.keys_free, 1);
     mbar_init(&C.ranks, max((P.splits - 1) * kAdders / 2, 1));
-    mbar_init(&C.others, kAdders / 2);
+    for (int i = 0; i < 2; ++i) mbar_init(&C.others[i], kAdders / 2);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -495,13 +498,13 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         unpair(sum[1], a2, a3);
         s = (a0 + a1) + (a2 + a3);
         if (group == 1) {
-          C.other[mine] = s;  // read before the next item's keys are, which that item's products wait for
+          C.other[(nth - 1) & 1][mine] = s;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&C.others);
+          if (lane == 0) mbar_arrive(&C.others[(nth - 1) & 1]);
         } else {
-          go = wait(&C.others, (nth - 1) & 1, ctl, P.status);
+          go = wait(&C.others[(nth - 1) & 1], (nth - 1) / 2 & 1, ctl, P.status);
           if (!go) break;
-          s += C.other[mine];
+          s += C.other[(nth - 1) & 1][mine];
         }
       }
       if (group == 1) continue;

@@ -191,6 +191,15 @@ def test_weigh_more_tiles_than_blocks(bkv):
     assert weigh_case(bkv, 4, 4, lens, [0] * 320, None, 9) <= 0
 
 
+@pytest.mark.parametrize("heads,kv", [(8, 8), (16, 4)])
+def test_weigh_chunks_of_one_tile(bkv, heads, kv):
+    """Blocks take several tiles of slots, most of them seen by one tile of queries: half of the
+    adding warps have none of it and come to the next item ahead of the others."""
+    lens = [(1, 24, 97, 0, 23, 130, 5, 2)[b % 8] for b in range(310)]
+    first = [(600, 130, 0, 50, 255, 300, 511, 17)[b % 7] for b in range(310)]
+    assert weigh_case(bkv, heads, kv, lens, first, 16, 41, decay=0.5) <= 0
+
+
 # ---------------------------------------------------------------- eviction by weight
 
 def evict_case(bkv, heads, kv, lens, page, seed, *, budget, prefix=0, recent=0, layers=2, order_free=False, values=None):
