@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   depend_wait();
-  depend_go();
   // tiles of slots of the longest sequence: the order of items is tile by tile. A block or
   // cluster that has one item only needs no answer but that its item is there.
   const bool one = item_step >= P.items;
@@ -304,6 +303,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
+  depend_go();  // with the TMEM allocated: a later kernel's block on this SM must not get there first
   if (P.splits > 1) cluster_sync();  // the ranks' barriers are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;

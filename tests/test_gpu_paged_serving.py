@@ -241,6 +241,34 @@ print("FIRST_OK")
 """
 
 
+def test_prompt_layers_back_to_back(bkv):
+    """Attention and weights of one layer after the other, nothing between them: each launch starts
+    while the one before it drains, and both take TMEM. The results are those of calls that were
+    waited for one by one."""
+    heads, kv, lens = 8, 2, [700, 129]
+    pool = Pool(2, kv, lens, None, 6)
+    cfg, total, n = pool.config(bkv, heads), sum(lens), 12
+    cu, zero = i32([0, lens[0], total]), i32([0, 0])
+    K, V = ([pool.fresh(lens, 10 * l + s) for l in range(n)] for s in (1, 2))
+    q = [randn((total, heads, D), 900 + l) for l in range(n)]
+    out, lse = torch.empty_like(q[0]), [torch.empty((total, heads), device="cuda") for _ in range(n)]
+
+    def run(wait):
+        W = [torch.zeros(pool.shape(), device="cuda") for _ in range(n)]
+        for l in range(n):
+            bkv.bkv_attend_prompt(cfg, q[l], K[l], V[l], cu, zero, out, lse=lse[l], stream=stream())
+            if wait:
+                torch.cuda.synchronize()
+            bkv.bkv_weigh_prompt(cfg, q[l], lse[l], K[l], cu, zero, W[l], decay=0.0, stream=stream())
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(W)
+
+    want = run(True)
+    for _ in range(10):
+        assert torch.equal(run(False), want)
+
+
 def test_first_calls_of_a_process_are_captured(bkv):
     r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "FIRST_OK" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
