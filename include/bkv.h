@@ -520,7 +520,8 @@ bkv_status bkv_weigh_prompt(const bkv_config* cfg, const bkv_pages* pages, const
  *            after the call.
  * With BKV_FLAG_ORDER_FREE a sequence with budget < length < budget + recent is
  * refused on the device (BKV_ERR_INVALID_ARG in status, kept -1, nothing moves),
- * and a budget above 2^19 on the host (BKV_ERR_UNSUPPORTED). */
+ * and a budget above 2^19 on the host (BKV_ERR_UNSUPPORTED); without it a budget
+ * above 2^31 - 4097. */
 bkv_status bkv_evict_weight(const bkv_config* cfg, const bkv_pages* pages, void* const* K, void* const* V,
                             float* const* weights, const int32_t* cache_lens, int32_t* kept, int32_t* new_lens,
                             uint32_t* status, void* cuda_stream);

@@ -267,7 +267,8 @@ bkv_status bkv_evict_weight(const bkv_config* cfg, const bkv_pages* pages, void*
       return BKV_ERR_INVALID_ARG;
   p.order_free = (c.flags & BKV_FLAG_ORDER_FREE) != 0;
   const int64_t units = (int64_t)c.layers * c.batch * c.kv_heads;
-  if (units > 0x7FFFFFFF || (p.order_free && c.budget > (1 << 19))) return BKV_ERR_UNSUPPORTED;
+  // the kernel counts slots of the keep set in 32 bits, a block's width at a time
+  if (units > 0x7FFFFFFF || c.budget > 0x7FFFFFFF - 4096 || (p.order_free && c.budget > (1 << 19))) return BKV_ERR_UNSUPPORTED;
   for (int l = 0; l < c.layers; ++l) {
     p.K[l] = static_cast<uint4*>(K[l]);
     p.V[l] = static_cast<uint4*>(V[l]);

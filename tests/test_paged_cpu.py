@@ -112,6 +112,8 @@ def test_unsupported(bkv):
     assert call(bkv, "bkv_weigh_prompt", cfg_for(bkv, heads=97, kv_heads=1), {**GOOD["bkv_weigh_prompt"], "qs": 97 * 128}.values()) == 7
     big = cfg_for(bkv, budget=(1 << 19) + 1, max_cache=1 << 20, flags=2)
     assert call(bkv, "bkv_evict_weight", big, GOOD["bkv_evict_weight"].values()) == 7
+    far = cfg_for(bkv, budget=2 ** 31 - 4096, max_cache=2 ** 31 - 1)
+    assert call(bkv, "bkv_evict_weight", far, GOOD["bkv_evict_weight"].values(), pages=bkv.BkvPages(10, 16, 4, A)) == 7
 
 
 def test_ropes(bkv):
