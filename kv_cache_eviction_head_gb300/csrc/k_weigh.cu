@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         float old = 0.f;
         if (slot < w.first && P.decay != 0.f) old = P.decay * P.weights[row];
         P.weights[row] = old + s;
-        if (!(fabsf(s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
+        if (!(fabsf(old + s) < __builtin_huge_valf())) latch(P.status, BKV_ERR_NONFINITE);
       }
     }
   }

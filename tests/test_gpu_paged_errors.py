@@ -214,6 +214,22 @@ def test_weigh_pages_out_of_range_and_odd_rows(bkv):
     assert bool(torch.isnan(got[:41]).all()) and bool(torch.isfinite(got[41:]).all())
 
 
+@pytest.mark.parametrize("odd", [math.nan, math.inf])
+def test_weigh_onto_odd_weights(bkv, odd):
+    """An old weight that is not finite stays so and is latched, unless decay is 0 or the slot is new."""
+    pool = Pool(1, 1, [48], 16, 8)
+    K = pool.fresh([48], 5)
+    cfg = pool.config(bkv, 4)
+    q, lse = randn((8, 4, D), 8), torch.full((8, 4), 4.0, device="cuda")
+    for slot, decay, bad in [(39, 1.0, True), (39, 0.0, False), (40, 1.0, False)]:
+        W, status = torch.zeros(pool.shape(), device="cuda"), new_status()
+        page, place = pool.at(0, slot + 1, slot)
+        W[page, :, place] = odd
+        bkv.bkv_weigh_prompt(cfg, q, lse, K, i32([0, 8]), i32([40]), W, table=pool.table, decay=decay, status=status, stream=stream())
+        assert int(status) == (NONFINITE if bad else 0)
+        assert int((~torch.isfinite(pool.get(W, 0, 48))).sum()) == (1 if bad else 0)
+
+
 @pytest.mark.parametrize("heads,group_fills", [(4, True), (5, False)])
 def test_weigh_infinite_key(bkv, heads, group_fills):
     """A key of infinities: its logits are infinite, the other slots' as ever, whether the query
