@@ -16,8 +16,10 @@
 //
 // Bound: HBM; moved rows are read and written once, weights read once. In one launch a
 // block's selection, which is latency, lies under the copies of others: 6,144 units of up to
-// 2,048 slots cut to 1,792 take 1,700 us for 11.4 GB, 0.99 of a copy's rate (as two launches
-// 1,640 + 164). Order-free, 16 rows of 4,096 units, 62 us: the selection's instructions.
+// 2,048 slots cut to 1,792 take 1,679 us for 11.4 GB, a copy's rate (as two launches
+// 1,640 + 164). Order-free, 16 rows of 4,096 units, 48 us: the selection's instructions (62 with
+// a look-up of the row for every key, the first histogram in a pass of its own, and prefix and
+// recent slots told by their numbers and not by their keys).
 #include "paged/paged.cuh"
 
 namespace bkv {
@@ -26,6 +28,8 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kBins = 2048;                                 // eleven bits of a key
 constexpr int kMostCached = 8192;                           // slots whose keys stay in shared memory
+constexpr uint32_t kAlways = ~0u;                           // in place of a key: the slot is kept in any case. No weight
+                                                            // has this key, nor one that shares its top eleven bits
 constexpr int kMoveLoads = 4;                               // 16-byte pieces per thread and step
 
 struct Unit {
@@ -81,6 +85,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
   extern __shared__ uint32_t dynamic[];
   __shared__ __align__(16) Shared<kThreads> S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; ++i) reinterpret_cast<int4*>(S.hist)[tid + i * kThreads] = make_int4(0, 0, 0, 0);
+  };
+  clear();
+  if (tid == 0) S.found = 0;
+  __syncthreads();
   depend_wait();
   depend_go();
   const Unit u = unit_of(P);
@@ -104,29 +115,59 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
     }
     return BKV_IN_RANGE(row < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status) ? key_of(W[row]) : 0u;
   };
-  uint32_t* cache = dynamic;
-#pragma unroll 8
-  for (int s = tid; s < min(to, P.cached); s += kThreads) cache[s] = s >= from ? read_key(s) : 0u;
-  auto key = [&](int slot) { return slot < P.cached ? cache[slot] : read_key(slot); };
-
-  // The smallest kept key, as far as its bits are known, and how many of those equal in these
-  // bits are kept (the lowest slots): `need`.
   int need = P.budget - P.prefix - P.recent;  // of the candidates, fewer than there are
   const bool any = need > 0;
-  uint32_t least = 0, known = 0;
+
+  // The keys of the first slots, four a thread (in one page), and the histogram of the first bits.
+  uint32_t* cache = dynamic;
+  const int cached = min(u.len, P.cached);
+  const bool quads = P.pg.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
+  auto count_key = [&](uint32_t k, int shift, uint32_t digit) { atomicAdd(&S.hist[kBins - 1 - (k >> shift & digit)], 1); };
+#pragma unroll 2
+  for (int s = 4 * tid; s < cached; s += 4 * kThreads) {
+    const int64_t row = pool_row(P.pg, P.kv_heads, u.b, u.h, s);
+    float4 w = make_float4(__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""));
+    if (row < 0) {
+      latch(P.status, BKV_ERR_INVALID_ARG);
+    } else if (BKV_IN_RANGE(row + min(3, u.len - 1 - s) < (int64_t)P.pg.pages * P.kv_heads * P.pg.page_size, P.status)) {
+      if (quads) {
+        w = *reinterpret_cast<const float4*>(W + row);
+      } else {
+        w.x = W[row];
+        if (s + 1 < u.len) w.y = W[row + 1];
+        if (s + 2 < u.len) w.z = W[row + 2];
+        if (s + 3 < u.len) w.w = W[row + 3];
+      }
+    }
+    uint32_t k[4] = {key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (s + e < from || s + e >= to) k[e] = kAlways;
+      else if (any) count_key(k[e], 21, 2047u);
+    }
+    *reinterpret_cast<uint4*>(cache + s) = make_uint4(k[0], k[1], k[2], k[3]);
+  }
+  auto key = [&](int slot) { return slot < cached ? cache[slot] : slot < from || slot >= to ? kAlways : read_key(slot); };
+  const int behind = max(cached, from);  // candidates from here on have no key on chip
+  if (any)
+    for (int s = behind + tid; s < to; s += kThreads) count_key(read_key(s), 21, 2047u);
+
+  // The smallest kept key, as far as its bits are known, and how many of those equal in these
+  // bits are kept (the lowest slots): `need`. Without a candidate to keep, a key above all weights'.
+  uint32_t least = any ? 0u : kAlways - 1, known = any ? 0u : ~0u;
+  __syncthreads();
   for (int shift = 21; any && shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
     const uint32_t digit = shift == 0 ? 1023u : 2047u;
-    int4* clear = reinterpret_cast<int4*>(S.hist);
-#pragma unroll
-    for (int i = 0; i < kPerThread / 4; ++i) clear[tid + i * kThreads] = make_int4(0, 0, 0, 0);
-    if (tid == 0) S.found = 0;
-    __syncthreads();
-    for (int s = tid; s < to; s += kThreads) {
-      if (s < from) continue;
-      const uint32_t k = key(s);
-      if ((k & known) == least) atomicAdd(&S.hist[kBins - 1 - (k >> shift & digit)], 1);
+    if (shift < 21) {
+      clear();
+      __syncthreads();
+      auto count = [&](uint32_t k) {
+        if ((k & known) == least) count_key(k, shift, digit);
+      };
+      for (int s = tid; s < cached; s += kThreads) count(cache[s]);
+      for (int s = behind + tid; s < to; s += kThreads) count(read_key(s));
+      __syncthreads();
     }
-    __syncthreads();
     // the bin, from the top, in which the need-th largest lies: neighbouring bins a thread
     int mine[kPerThread], sum = 0;
 #pragma unroll
@@ -167,14 +208,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
     if (in_bin <= kFew) {
       // few: each counts those above it
       __syncthreads();
-      for (int s = tid; s < to; s += kThreads) {
-        if (s < from) continue;
-        const uint32_t k = key(s);
+      auto list = [&](uint32_t k) {
         if ((k & known) == least) {
           const int at = atomicAdd(&S.found, 1);
           if (at < kFew) S.few[at] = k;
         }
-      }
+      };
+      for (int s = tid; s < cached; s += kThreads) list(cache[s]);
+      for (int s = behind + tid; s < to; s += kThreads) list(read_key(s));
       __syncthreads();
       if (tid < in_bin) {
         const uint32_t k = S.few[tid];
@@ -207,25 +248,26 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
   uint32_t greater = 0, equal = 0;  // word `lane` of the 32 looked at: slots kept in any case, slots equal to the least
   auto look = [&](int s0) {
     greater = equal = 0;
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-      const int s = s0 + i * 32 + lane;
-      if (s0 + i * 32 >= end) break;
-      bool gt = false, eq = false;
-      if (s < end) {
-        if (s < from || s >= to) {
-          gt = true;
-        } else if (any) {
-          const uint32_t k = key(s) & known;
-          gt = k > least;
-          eq = k == least;
-        }
-      }
-      const unsigned bg = __ballot_sync(kAll, gt), be = __ballot_sync(kAll, eq);
+    const int n = min((end - s0 + 31) / 32, 32);
+    auto word = [&](int i, uint32_t k) {
+      const unsigned bg = __ballot_sync(kAll, (k & known) > least), be = __ballot_sync(kAll, (k & known) == least);
       if (lane == i) {
         greater = bg;
         equal = be;
       }
+    };
+    if (end <= cached) {
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) word(i, cache[s0 + i * 32 + lane]);
+    } else {
+      for (int i = 0; i < n; ++i) word(i, key(s0 + i * 32 + lane));
+    }
+    // slots behind the last one
+    const int in = end - s0 - lane * 32;
+    if (in < 32) {
+      const uint32_t mask = in > 0 ? (1u << in) - 1 : 0u;
+      greater &= mask;
+      equal &= mask;
     }
   };
   __syncthreads();  // the keys are all there; S.warp_sum is free
@@ -248,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
   }
   const unsigned lower = (1u << lane) - 1;
   const int words = (P.budget + 31) / 32;
-  uint32_t* bits = dynamic + P.cached;
+  uint32_t* bits = dynamic + (P.cached + 31) / 32 * 32;
   int* in_front = reinterpret_cast<int*>(bits + words);
   uint32_t keep = 0;  // of word `lane`: its kept slots, and those in front of it
   int at = 0;
@@ -314,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_weight_kernel
       e0 = e_begin;
       for (int s0 = begin; s0 < end; s0 += 1024) {
         keep_words(s0);
-        for (int i = 0; i < 32 && s0 + i * 32 < end; ++i) {
+        for (int i = max(P.budget - s0, 0) / 32; i < 32 && s0 + i * 32 < end; ++i) {
           const uint32_t k = __shfl_sync(kAll, keep, i);
           const int t = __shfl_sync(kAll, at, i) + __popc(k & lower) - below, source = s0 + i * 32 + lane;
           if (source < P.budget || !(k >> lane & 1)) continue;
@@ -408,7 +450,7 @@ cudaError_t launch(const EvictWeightParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)p.layers * p.batch * p.kv_heads));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)p.cached * 4 + (p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0);
+  cfg.dynamicSmemBytes = (size_t)((p.cached + 31) / 32 * 32) * 4 + (p.order_free ? (size_t)((p.budget + 31) / 32) * 8 : 0);
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
@@ -421,9 +463,9 @@ cudaError_t launch_evict_weight(const EvictWeightParams& given, cudaStream_t s) 
   EvictWeightParams p = given;
   p.cached = p.pg.cap < kMostCached ? p.pg.cap : kMostCached;
   // Few units: 512 threads each (288 units of 2,064 slots: 27 us, with 256 threads 31, with 128
-  // 44). Many: 256 (6,144 units of 2,048 slots: 1,699 us, with 512 1,692, with 128 1,758), or
+  // 44). Many: 256 (6,144 units of 2,048 slots: 1,680 us, with 512 1,673, with 128 1,719), or
   // order-free, where a unit is a chain of latencies and little else, 128 and so twice the
-  // units at once (4,096 units of 1,040 slots: 81 us, with 256 93, with 512 138).
+  // units at once (4,096 units of 1,040 slots: 48 us, with 256 70, with 512 109).
   const int64_t units = (int64_t)p.layers * p.batch * p.kv_heads;
   return units <= 2 * kSms ? launch<512>(p, s) : p.order_free ? launch<128>(p, s) : launch<256>(p, s);
 }

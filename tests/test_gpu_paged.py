@@ -202,7 +202,7 @@ def test_weigh_chunks_of_one_tile(bkv, heads, kv):
 
 # ---------------------------------------------------------------- eviction by weight
 
-def evict_case(bkv, heads, kv, lens, page, seed, *, budget, prefix=0, recent=0, layers=2, order_free=False, values=None):
+def evict_case(bkv, heads, kv, lens, page, seed, *, budget, prefix=0, recent=0, layers=2, order_free=False, values=None, shift=0):
     flags = bkv.BKV_FLAG_ORDER_FREE if order_free else 0
     pool = Pool(len(lens), kv, lens, page, seed)
     cap = pool.size if pool.table is None else pool.size * pool.table.shape[1]
@@ -217,6 +217,9 @@ def evict_case(bkv, heads, kv, lens, page, seed, *, budget, prefix=0, recent=0, 
     if values is not None:  # few different weights: ties, infinities, NaN
         pick = torch.tensor(values, device="cuda")
         W = [pick[torch.randint(0, len(values), pool.shape(), device="cuda", generator=g)] for _ in range(layers)]
+    if shift:  # weights that begin `shift` elements behind a 16-byte boundary
+        W = [torch.cat([x.new_zeros(shift), x.flatten()])[shift:].view(x.shape) for x in W]
+        assert all(x.data_ptr() % 16 for x in W)
     K0, V0, W0 = ([x.clone() for x in y] for y in (K, V, W))
     kept = torch.full((layers, len(lens), kv, budget), 9999999, dtype=torch.int32, device="cuda")
     left, status = i32([5] * len(lens)), new_status()
@@ -260,6 +263,27 @@ def test_evict_budgets(bkv, budget, prefix, recent, over, page, order_free):
                                     [1.0, 1.0000001, 1.0000002]])
 def test_evict_ties_and_odd_weights(bkv, values, order_free):
     evict_case(bkv, 4, 1, [200, 90, 130], 16, 12, budget=70, prefix=4, recent=7, order_free=order_free, values=values)
+
+
+@pytest.mark.parametrize("order_free", [False, True])
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_evict_weights_off_the_boundary(bkv, shift, order_free):
+    evict_case(bkv, 4, 2, [200, 131, 70, 94], 16, 18, budget=70, prefix=3, recent=7, order_free=order_free, shift=shift)
+
+
+@pytest.mark.parametrize("over", [8, 9, 10, 11])
+def test_evict_dense_caches_of_any_size(bkv, over):
+    evict_case(bkv, 4, 2, [120 + over, 120, 119 + over], None, 19, budget=100, prefix=3, recent=7)
+
+
+@pytest.mark.parametrize("order_free", [False, True])
+@pytest.mark.parametrize("length,budget,prefix,recent", [(9001, 8400, 8300, 30), (8210, 8100, 4, 40), (9001, 8230, 4, 820), (8192, 8000, 0, 0),
+                                                         (8193, 100, 50, 50)])
+def test_evict_around_the_keys_on_chip(bkv, length, budget, prefix, recent, order_free):
+    """Candidates, prefix and recent slots on either side of the 8,192nd."""
+    if order_free and length - 1 - budget < recent:
+        pytest.skip("an order-free eviction refuses sequences this short")
+    evict_case(bkv, 2, 2, [length, length - 1], 16, 21, budget=budget, prefix=prefix, recent=recent, layers=1, order_free=order_free)
 
 
 def test_evict_many_layers_and_sequences(bkv):
