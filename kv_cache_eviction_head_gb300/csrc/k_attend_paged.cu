@@ -47,7 +47,7 @@ constexpr int kBox = kTileSlots * 128;       // 16 slots x 64 elements
 constexpr int kTileBox = 4 * kBox;           // K and V of a tile: 8 KB
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 3;                // per SM
-constexpr int kAhead = 4;                   // heads whose logits are asked for ahead
+constexpr int kAhead = 2;                   // heads whose logits are asked for ahead
 constexpr int kJoinTiles = 16;              // tiles of a block's weights, at least
 constexpr int kJoinHeads = 512;             // heads whose sums a block holds at a time
 constexpr float kMinusInf = -__builtin_huge_valf();
@@ -466,16 +466,16 @@ __device__ __forceinline__ Pieces pieces_of(int before, int u, int n, int units,
   const int from = before * units + u * n;
   return Pieces{from / share, (from + n - 1) / share};
 }
-// A head's largest reference over the unit's pieces and the sum relative to it. One warp,
-// all lanes get it.
+// A head's largest reference over the unit's pieces and the sum relative to it. Eight lanes,
+// all get it; the warp's four eights each have their own pieces (or none).
 __device__ __forceinline__ float2 join_sum(const AttendPagedParams& P, const Pieces& pc, int in_chunk, int lane) {
   // four pieces a lane at once, more in rounds: a running maximum and sum
   float m = kMinusInf, l = 0.f;
-  for (int c0 = pc.c0; c0 <= pc.c1; c0 += 128) {
+  for (int c0 = pc.c0; c0 <= pc.c1; c0 += 32) {
     float2 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * 32 + lane;
+      const int c = c0 + k * 8 + (lane & 7);
       x[k] = c <= pc.c1 ? P.part_ml[pc.at(c) * 16 + in_chunk] : make_float2(kMinusInf, 0.f);
     }
     float top = m;
@@ -489,10 +489,10 @@ __device__ __forceinline__ float2 join_sum(const AttendPagedParams& P, const Pie
   }
   float top = m;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+  for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
   if (m != kMinusInf) l *= exp2_approx(m - top);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kAll, l, off);
+  for (int off = 4; off > 0; off >>= 1) l += __shfl_xor_sync(kAll, l, off);
   return make_float2(top, l);
 }
 
@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   const int units = P.kv_heads * P.chunks;
   depend_wait();
   depend_go();
+  const int x0 = tid < P.batch ? P.seq[tid].x : 0;
   const int tiles = P.seq[P.batch].x;
   const int share = share_of(tiles * units, P.shares);
 
@@ -607,12 +608,11 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
   int t = (int)begin;
   const int end = (int)min(begin + each, all);
   // the sequence of tile t: the last with at most t tiles in front of it that has any itself
-  int b = 0;
-  for (int b0 = 0; b0 < P.batch; b0 += 32) {
-    const bool in_front = b0 + lane < P.batch && P.seq[b0 + lane].x * P.kv_heads <= t;
-    const int n = __popc(__ballot_sync(kAll, in_front));
-    b = n ? b0 + n - 1 : b;
-    if (n < 32) break;
+  int b = -1;
+  for (int b0 = 0; b0 < P.batch; b0 += kJoinThreads) {
+    const int n = __syncthreads_count(b0 + tid < P.batch && (b0 == 0 ? x0 : P.seq[b0 + tid].x) * P.kv_heads <= t);
+    b += n;
+    if (n < kJoinThreads) break;
   }
   const int most_heads = kJoinHeads / P.group;  // KV heads whose sums fit
   while (true) {
@@ -653,17 +653,16 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_paged_kernel(con
     };
     Slots now, next;
     fetch(tid, now);
-    for (int k = warp; k < heads; k += kWarps) {
+    for (int k0 = warp * 4; k0 < heads; k0 += kWarps * 4) {
+      const int k = min(k0 + (lane >> 3), heads - 1);
       const int h = h0 + k / P.group, g = k % P.group;
-      const Pieces pc = pieces_of(before, h * P.chunks + g / P.chunk, n, units, share);
-      float x;
-      if (pc.c0 == pc.c1) {
-        x = P.lse2[(int64_t)b * P.heads + h0 * P.group + k];
-      } else {
-        const float2 ml = join_sum(P, pc, g % P.chunk, lane);
-        x = ml.x + log2f(ml.y);
-      }
-      if (lane == 0) lse2[k] = x;
+      Pieces pc = pieces_of(before, h * P.chunks + g / P.chunk, n, units, share);
+      const bool whole = pc.c0 == pc.c1;
+      if (whole) --pc.c1;  // no pieces
+      float x = whole ? P.lse2[(int64_t)b * P.heads + h0 * P.group + k] : 0.f;
+      const float2 ml = join_sum(P, pc, g % P.chunk, lane);
+      if (!whole) x = ml.x + log2f(ml.y);
+      if ((lane & 7) == 0) lse2[k] = x;  // lanes behind the last head write that one's again
     }
     __syncthreads();
     for (int q = tid; q < cnt * 4; q += kJoinThreads) {
